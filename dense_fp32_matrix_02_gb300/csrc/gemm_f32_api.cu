@@ -355,6 +355,18 @@ namespace gemm_f32_impl {
 
 int record_cuda_error(cudaError_t e) { return fail_cuda(e); }
 
+cudaError_t device_facts(int* sm_count, int* cc_major, WaitCfg* wc) {
+  const DeviceInfo* d = nullptr;
+  cudaError_t e = device_info(&d);
+  if (e != cudaSuccess) return e;
+  *sm_count = d->sm_count;
+  *cc_major = d->cc_major;
+  wc->limit = g_wait_ns.load();
+  wc->debug = g_debug_flags.load();
+  wc->status = d->status;
+  return cudaSuccess;
+}
+
 long long auto_plan_scratch_bytes(int64_t M, int64_t N, int64_t K,
                                   const float* A, int64_t lda, const float* B,
                                   int64_t ldb, const float* C, int64_t ldc) {

@@ -151,6 +151,10 @@ cudaError_t launch_tma_ffma(const Problem& p, bool c_vec, const WaitCfg& wc,
 // GEMM_F32_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
 
+// The current device's SM count and compute capability major, and the
+// bounded-wait configuration for a launch on it.
+cudaError_t device_facts(int* sm_count, int* cc_major, WaitCfg* wc);
+
 // gemm_f32_ws's path: automatic plan with the given scratch.
 int run_auto_with_scratch(int64_t M, int64_t N, int64_t K, const float* A,
                           int64_t lda, const float* B, int64_t ldb, float* C,

@@ -118,6 +118,22 @@ def lib() -> ctypes.CDLL:
                                               ctypes.POINTER(i64)]
         L.gemm_f32_host_chunks.restype = ci
         L.gemm_f32_host_chunks.argtypes = [i64, i64, ci, ctypes.POINTER(i64)]
+        cf = ctypes.c_float
+        head = [ci, i64, i64, i64, vp, i64, vp, i64]
+        teacher = [i64, vp, i64, vp, i64, cf]
+        back = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.gemm_f32_vocab_ce.restype = ci
+        L.gemm_f32_vocab_ce.argtypes = head + [vp, vp, vp, vp, i64, vp]
+        L.gemm_f32_vocab_ce_grad.restype = ci
+        L.gemm_f32_vocab_ce_grad.argtypes = head + [vp] + back
+        L.gemm_f32_vocab_distill.restype = ci
+        L.gemm_f32_vocab_distill.argtypes = head + teacher + [vp, vp, vp, i64,
+                                                              vp]
+        L.gemm_f32_vocab_distill_grad.restype = ci
+        L.gemm_f32_vocab_distill_grad.argtypes = head + teacher + back
+        L.gemm_f32_vocab_workspace_size.restype = i64
+        L.gemm_f32_vocab_workspace_size.argtypes = [i64, i64, i64, i64, ci,
+                                                    ci]
         _lib = L
         return L
 

@@ -424,6 +424,94 @@ GEMM_F32_API int gemm_f32_mixed_plan_sms(int64_t M, int64_t N, int64_t K,
 GEMM_F32_API int gemm_f32_host_chunks(int64_t M, int64_t N, int sm_count,
                                       int64_t bounds[17]);
 
+/*
+ * Vocabulary losses: the last product of a language model with its loss.
+ *
+ * X (T×D, ldx) holds hidden states, one row per token; W (V×D, ldw) one row
+ * per entry of the vocabulary; both 16-bit of `type` (gemm_f32_mixed_type),
+ * row-major in device memory, on any element boundary.  The logits are
+ *   z[t][v] = Σ_k X[t][k]·W[v][k],
+ * summed in fp32 and never stored whole: they are made tile by tile, and for
+ * the gradients once more in pieces of the vocabulary.
+ *
+ * gemm_f32_vocab_ce: softmax cross entropy against targets[t]:
+ *   lse_t  = log Σ_v exp(z[t][v]),   loss_t = lse_t − z[t][targets[t]].
+ * gemm_f32_vocab_distill: distillation from a teacher's `top` best logits
+ * u[t][j] = top_logits[t·ldt + j] at the ids top_ids[t·ldi + j], at the
+ * temperature τ:
+ *   q_tj   = exp(u[t][j]/τ) / Σ_i exp(u[t][i]/τ),
+ *   lse_t  = log Σ_v exp(z[t][v]/τ),
+ *   loss_t = τ²·Σ_j q_tj·(log q_tj − (z[t][id_tj]/τ − lse_t)),
+ * the divergence of the student's softmax from the teacher's, taken over the
+ * teacher's entries.  1 <= top <= 256; an id may appear more than once (its
+ * shares add up).
+ *
+ * Tokens that are not learnt from.  A target outside [0, V) marks one; so
+ * does a distillation row in which no entry counts (an entry counts unless
+ * its id is outside [0, V) or its logit is −Inf).  Their loss and lse are 0,
+ * they add nothing to dW and their row of dX is 0; their row of X is never
+ * read (it may hold NaN), and no work is done for it.
+ *
+ * The _grad forms take lse as the forward call returned it and the gradient
+ * of each token's loss, g_t = grad_loss[t·grad_stride] (grad_stride 0: one
+ * value for every token), and write
+ *   G[t][v] = g_t·(exp(z − lse_t) − [v = targets[t]])              (ce)
+ *   G[t][v] = g_t·τ·(exp(z/τ − lse_t) − Σ_j q_tj·[v = id_tj])      (distill)
+ *   dX = G·W (T×D, lddx),   dW = Gᵀ·X (V×D, lddw),
+ * both 16-bit of `type`, written whole (not added to what was there).  G is
+ * rounded to `type` once before the two products (in binary16 scaled by a
+ * power of two that brings the largest |g_t·τ| near 2^14), whose sums are
+ * fp32, and each result is rounded once.  Sums run in a fixed order: the
+ * same call gives the same bits.
+ *
+ * `workspace` is 16-byte aligned device memory of at least
+ * gemm_f32_vocab_workspace_size bytes (else GEMM_F32_ERR_INVALID_ARG), in
+ * use until the stream passes the call; nothing in it needs to start at any
+ * value and nothing is kept in it between calls.  T = 0: forward launches
+ * nothing, the gradients write dW = 0.  V, D >= 1; T, V, D < 2^31.
+ * GEMM_F32_ERR_UNSUPPORTED on a GPU without tcgen05 (not sm_10x);
+ * GEMM_F32_ERR_INVALID_ARG also for an unknown type, a temperature that is
+ * not a positive finite number, top outside [1, 256], leading dimensions
+ * below the row widths, grad_stride < 0, and NULL operands.
+ */
+GEMM_F32_API int gemm_f32_vocab_ce(int type, int64_t T, int64_t V, int64_t D,
+                                   const void *X, int64_t ldx, const void *W,
+                                   int64_t ldw, const int64_t *targets,
+                                   float *loss, float *lse, void *workspace,
+                                   int64_t workspace_bytes,
+                                   gemm_f32_stream_t stream);
+
+GEMM_F32_API int gemm_f32_vocab_ce_grad(
+    int type, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
+    const void *W, int64_t ldw, const int64_t *targets, const float *lse,
+    const float *grad_loss, int64_t grad_stride, void *dX, int64_t lddx,
+    void *dW, int64_t lddw, void *workspace, int64_t workspace_bytes,
+    gemm_f32_stream_t stream);
+
+GEMM_F32_API int gemm_f32_vocab_distill(
+    int type, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
+    const void *W, int64_t ldw, int64_t top, const float *top_logits,
+    int64_t ldt, const int64_t *top_ids, int64_t ldi, float temperature,
+    float *loss, float *lse, void *workspace, int64_t workspace_bytes,
+    gemm_f32_stream_t stream);
+
+GEMM_F32_API int gemm_f32_vocab_distill_grad(
+    int type, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
+    const void *W, int64_t ldw, int64_t top, const float *top_logits,
+    int64_t ldt, const int64_t *top_ids, int64_t ldi, float temperature,
+    const float *lse, const float *grad_loss, int64_t grad_stride, void *dX,
+    int64_t lddx, void *dW, int64_t lddw, void *workspace,
+    int64_t workspace_bytes, gemm_f32_stream_t stream);
+
+/* Workspace bytes the vocabulary losses need on the current device: the
+ * forward calls (grad = 0) or the gradients (grad = 1), with `top` entries a
+ * token (1 for cross entropy).  aligned = 1: X and W are 16-byte aligned
+ * with leading dimensions that are multiples of 8; 0: any layout (room for
+ * an aligned copy of W is included).  Minus a status on error. */
+GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
+                                                   int64_t D, int64_t top,
+                                                   int grad, int aligned);
+
 /* Static description of a status code. */
 GEMM_F32_API const char *gemm_f32_status_string(int status);
 
