@@ -16,6 +16,7 @@
 //      of that piece).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "gemm_f32.h"
 #include "kernels.h"
@@ -86,16 +87,23 @@ __global__ void __launch_bounds__(32 * kTargetWarps)
 // entropy also writes its one entry per token here.  Forward: loss and lse
 // of the other tokens are 0.  Gradients: the power of two that brings the
 // largest |g·τ| near 2^14 (binary16 G; 1 for bfloat16, whose exponents
-// need no help).
+// need no help), and the slots that dX is summed in.
+struct NumberArgs {
+  int T, V, top;
+  const int64_t* targets;  // cross entropy, else null
+  float *loss, *lse;       // forward, else null
+  const float* grad_loss;  // gradients, else null
+  long long grad_stride;
+  float tau;
+  int scaled;       // binary16
+  int always_pack;  // X has no tensor map
+  int D, piece, pairs, max_splits;
+};
+
 __global__ void __launch_bounds__(1024)
-    number_tokens_kernel(int T, int V, int top,
-                         const int64_t* __restrict__ targets,
-                         int* __restrict__ ids, float* __restrict__ log_q,
-                         float* __restrict__ loss, float* __restrict__ lse,
-                         const float* __restrict__ grad_loss,
-                         long long grad_stride, float tau, int scaled,
-                         int* __restrict__ token, int* __restrict__ row,
-                         VocabHeader* header) {
+    number_tokens_kernel(NumberArgs a, int* __restrict__ ids,
+                         float* __restrict__ log_q, int* __restrict__ token,
+                         int* __restrict__ row, VocabHeader* header) {
   __shared__ int s_count[32];
   __shared__ float s_max[32];
   griddep_wait();
@@ -103,17 +111,17 @@ __global__ void __launch_bounds__(1024)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int base = 0;
   float most = 0.f;
-  for (int t0 = 0; t0 < T; t0 += 1024) {
+  for (int t0 = 0; t0 < a.T; t0 += 1024) {
     const int t = t0 + threadIdx.x;
     bool learnt = false;
-    if (t < T) {
-      if (targets) {
-        const int64_t y = targets[t];
-        learnt = y >= 0 && y < V;
+    if (t < a.T) {
+      if (a.targets) {
+        const int64_t y = a.targets[t];
+        learnt = y >= 0 && y < a.V;
         ids[t] = learnt ? (int)y : INT_MAX;
         log_q[t] = learnt ? 0.f : -INFINITY;
       } else {
-        learnt = ids[(long long)t * top] != INT_MAX;
+        learnt = ids[(long long)t * a.top] != INT_MAX;
       }
     }
     const unsigned votes = __ballot_sync(0xffffffffu, learnt);
@@ -126,15 +134,15 @@ __global__ void __launch_bounds__(1024)
       total += c;
     }
     const int r = base + before + __popc(votes & ((1u << lane) - 1u));
-    if (t < T) {
+    if (t < a.T) {
       row[t] = learnt ? r : -1;
       if (learnt) token[r] = t;
-      if (loss && !learnt) {
-        loss[t] = 0.f;
-        lse[t] = 0.f;
+      if (a.loss && !learnt) {
+        a.loss[t] = 0.f;
+        a.lse[t] = 0.f;
       }
-      if (grad_loss && learnt)
-        most = fmaxf(most, fabsf(grad_loss[t * grad_stride]));
+      if (a.grad_loss && learnt)
+        most = fmaxf(most, fabsf(a.grad_loss[t * a.grad_stride]));
     }
     base += total;
     __syncthreads();
@@ -145,203 +153,160 @@ __global__ void __launch_bounds__(1024)
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 32; ++w) most = fmaxf(most, s_max[w]);
-    most *= tau;
+    most *= a.tau;
     int e = 0;
     // 0, Inf and NaN: no scale
-    if (scaled && most > 0.f && most < INFINITY)
+    if (a.scaled && most > 0.f && most < INFINITY)
       e = min(max(14 - ilogbf(most), -100), 100);
     header->learnt = base;
+    header->packed = a.always_pack || base != a.T;
+    header->dx_splits = vocab_dx_splits(base, a.D, a.piece, a.pairs,
+                                        a.max_splits);
     header->scale = ldexpf(1.f, e);
     header->inv_scale = ldexpf(1.f, -e);
   }
 }
 
-// ------------------------------------------------------------- products
-// C (rows × cols) = A·B, one 64 × 64 tile per block, 4 × 4 per thread.
-// Element (m, k) of A is A[rowA(m)·am + colA(k)·ak], where the map (token
-// numbers) applies to whichever index walks X's rows; likewise B.
-template <typename TA, typename TB>
-struct Operand2 {
-  const TA* A;
-  long long am, ak;
-  const int* map_m;  // A's row m is map_m[m]
-  const TB* B;
-  long long bk, bn;
-  const int* map_k;  // B's row k is map_k[k]
-};
-
-// rows or depth < 0: the header's count of learnt tokens.
-// out32 (+ add): fp32, C[m·ldc + n] (+)= sum.  out16: C = sum·inv_scale.
-template <typename TA, typename TB, typename TO>
+// ------------------------------------------------------------- copies
+// Rows of 16-bit values, `cols` wide, to 16-byte aligned rows: X's learnt
+// tokens in order, then zero rows up to a multiple of 64 (token given: the
+// count is the header's, and nothing is done unless X is read packed), or a
+// matrix whose rows have no tensor map.  vec: the source too is aligned.
 __global__ void __launch_bounds__(256)
-    simple_product_kernel(Operand2<TA, TB> o, int rows, int cols, int depth,
-                          const VocabHeader* header, TO* C, long long ldc,
-                          int add) {
-  __shared__ float sa[16][65], sb[16][65];
+    pack_rows_kernel(const uint16_t* __restrict__ src, long long lds, int cols,
+                     uint16_t* __restrict__ dst, long long ldd,
+                     const int* __restrict__ token, const VocabHeader* header,
+                     long long rows, int vec) {
   griddep_wait();
   griddep_launch_dependents();
-  if (rows < 0) rows = header->learnt;
-  if (depth < 0) depth = header->learnt;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  if (m0 >= rows) return;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < depth; k0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      {
-        const int k = o.ak == 1 ? i & 15 : i >> 6;
-        const int m = o.ak == 1 ? i >> 4 : i & 63;
-        float v = 0.f;
-        if (m0 + m < rows && k0 + k < depth) {
-          const long long mm = o.map_m ? o.map_m[m0 + m] : m0 + m;
-          v = load_f(o.A + mm * o.am + (long long)(k0 + k) * o.ak);
-        }
-        sa[k][m] = v;
-      }
-      {
-        const int k = o.bk == 1 ? i & 15 : i >> 6;
-        const int n = o.bk == 1 ? i >> 4 : i & 63;
-        float v = 0.f;
-        if (n0 + n < cols && k0 + k < depth) {
-          const long long kk = o.map_k ? o.map_k[k0 + k] : k0 + k;
-          v = load_f(o.B + kk * o.bk + (long long)(n0 + n) * o.bn);
-        }
-        sb[k][n] = v;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = sa[k][ty + 16 * i];
-        b[i] = sb[k][tx + 16 * i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
+  long long all = rows;
+  if (token) {
+    if (!header->packed) return;
+    rows = header->learnt;
+    all = (rows + 63) / 64 * 64;
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < rows && n < cols) {
-        TO* c = C + m * ldc + n;
-        if constexpr (sizeof(TO) == 4)
-          *c = add ? *c + acc[i][j] : acc[i][j];
-        else
-          store16(c, acc[i][j] * header->inv_scale);
+  const int chunks = (int)(ldd / 8);
+  const long long total = all * chunks;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total;
+       i += gridDim.x * 256ll) {
+    const long long r = i / chunks;
+    const int c = (int)(i - r * chunks) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const uint16_t* s = src + (token ? token[r] : r) * lds + c;
+      if (vec && c + 8 <= cols) {
+        v = *reinterpret_cast<const uint4*>(s);
+      } else {
+        uint16_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? s[j] : 0;
+        v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16,
+                       e[4] | e[5] << 16, e[6] | e[7] << 16);
       }
     }
-}
-
-// Softmax statistics of one piece of logits (columns v0 .. v0 + n), one
-// block per row: running maximum and sum of exponentials, and the targets'
-// logits (both over z/τ).
-__global__ void __launch_bounds__(256)
-    piece_stats_kernel(VocabTargets tg, const float* __restrict__ Z,
-                       long long ldz, int v0, int n, float2* stats,
-                       float* picked) {
-  __shared__ float s_red[8];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int r = blockIdx.x;
-  if (r >= tg.header->learnt) return;
-  const int t = tg.token[r], warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* z = Z + (long long)r * ldz;
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, z[i] * tg.inv_tau);
-  for (int o = 16; o; o >>= 1)
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s_red[warp] = m;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, s_red[w]);
-  const float2 old = v0 ? stats[r] : make_float2(-INFINITY, 0.f);
-  const float peak = fmaxf(m, old.x);
-  float s = 0.f;
-  for (int i = threadIdx.x; i < n; i += 256)
-    s += expf(z[i] * tg.inv_tau - peak);
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  __syncthreads();
-  if (lane == 0) s_red[warp] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = old.y * expf(old.x - peak);
-    for (int w = 0; w < 8; ++w) s += s_red[w];
-    stats[r] = make_float2(peak, s);
-  }
-  for (int j = threadIdx.x; j < tg.top; j += 256) {
-    const int id = tg.ids[(long long)t * tg.top + j];
-    if (id >= v0 && id < v0 + n)
-      picked[(long long)r * tg.top + j] = z[id - v0] * tg.inv_tau;
+    *reinterpret_cast<uint4*>(dst + r * ldd + c) = v;
   }
 }
 
-// loss and lse of the learnt tokens, one thread each.
-__global__ void __launch_bounds__(128)
-    finish_loss_kernel(VocabTargets tg, const float2* __restrict__ stats,
+// ------------------------------------------------------------- results
+__device__ __forceinline__ float2 merge_stats(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * exp2f(a.x - ref) + b.y * exp2f(b.x - ref));
+}
+
+// loss and lse of the learnt tokens: 8 rows a block, 128 threads a row that
+// share out its statistics (parts of them, [part][T]) and join them in a
+// fixed order.
+__global__ void __launch_bounds__(1024)
+    finish_loss_kernel(VocabTargets tg, int T, int parts,
+                       const float2* __restrict__ stats,
                        const float* __restrict__ picked, float tau,
                        float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 s_part[32][8];
   griddep_wait();
   griddep_launch_dependents();
-  const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= tg.header->learnt) return;
-  const int t = tg.token[r];
-  const float2 st = stats[r];
-  const float l = st.x + logf(st.y);
+  const int r = blockIdx.x * 8 + (threadIdx.x & 7);
+  const int slice = threadIdx.x >> 3, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const bool here = r < tg.header->learnt;
+  float2 st = make_float2(-INFINITY, 0.f);
+  if (here) {
+#pragma unroll 4
+    for (int e = slice; e < parts; e += 128)
+      st = merge_stats(st, stats[(long long)e * T + r]);
+  }
+  for (int o = 8; o < 32; o <<= 1)
+    st = merge_stats(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, o),
+                                     __shfl_xor_sync(0xffffffffu, st.y, o)));
+  if (lane < 8) s_part[warp][lane] = st;
+  __syncthreads();
+  if (warp > 0) return;
+  st = make_float2(-INFINITY, 0.f);
+  for (int w = lane >> 3; w < 32; w += 4)
+    st = merge_stats(st, s_part[w][lane & 7]);
+  for (int o = 8; o < 32; o <<= 1)
+    st = merge_stats(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, o),
+                                     __shfl_xor_sync(0xffffffffu, st.y, o)));
+  const float l = st.x * 0.69314718f + logf(st.y);
   float sum = 0.f;
-  for (int j = 0; j < tg.top; ++j) {
-    if (tg.ids[(long long)t * tg.top + j] == INT_MAX) break;
-    const float lq = tg.log_q[(long long)t * tg.top + j];
-    sum += expf(lq) * (lq - (picked[(long long)r * tg.top + j] - l));
-  }
-  loss[t] = tau * tau * sum;
-  lse[t] = l;
-}
-
-// Z of one piece becomes G·scale in place, one block per row.
-__global__ void __launch_bounds__(256)
-    piece_grad_kernel(VocabTargets tg, float* __restrict__ Z, long long ldz,
-                      int v0, int n, const float* __restrict__ lse,
-                      const float* __restrict__ grad_loss,
-                      long long grad_stride, float tau) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int r = blockIdx.x;
-  if (r >= tg.header->learnt) return;
-  const int t = tg.token[r];
-  float* z = Z + (long long)r * ldz;
-  const float l = lse[t];
-  const float g = grad_loss[t * grad_stride] * tau * tg.header->scale;
-  for (int i = threadIdx.x; i < n; i += 256) {
-    float p = expf(z[i] * tg.inv_tau - l);
-    for (int j = 0; j < tg.top; ++j) {
-      const int id = tg.ids[(long long)t * tg.top + j];
-      if (id > v0 + i) break;
-      if (id == v0 + i) p -= expf(tg.log_q[(long long)t * tg.top + j]);
+  long long t = 0;
+  if (here) {
+    t = tg.token[r];
+    for (int j = lane >> 3; j < tg.top; j += 4) {
+      if (tg.ids[t * tg.top + j] == INT_MAX) break;
+      const float lq = tg.log_q[t * tg.top + j];
+      sum += expf(lq) * (lq - (picked[(long long)r * tg.top + j] - l));
     }
-    z[i] = g * p;
+  }
+  for (int o = 8; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (here && lane < 8) {
+    loss[t] = tau * tau * sum;
+    lse[t] = l;
   }
 }
 
-// dX row by row: the sum over the pieces, rounded; zeros for the tokens
-// that are not learnt from.
+// dX row by row: the slots' sum in order, rounded; zeros for the tokens that
+// are not learnt from.  vec: four columns at a time (dX's rows are 8-byte
+// aligned).
 template <typename T16>
 __global__ void __launch_bounds__(256)
     finish_dx_kernel(int T, int D, const int* __restrict__ row,
                      const VocabHeader* header,
-                     const float* __restrict__ sum, T16* __restrict__ dX,
-                     long long lddx) {
+                     const float* __restrict__ slots, long long ld_slot,
+                     T16* __restrict__ dX, long long lddx, int vec) {
   griddep_wait();
   griddep_launch_dependents();
-  const int t = blockIdx.x;
-  const int r = row[t];
-  for (int i = threadIdx.x; i < D; i += 256)
-    store16(dX + t * lddx + i,
-            r < 0 ? 0.f : sum[(long long)r * D + i] * header->inv_scale);
+  const long long t = blockIdx.x;
+  const int r = row[t], splits = header->dx_splits;
+  const float inv_scale = header->inv_scale;
+  const float* from = slots + (long long)r * ld_slot;
+  for (int i = 4 * threadIdx.x; i < D; i += 1024) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r >= 0) {
+      for (int s = 0; s < splits; ++s) {
+        const float4 a = *reinterpret_cast<const float4*>(
+            from + (long long)s * T * ld_slot + i);
+        v.x += a.x;
+        v.y += a.y;
+        v.z += a.z;
+        v.w += a.w;
+      }
+    }
+    T16 o[4];
+    store16(o, v.x * inv_scale);
+    store16(o + 1, v.y * inv_scale);
+    store16(o + 2, v.z * inv_scale);
+    store16(o + 3, v.w * inv_scale);
+    T16* to = dX + t * lddx + i;
+    if (vec && i + 4 <= D) {
+      *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(o);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < D) to[j] = o[j];
+    }
+  }
 }
 
 // ------------------------------------------------------------- host side
@@ -375,18 +340,23 @@ struct VocabCall {
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Where a call's state lies in its workspace.
+// Where a call's state lies in its workspace, and the pieces of the
+// vocabulary the gradients go through.
 struct VocabLayout {
-  int64_t piece;  // columns of a piece
-  int64_t header, token, row, ids, log_q, stats, picked, z, dx, total;
+  int64_t piece;       // columns of G
+  int64_t max_splits;  // slots of dX
+  int64_t ld_pack;     // row stride of the packed copies
+  int64_t header, token, row, ids, log_q, x_pack, w_pack, total;
+  int64_t stats, picked;  // forward
+  int64_t g, slots;       // gradients
 };
 
-VocabLayout layout(int64_t T, int64_t V, int64_t D, int64_t top, bool grad) {
+VocabLayout layout(int64_t T, int64_t V, int64_t D, int64_t top, bool grad,
+                   bool pack_w) {
+  constexpr int64_t kMostG = 256ll << 20, kMostSlots = 512ll << 20;
   VocabLayout l = {};
-  const int64_t most = 64ll << 20;  // logits of a piece
-  l.piece = std::min(up(V, 64),
-                     std::max<int64_t>(64, most / std::max<int64_t>(T, 1) /
-                                               64 * 64));
+  const int64_t rows = std::max<int64_t>(T, 1);
+  l.ld_pack = up(D, 8);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -394,19 +364,33 @@ VocabLayout layout(int64_t T, int64_t V, int64_t D, int64_t top, bool grad) {
     return here;
   };
   l.header = take(sizeof(VocabHeader));
-  l.token = take(T * 4);
-  l.row = take(T * 4);
-  l.ids = take(T * top * 4);
-  l.log_q = take(T * top * 4);
-  l.z = take(T * l.piece * 4);
+  l.token = take(rows * 4);
+  l.row = take(rows * 4);
+  l.ids = take(rows * top * 4);
+  l.log_q = take(rows * top * 4);
+  l.x_pack = take(up(rows, 64) * l.ld_pack * 2);
+  if (pack_w) l.w_pack = take(V * l.ld_pack * 2);
   if (grad) {
-    l.dx = take(T * D * 4);
+    // equal pieces, whole tiles, of at most kMostG bytes of G
+    const int64_t widest = std::max<int64_t>(
+        kVocabTile, kMostG / (2 * rows) / kVocabTile * kVocabTile);
+    const int64_t pieces = (V + widest - 1) / widest;
+    l.piece = up((V + pieces - 1) / pieces, kVocabTile);
+    const int64_t slot = rows * up(D, 4) * 4;
+    l.max_splits = std::min<int64_t>(
+        64, std::max<int64_t>(1, kMostSlots / slot));
+    l.g = take(rows * l.piece * 2);
+    l.slots = take(l.max_splits * slot);
   } else {
-    l.stats = take(T * 8);
-    l.picked = take(T * top * 4);
+    l.stats = take((V + 127) / 128 * rows * 8);
+    l.picked = take(rows * top * 4);
   }
   l.total = at;
   return l;
+}
+
+bool fits_tensor_map(const void* p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
 }
 
 int check_call(const VocabCall& c, bool grad, bool distill) {
@@ -435,23 +419,25 @@ int check_call(const VocabCall& c, bool grad, bool distill) {
   return GEMM_F32_OK;
 }
 
-template <typename T16>
-cudaError_t run_typed(const VocabCall& c, bool grad, const WaitCfg&) {
+cudaError_t run_checked(const VocabCall& c, bool grad, int sms,
+                        const WaitCfg& wc) {
   const int T = (int)c.T, V = (int)c.V, D = (int)c.D, top = (int)c.top;
   cudaStream_t s = c.stream;
-  const VocabLayout l = layout(c.T, c.V, c.D, c.top, grad);
+  if (T == 0)  // gradients: dW = 0
+    return cudaMemset2DAsync(c.dW, c.lddw * 2, 0, c.D * 2, c.V, s);
+  const bool w_fits = fits_tensor_map(c.W, c.ldw);
+  const bool x_fits = fits_tensor_map(c.X, c.ldx);
+  const VocabLayout l = layout(c.T, c.V, c.D, c.top, grad, !w_fits);
   char* ws = static_cast<char*>(c.ws);
   auto* header = reinterpret_cast<VocabHeader*>(ws + l.header);
   int* token = reinterpret_cast<int*>(ws + l.token);
   int* row = reinterpret_cast<int*>(ws + l.row);
   int* ids = reinterpret_cast<int*>(ws + l.ids);
   float* log_q = reinterpret_cast<float*>(ws + l.log_q);
-  float* z = reinterpret_cast<float*>(ws + l.z);
-  const T16* X = static_cast<const T16*>(c.X);
-  const T16* W = static_cast<const T16*>(c.W);
-  cudaError_t e;
   const float inv_tau = 1.f / c.tau;
-  if (!c.targets && T > 0) {
+  cudaError_t e;
+
+  if (!c.targets) {
     e = launch_pdl(distill_targets_kernel,
                    dim3((T + kTargetWarps - 1) / kTargetWarps),
                    dim3(32 * kTargetWarps), 0, s, T, V, top, c.top_logits,
@@ -459,67 +445,89 @@ cudaError_t run_typed(const VocabCall& c, bool grad, const WaitCfg&) {
                    ids, log_q);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(number_tokens_kernel, dim3(1), dim3(1024), 0, s, T, V, top,
-                 c.targets, ids, log_q, c.loss, c.lse, c.grad_loss,
-                 (long long)c.grad_stride, c.tau,
-                 c.type == GEMM_F32_MIXED_F16 ? 1 : 0, token, row, header);
+  NumberArgs na = {};
+  na.T = T, na.V = V, na.top = top;
+  na.targets = c.targets;
+  na.loss = c.loss, na.lse = c.lse;
+  na.grad_loss = c.grad_loss, na.grad_stride = c.grad_stride;
+  na.tau = c.tau;
+  na.scaled = c.type == GEMM_F32_MIXED_F16;
+  na.always_pack = !x_fits;
+  na.D = D, na.piece = (int)std::min(l.piece, c.V);
+  na.pairs = std::max(1, sms / 2), na.max_splits = (int)l.max_splits;
+  e = launch_pdl(number_tokens_kernel, dim3(1), dim3(1024), 0, s, na, ids,
+                 log_q, token, row, header);
   if (e != cudaSuccess) return e;
-  const VocabTargets tg{header, token, row, ids, log_q, top, inv_tau};
-  float* sum = reinterpret_cast<float*>(ws + l.dx);
-  float2* stats = reinterpret_cast<float2*>(ws + l.stats);
-  float* picked = reinterpret_cast<float*>(ws + l.picked);
-  const unsigned rows64 = (T + 63) / 64, cols64 = (D + 63) / 64;
-  for (int64_t v0 = 0; v0 < c.V; v0 += l.piece) {
-    const int n = (int)std::min(l.piece, c.V - v0);
-    const T16* Wp = W + v0 * c.ldw;
-    if (T > 0) {
-      const Operand2<T16, T16> logits{X, c.ldx, 1, token,
-                                      Wp, 1, c.ldw, nullptr};
-      e = launch_pdl(simple_product_kernel<T16, T16, float>,
-                     dim3((n + 63) / 64, rows64), dim3(256), 0, s, logits, -1,
-                     n, D, header, z, (long long)l.piece, 0);
-      if (e != cudaSuccess) return e;
-    }
-    if (!grad) {
-      e = launch_pdl(piece_stats_kernel, dim3(T), dim3(256), 0, s, tg, z,
-                     (long long)l.piece, (int)v0, n, stats, picked);
-      if (e != cudaSuccess) return e;
-      continue;
-    }
-    if (T > 0) {
-      e = launch_pdl(piece_grad_kernel, dim3(T), dim3(256), 0, s, tg, z,
-                     (long long)l.piece, (int)v0, n, c.lse_in, c.grad_loss,
-                     (long long)c.grad_stride, c.tau);
-      if (e != cudaSuccess) return e;
-      const Operand2<float, T16> back{z, l.piece, 1, nullptr,
-                                      Wp, c.ldw, 1, nullptr};
-      e = launch_pdl(simple_product_kernel<float, T16, float>,
-                     dim3(cols64, rows64), dim3(256), 0, s, back, -1, D, n,
-                     header, sum, (long long)D, v0 ? 1 : 0);
-      if (e != cudaSuccess) return e;
-    }
-    const Operand2<float, T16> outer{z, 1, l.piece, nullptr,
-                                     X, c.ldx, 1, token};
-    e = launch_pdl(simple_product_kernel<float, T16, T16>,
-                   dim3(cols64, (n + 63) / 64), dim3(256), 0, s, outer, n, D,
-                   -1, header, static_cast<T16*>(c.dW) + v0 * c.lddw,
-                   (long long)c.lddw, 0);
-    if (e != cudaSuccess) return e;
+
+  auto pack = [&](const void* src, int64_t ld, int64_t dst, int64_t rows,
+                  const int* map, bool vec) {
+    const int64_t blocks = (up(rows, 64) * (l.ld_pack / 8) + 255) / 256;
+    return launch_pdl(pack_rows_kernel,
+                      dim3((unsigned)std::min<int64_t>(blocks, 8ll * sms)),
+                      dim3(256), 0, s, static_cast<const uint16_t*>(src),
+                      (long long)ld, D, reinterpret_cast<uint16_t*>(ws + dst),
+                      (long long)l.ld_pack, map, header, (long long)rows,
+                      vec ? 1 : 0);
+  };
+  if ((e = pack(c.X, c.ldx, l.x_pack, T, token, x_fits)) != cudaSuccess)
+    return e;
+  if (!w_fits &&
+      (e = pack(c.W, c.ldw, l.w_pack, V, nullptr, false)) != cudaSuccess)
+    return e;
+  const char* W = w_fits ? static_cast<const char*>(c.W) : ws + l.w_pack;
+  const int64_t ldw = w_fits ? c.ldw : l.ld_pack;
+
+  VocabGemm p = {};
+  p.type = c.type;
+  p.T = T, p.D = D;
+  p.X = c.X, p.ldx = c.ldx;
+  p.Xp = ws + l.x_pack, p.ldxp = l.ld_pack, p.rows_xp = (int)up(c.T, 64);
+  p.W = W, p.ldw = ldw;
+  p.v0 = 0, p.n = V;
+  p.targets = VocabTargets{header, token, ids, log_q, top, inv_tau};
+  if (!grad) {
+    p.stats = reinterpret_cast<float2*>(ws + l.stats);
+    p.picked = reinterpret_cast<float*>(ws + l.picked);
+    if ((e = launch_vocab_gemm(kVocabStats, p, sms, wc, s)) != cudaSuccess)
+      return e;
+    return launch_pdl(finish_loss_kernel, dim3((T + 7) / 8), dim3(1024), 0, s,
+                      p.targets, T, (V + 127) / 128, p.stats, p.picked, c.tau,
+                      c.loss, c.lse);
   }
-  if (T == 0) return cudaSuccess;
-  if (!grad)
-    return launch_pdl(finish_loss_kernel, dim3((T + 127) / 128), dim3(128), 0,
-                      s, tg, stats, picked, c.tau, c.loss, c.lse);
-  return launch_pdl(finish_dx_kernel<T16>, dim3(T), dim3(256), 0, s, T, D,
-                    row, header, sum, static_cast<T16*>(c.dX),
-                    (long long)c.lddx);
+  p.G = ws + l.g, p.ldg = l.piece;
+  p.lse = c.lse_in;
+  p.grad_loss = c.grad_loss, p.grad_stride = c.grad_stride, p.tau = c.tau;
+  p.slots = reinterpret_cast<float*>(ws + l.slots);
+  p.ld_slot = up(c.D, 4), p.max_splits = (int)l.max_splits;
+  p.lddw = c.lddw;
+  for (int64_t v0 = 0; v0 < c.V; v0 += l.piece) {
+    p.v0 = (int)v0, p.n = (int)std::min(l.piece, c.V - v0);
+    p.W = W + v0 * ldw * 2;
+    p.dW = static_cast<char*>(c.dW) + v0 * c.lddw * 2;
+    p.add = v0 > 0;
+    for (VocabProduct product : {kVocabGrad, kVocabDx, kVocabDw})
+      if ((e = launch_vocab_gemm(product, p, sms, wc, s)) != cudaSuccess)
+        return e;
+  }
+  const int vec = (reinterpret_cast<uintptr_t>(c.dX) & 7u) == 0 &&
+                  c.lddx % 4 == 0;
+  auto finish = [&](auto* dX) {
+    return launch_pdl(
+        finish_dx_kernel<std::remove_pointer_t<decltype(dX)>>, dim3(T),
+        dim3(256), 0, s, T, D, row, header, p.slots, p.ld_slot, dX,
+        (long long)c.lddx, vec);
+  };
+  return c.type == GEMM_F32_MIXED_BF16
+             ? finish(static_cast<__nv_bfloat16*>(c.dX))
+             : finish(static_cast<__half*>(c.dX));
 }
 
 int run_vocab(const VocabCall& c, bool grad, bool distill) {
   int st = check_call(c, grad, distill);
   if (st != GEMM_F32_OK) return st;
   if (c.T == 0 && !grad) return GEMM_F32_OK;
-  const VocabLayout l = layout(c.T, c.V, c.D, c.top, grad);
+  const VocabLayout l = layout(c.T, c.V, c.D, c.top, grad,
+                               !fits_tensor_map(c.W, c.ldw));
   if (!c.ws || (reinterpret_cast<uintptr_t>(c.ws) & 15u) != 0 ||
       c.ws_bytes < l.total)
     return GEMM_F32_ERR_INVALID_ARG;
@@ -528,8 +536,7 @@ int run_vocab(const VocabCall& c, bool grad, bool distill) {
   cudaError_t e = device_facts(&sms, &cc, &wc);
   if (e != cudaSuccess) return record_cuda_error(e);
   if (cc != 10) return GEMM_F32_ERR_UNSUPPORTED;
-  e = c.type == GEMM_F32_MIXED_BF16 ? run_typed<__nv_bfloat16>(c, grad, wc)
-                                    : run_typed<__half>(c, grad, wc);
+  e = run_checked(c, grad, sms, wc);
   return e == cudaSuccess ? GEMM_F32_OK : record_cuda_error(e);
 }
 
@@ -618,7 +625,7 @@ int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V, int64_t D,
     return -GEMM_F32_ERR_INVALID_ARG;
   if (T > 0x7fffffff || V > 0x7fffffff || D > 0x7fffffff)
     return -GEMM_F32_ERR_UNSUPPORTED;
-  return layout(T, V, D, top, grad != 0).total;
+  return layout(T, V, D, top, grad != 0, aligned == 0).total;
 }
 
 }  // extern "C"
