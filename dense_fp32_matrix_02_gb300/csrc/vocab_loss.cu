@@ -35,7 +35,8 @@ __global__ void __launch_bounds__(32 * kTargetWarps)
                            const float* __restrict__ logits, long long ldt,
                            const int64_t* __restrict__ top_ids, long long ldi,
                            float inv_tau, int* __restrict__ ids,
-                           float* __restrict__ log_q) {
+                           float* __restrict__ log_q,
+                           uint8_t* __restrict__ flags) {
   __shared__ int s_id[kTargetWarps][kVocabMaxTop];
   griddep_wait();
   griddep_launch_dependents();
@@ -67,6 +68,8 @@ __global__ void __launch_bounds__(32 * kTargetWarps)
     if (u[i] != -INFINITY) sum += expf(u[i] - peak);
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float log_sum = logf(sum);
+  // sum is 0 only where nothing counts (the largest term is 1, or NaN)
+  if (lane == 0) flags[t] = sum != 0.f;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -83,22 +86,51 @@ __global__ void __launch_bounds__(32 * kTargetWarps)
   }
 }
 
-// Numbers the tokens that are learnt from, in order (one block).  Cross
-// entropy also writes its one entry per token here.  Forward: loss and lse
-// of the other tokens are 0.  Gradients: the power of two that brings the
-// largest |g·τ| near 2^14 (binary16 G; 1 for bfloat16, whose exponents
-// need no help), and the slots that dX is summed in.
+// Numbers the tokens that are learnt from, in order, and packs their rows of
+// X where they are not read in place (some token is not learnt from, or X
+// has no tensor map).  Every block numbers all tokens, 256 a warp at a time
+// (the flags come from L2; at 8192 tokens this took a single block followed
+// by a packing kernel 17 + 11 us), and writes what belongs to its own share
+// of them.  Forward: loss and lse of the other tokens are 0.  Gradients: the
+// power of two that brings the largest |g·τ| near 2^14 (binary16 G; 1 for
+// bfloat16, whose exponents need no help), and dX's slots.
 struct NumberArgs {
-  int T, V, top;
-  const int64_t* targets;  // cross entropy, else null
+  int T, V;
+  const int64_t* targets;  // cross entropy
+  const uint8_t* flags;    // distillation
   float *loss, *lse;       // forward, else null
   const float* grad_loss;  // gradients, else null
   long long grad_stride;
   float tau;
   int scaled;       // binary16
   int always_pack;  // X has no tensor map
+  const uint16_t* X;
+  long long ldx;
+  uint16_t* Xp;
+  long long ldxp;
   int D, piece, pairs, max_splits;
+  int share;        // tokens of a block
 };
+
+// 16-bit row of n elements, then zeros up to a multiple of 8, to a 16-byte
+// aligned row; by one warp.  vec: the source is aligned too.
+__device__ __forceinline__ void pack_row(const uint16_t* __restrict__ src,
+                                         int n, uint16_t* __restrict__ dst,
+                                         bool vec, int lane) {
+  for (int c = 8 * lane; c < n; c += 256) {
+    uint4 v;
+    if (vec && c + 8 <= n) {
+      v = *reinterpret_cast<const uint4*>(src + c);
+    } else {
+      uint32_t e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = c + j < n ? src[c + j] : 0;
+      v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
+                     e[6] | e[7] << 16);
+    }
+    *reinterpret_cast<uint4*>(dst + c) = v;
+  }
+}
 
 __global__ void __launch_bounds__(1024)
     number_tokens_kernel(NumberArgs a, int* __restrict__ ids,
@@ -109,44 +141,79 @@ __global__ void __launch_bounds__(1024)
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long own0 = (long long)blockIdx.x * a.share;
+  const long long own1 = min((long long)a.T, own0 + a.share);
   int base = 0;
-  float most = 0.f;
-  for (int t0 = 0; t0 < a.T; t0 += 1024) {
-    const int t = t0 + threadIdx.x;
-    bool learnt = false;
-    if (t < a.T) {
-      if (a.targets) {
-        const int64_t y = a.targets[t];
-        learnt = y >= 0 && y < a.V;
-        ids[t] = learnt ? (int)y : INT_MAX;
-        log_q[t] = learnt ? 0.f : -INFINITY;
-      } else {
-        learnt = ids[(long long)t * a.top] != INT_MAX;
-      }
+  for (long long t0 = 0; t0 < a.T; t0 += 8192) {
+    unsigned votes[8];
+    int count = 0;
+    int64_t y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long t = t0 + warp * 256 + i * 32 + lane;
+      y[i] = -1;
+      if (t < a.T) y[i] = a.targets ? a.targets[t] : (int64_t)a.flags[t] - 1;
     }
-    const unsigned votes = __ballot_sync(0xffffffffu, learnt);
-    if (lane == 0) s_count[warp] = __popc(votes);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      votes[i] = __ballot_sync(0xffffffffu, y[i] >= 0 && y[i] < a.V);
+      count += __popc(votes[i]);
+    }
+    if (lane == 0) s_count[warp] = count;
     __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int c = s_count[w];
-      if (w < warp) before += c;
-      total += c;
+    int incl = s_count[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
     }
-    const int r = base + before + __popc(votes & ((1u << lane) - 1u));
-    if (t < a.T) {
-      row[t] = learnt ? r : -1;
-      if (learnt) token[r] = t;
-      if (a.loss && !learnt) {
-        a.loss[t] = 0.f;
-        a.lse[t] = 0.f;
+    int r0 = base + (warp ? __shfl_sync(0xffffffffu, incl, (warp - 1) & 31) : 0);
+    base += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long t = t0 + warp * 256 + i * 32 + lane;
+      const bool learnt = (votes[i] >> lane) & 1u;
+      const int r = r0 + __popc(votes[i] & ((1u << lane) - 1u));
+      if (t >= own0 && t < own1) {
+        row[t] = learnt ? r : -1;
+        if (learnt) token[r] = (int)t;
+        if (a.targets) {
+          ids[t] = learnt ? (int)y[i] : INT_MAX;
+          log_q[t] = learnt ? 0.f : -INFINITY;
+        }
+        if (a.loss && !learnt) {
+          a.loss[t] = 0.f;
+          a.lse[t] = 0.f;
+        }
       }
-      if (a.grad_loss && learnt)
-        most = fmaxf(most, fabsf(a.grad_loss[t * a.grad_stride]));
+      r0 += __popc(votes[i]);
     }
-    base += total;
     __syncthreads();
   }
+  const bool packed = a.always_pack || base != a.T;
+  if (packed) {
+    const bool vec = (reinterpret_cast<uintptr_t>(a.X) & 15u) == 0 &&
+                     a.ldx % 8 == 0;
+    for (long long t = own0 + warp; t < own1; t += 32) {
+      const int r = row[t];  // written by this block, before the barrier
+      if (r >= 0)
+        pack_row(a.X + t * a.ldx, a.D, a.Xp + r * a.ldxp, vec, lane);
+    }
+  }
+  if (blockIdx.x != 0) return;
+  if (packed) {  // Dw sums over the rows up to a multiple of 64
+    for (int r = base + warp; r < (base + 63) / 64 * 64; r += 32)
+      for (int c = 8 * lane; c < a.D; c += 256)
+        *reinterpret_cast<uint4*>(a.Xp + r * a.ldxp + c) =
+            make_uint4(0, 0, 0, 0);
+  }
+  float most = 0.f;
+  if (a.grad_loss && a.scaled)
+    for (long long t = threadIdx.x; t < a.T; t += 1024) {
+      const bool learnt = a.targets
+                              ? a.targets[t] >= 0 && a.targets[t] < a.V
+                              : a.flags[t] != 0;
+      if (learnt) most = fmaxf(most, fabsf(a.grad_loss[t * a.grad_stride]));
+    }
   for (int o = 16; o; o >>= 1)
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   if (lane == 0) s_max[warp] = most;
@@ -159,53 +226,24 @@ __global__ void __launch_bounds__(1024)
     if (a.scaled && most > 0.f && most < INFINITY)
       e = min(max(14 - ilogbf(most), -100), 100);
     header->learnt = base;
-    header->packed = a.always_pack || base != a.T;
-    header->dx_splits = vocab_dx_splits(base, a.D, a.piece, a.pairs,
-                                        a.max_splits);
+    header->packed = packed;
+    header->dx_splits = a.grad_loss ? vocab_dx_splits(base, a.D, a.piece,
+                                                      a.pairs, a.max_splits)
+                                    : 1;
     header->scale = ldexpf(1.f, e);
     header->inv_scale = ldexpf(1.f, -e);
   }
 }
 
-// ------------------------------------------------------------- copies
-// Rows of 16-bit values, `cols` wide, to 16-byte aligned rows: X's learnt
-// tokens in order, then zero rows up to a multiple of 64 (token given: the
-// count is the header's, and nothing is done unless X is read packed), or a
-// matrix whose rows have no tensor map.  vec: the source too is aligned.
+// W's rows where they have no tensor map, one warp a row.
 __global__ void __launch_bounds__(256)
     pack_rows_kernel(const uint16_t* __restrict__ src, long long lds, int cols,
-                     uint16_t* __restrict__ dst, long long ldd,
-                     const int* __restrict__ token, const VocabHeader* header,
-                     long long rows, int vec) {
+                     uint16_t* __restrict__ dst, long long ldd, int rows) {
   griddep_wait();
   griddep_launch_dependents();
-  long long all = rows;
-  if (token) {
-    if (!header->packed) return;
-    rows = header->learnt;
-    all = (rows + 63) / 64 * 64;
-  }
-  const int chunks = (int)(ldd / 8);
-  const long long total = all * chunks;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total;
-       i += gridDim.x * 256ll) {
-    const long long r = i / chunks;
-    const int c = (int)(i - r * chunks) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const uint16_t* s = src + (token ? token[r] : r) * lds + c;
-      if (vec && c + 8 <= cols) {
-        v = *reinterpret_cast<const uint4*>(s);
-      } else {
-        uint16_t e[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? s[j] : 0;
-        v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16,
-                       e[4] | e[5] << 16, e[6] | e[7] << 16);
-      }
-    }
-    *reinterpret_cast<uint4*>(dst + r * ldd + c) = v;
-  }
+  const int warps = gridDim.x * 8;
+  for (long long r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps)
+    pack_row(src + r * lds, cols, dst + r * ldd, false, threadIdx.x & 31);
 }
 
 // ------------------------------------------------------------- results
@@ -230,6 +268,18 @@ __global__ void __launch_bounds__(1024)
   const int slice = threadIdx.x >> 3, warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const bool here = r < tg.header->learnt;
+  // the first warp's later loads, ahead of the statistics'
+  long long t = 0;
+  int id = INT_MAX;
+  float lq = 0.f, at = 0.f;
+  if (warp == 0 && here) {
+    t = tg.token[r];
+    if (lane >> 3 < tg.top) {
+      id = tg.ids[t * tg.top + (lane >> 3)];
+      lq = tg.log_q[t * tg.top + (lane >> 3)];
+      at = picked[(long long)r * tg.top + (lane >> 3)];
+    }
+  }
   float2 st = make_float2(-INFINITY, 0.f);
   if (here) {
 #pragma unroll 4
@@ -250,14 +300,13 @@ __global__ void __launch_bounds__(1024)
                                      __shfl_xor_sync(0xffffffffu, st.y, o)));
   const float l = st.x * 0.69314718f + logf(st.y);
   float sum = 0.f;
-  long long t = 0;
-  if (here) {
-    t = tg.token[r];
-    for (int j = lane >> 3; j < tg.top; j += 4) {
-      if (tg.ids[t * tg.top + j] == INT_MAX) break;
-      const float lq = tg.log_q[t * tg.top + j];
-      sum += expf(lq) * (lq - (picked[(long long)r * tg.top + j] - l));
-    }
+  for (int j = lane >> 3; id != INT_MAX;) {
+    sum += expf(lq) * (lq - (at - l));
+    j += 4;
+    if (j >= tg.top) break;
+    id = tg.ids[t * tg.top + j];
+    lq = tg.log_q[t * tg.top + j];
+    at = picked[(long long)r * tg.top + j];
   }
   for (int o = 8; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (here && lane < 8) {
@@ -346,7 +395,7 @@ struct VocabLayout {
   int64_t piece;       // columns of G
   int64_t max_splits;  // slots of dX
   int64_t ld_pack;     // row stride of the packed copies
-  int64_t header, token, row, ids, log_q, x_pack, w_pack, total;
+  int64_t header, token, row, flags, ids, log_q, x_pack, w_pack, total;
   int64_t stats, picked;  // forward
   int64_t g, slots;       // gradients
 };
@@ -366,6 +415,7 @@ VocabLayout layout(int64_t T, int64_t V, int64_t D, int64_t top, bool grad,
   l.header = take(sizeof(VocabHeader));
   l.token = take(rows * 4);
   l.row = take(rows * 4);
+  l.flags = take(rows);
   l.ids = take(rows * top * 4);
   l.log_q = take(rows * top * 4);
   l.x_pack = take(up(rows, 64) * l.ld_pack * 2);
@@ -437,43 +487,40 @@ cudaError_t run_checked(const VocabCall& c, bool grad, int sms,
   const float inv_tau = 1.f / c.tau;
   cudaError_t e;
 
+  auto* flags = reinterpret_cast<uint8_t*>(ws + l.flags);
   if (!c.targets) {
     e = launch_pdl(distill_targets_kernel,
                    dim3((T + kTargetWarps - 1) / kTargetWarps),
                    dim3(32 * kTargetWarps), 0, s, T, V, top, c.top_logits,
                    (long long)c.ldt, c.top_ids, (long long)c.ldi, inv_tau,
-                   ids, log_q);
+                   ids, log_q, flags);
     if (e != cudaSuccess) return e;
   }
   NumberArgs na = {};
-  na.T = T, na.V = V, na.top = top;
-  na.targets = c.targets;
+  na.T = T, na.V = V;
+  na.targets = c.targets, na.flags = flags;
   na.loss = c.loss, na.lse = c.lse;
   na.grad_loss = c.grad_loss, na.grad_stride = c.grad_stride;
   na.tau = c.tau;
   na.scaled = c.type == GEMM_F32_MIXED_F16;
   na.always_pack = !x_fits;
+  na.X = static_cast<const uint16_t*>(c.X), na.ldx = c.ldx;
+  na.Xp = reinterpret_cast<uint16_t*>(ws + l.x_pack), na.ldxp = l.ld_pack;
   na.D = D, na.piece = (int)std::min(l.piece, c.V);
   na.pairs = std::max(1, sms / 2), na.max_splits = (int)l.max_splits;
-  e = launch_pdl(number_tokens_kernel, dim3(1), dim3(1024), 0, s, na, ids,
+  const int blocks = std::min(sms, (T + 31) / 32);
+  na.share = (T + blocks - 1) / blocks;
+  e = launch_pdl(number_tokens_kernel, dim3(blocks), dim3(1024), 0, s, na, ids,
                  log_q, token, row, header);
   if (e != cudaSuccess) return e;
-
-  auto pack = [&](const void* src, int64_t ld, int64_t dst, int64_t rows,
-                  const int* map, bool vec) {
-    const int64_t blocks = (up(rows, 64) * (l.ld_pack / 8) + 255) / 256;
-    return launch_pdl(pack_rows_kernel,
-                      dim3((unsigned)std::min<int64_t>(blocks, 8ll * sms)),
-                      dim3(256), 0, s, static_cast<const uint16_t*>(src),
-                      (long long)ld, D, reinterpret_cast<uint16_t*>(ws + dst),
-                      (long long)l.ld_pack, map, header, (long long)rows,
-                      vec ? 1 : 0);
-  };
-  if ((e = pack(c.X, c.ldx, l.x_pack, T, token, x_fits)) != cudaSuccess)
-    return e;
-  if (!w_fits &&
-      (e = pack(c.W, c.ldw, l.w_pack, V, nullptr, false)) != cudaSuccess)
-    return e;
+  if (!w_fits) {
+    e = launch_pdl(pack_rows_kernel, dim3(std::min(8 * sms, (V + 7) / 8)),
+                   dim3(256), 0, s, static_cast<const uint16_t*>(c.W),
+                   (long long)c.ldw, D,
+                   reinterpret_cast<uint16_t*>(ws + l.w_pack),
+                   (long long)l.ld_pack, V);
+    if (e != cudaSuccess) return e;
+  }
   const char* W = w_fits ? static_cast<const char*>(c.W) : ws + l.w_pack;
   const int64_t ldw = w_fits ? c.ldw : l.ld_pack;
 

@@ -264,26 +264,32 @@ def batched_workspace_size(opA, opB, M, N, K, batch=1) -> int:
     return n
 
 
-def _scratch(nbytes, device, stream):
-    """A device byte buffer for one call on `stream` (a torch stream, a raw
-    handle or None = current).  The caching allocator is told when the
-    stream is not the current one, so that the buffer is not handed out
-    again while that stream may still use it."""
+def _in_use_on(buf, stream):
+    """Tells the caching allocator that `stream` (a torch stream or a raw
+    handle) uses `buf`, when it is not the current one, so that the buffer
+    is not handed out again while that stream may still use it."""
     import torch
-    buf = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
-    if stream is None:
-        return buf
-    current = torch.cuda.current_stream(device)
+    current = torch.cuda.current_stream(buf.device)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") \
         else int(stream)
     if handle == current.cuda_stream:
-        return buf
+        return
     if isinstance(stream, torch.cuda.Stream):
         buf.record_stream(stream)
     elif handle == 0:
-        buf.record_stream(torch.cuda.default_stream(device))
+        buf.record_stream(torch.cuda.default_stream(buf.device))
     else:
-        buf.record_stream(torch.cuda.ExternalStream(handle, device=device))
+        buf.record_stream(torch.cuda.ExternalStream(handle,
+                                                    device=buf.device))
+
+
+def _scratch(nbytes, device, stream):
+    """A device byte buffer for one call on `stream` (a torch stream, a raw
+    handle or None = current)."""
+    import torch
+    buf = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        _in_use_on(buf, stream)
     return buf
 
 

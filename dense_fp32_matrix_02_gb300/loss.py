@@ -88,10 +88,11 @@ def _teacher(top_logits, top_ids, T, like):
 def _new(shape, dtype, like, stream):
     """An output allocated here, known to the allocator to be in use on
     `stream` when that is not the current one."""
-    import math
     import torch
-    n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
-    return _g._scratch(n, like.device, stream)[:n].view(dtype).view(shape)
+    out = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        _g._in_use_on(out, stream)
+    return out
 
 
 def _given(t, shape, dtype, like, name, stream):
