@@ -4,17 +4,21 @@
 //   Stats  z = X·Wᵀ:  per row and 128 columns max and Σ exp, and the logits
 //          of the row's targets;
 //   Grad   z = X·W_pᵀ: G = g·τ·(exp(z/τ − lse) − q), rounded to 16 bits;
-//   Dx     G·W_p, added into fp32 slots (one per split of the depth);
-//   Dw     Gᵀ·X, rounded to 16 bits.
+//   Dw     Gᵀ·X, rounded to 16 bits (or, few tiles, into fp32 slots);
+//   Dx     G·W_p, added into fp32 slots.
+// Stats is the forward launch.  The gradients take one launch per piece of
+// the vocabulary, which makes Grad of one piece beside Dw and Dx of the one
+// before: they do not depend on each other, and the depth of Dx is cut so
+// that every pair of CTAs ends at the same time (VocabShare).
 //
 // Persistent clusters of two CTAs, one pair per two SMs, walk the tiles.  A
 // pair works on one tile by tcgen05.mma.cta_group::2 (M 256, N 256, K 16):
 // each CTA holds 128 rows of A and 128 columns of B in its shared memory
-// (32 KB a k-block of 64), the tensor cores read B from both, and each CTA's
+// (32 KB a step of 64), the tensor cores read B from both, and each CTA's
 // TMEM receives its 128 rows × 256 columns of the result.  Against a tile of
-// 128 × 256 per CTA this loads a third less per multiply (measured with the
-// kernels below).  Two accumulators of 256 columns fill TMEM, so a tile's
-// epilogue overlaps the next tile's products.
+// 128 × 256 per CTA this loads a third less per multiply.  Two accumulators
+// of 256 columns fill TMEM, so a tile's epilogue overlaps the next tile's
+// products.
 //   warp 0      TMA producer of its own CTA's halves, into a ring; the bytes
 //               of both CTAs count on the first CTA's barrier.
 //   warp 1      of the first CTA: MMA issuer.  tcgen05.commit releases the
@@ -43,26 +47,29 @@ constexpr int kPartBytes = kHalf * kBK * 2;  // 16 KB: one operand, one stage
 constexpr int kStageBytes = 2 * kPartBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kStagingBytes = 4096;          // one epilogue warp's block
+constexpr int kStagingBytes = 2 * 4096;      // one epilogue warp's two blocks
 constexpr int kTmemCols = 512;
 constexpr long long kDrainNs = 2000000000LL;
 constexpr uint32_t kSleepNs = 100000;
-constexpr int kGroup = 16;  // tile rows walked together (L2 reuse)
 constexpr float kLog2e = 1.4426950408889634f;
+// Stats: steps summed in the tensor cores before the epilogue adds them to
+// its own fp32 sums.  The accumulator drops bits below its last at every
+// step, always towards zero; at a depth of 2048 to 4096 the losses' error
+// against 64 bits was 1-3e-6 without this.
+constexpr int kSumSteps = 16;
 
-template <int PRODUCT>
+enum Kind { kStats, kGrad, kDw, kDx };
+
+template <bool FORWARD>
 struct Shape {
-  static constexpr bool kMnA = PRODUCT == kVocabDw;  // A along M
-  static constexpr bool kMnB = PRODUCT == kVocabDx || PRODUCT == kVocabDw;
-  static constexpr bool kStaged = PRODUCT != kVocabStats;
-  static constexpr int kStages = kStaged ? 6 : 7;
+  static constexpr int kStages = FORWARD ? 7 : 5;
   static constexpr int kOffStaging = kStages * kStageBytes;
   static constexpr int kOffCtl =
-      kOffStaging + (kStaged ? kEpiWarps * kStagingBytes : 0);
+      kOffStaging + (FORWARD ? 0 : kEpiWarps * kStagingBytes);
   struct __align__(8) Control {
     uint64_t full[kStages];   // TMA of both CTAs -> MMA (first CTA's is used)
     uint64_t empty[kStages];  // MMA completion -> producers
-    uint64_t acc_full[2];     // last MMA of a tile -> epilogues
+    uint64_t acc_full[2];     // last MMA of a sum -> epilogues
     uint64_t acc_empty[2];    // epilogue warps of both CTAs -> MMA
     uint64_t mma_done;
     uint32_t tmem_base;
@@ -163,13 +170,13 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
-// 3-D fp32 store and in-memory addition of a block (c0 innermost).
-__device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src,
-                                           int c0, int c1, int c2) {
+// Adds a block in memory (c0 innermost).
+__device__ __forceinline__ void tma_add_2d(const void* tmap, uint32_t src,
+                                           int c0, int c1) {
   asm volatile(
-      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
-      "[%0, {%2, %3, %4}], [%1];\n" ::"l"(tmap),
-      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group "
+      "[%0, {%2, %3}], [%1];\n" ::"l"(tmap),
+      "r"(src), "r"(c0), "r"(c1)
       : "memory");
 }
 
@@ -194,57 +201,201 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 
 // What the kernel needs beside the tensor maps.
 struct Args {
-  int T, D, n;        // n: columns of the piece
-  int v0;
+  int T, V, D;
   VocabTargets targets;
   float2* stats;
   float* picked;
+  int grad_v0, grad_n, back_v0, back_n, piece, first;
   const float* lse;
   const float* grad_loss;
   long long grad_stride;
   float tau;
-  int add;
-  uint16_t* dw;       // direct stores (no tensor map fits dW), else null
+  int dw_rows;    // rows between two slots of dW
+  uint16_t* dw;   // dW where it has no tensor map, else null
   long long lddw;
 };
 
-// One tile of the walk: its place and its k-blocks.
-struct Unit {
-  int tm, tn, split, kb0, kb1;
+struct Maps {
+  CUtensorMap x, xp, w;  // operands, 64 × 64 boxes
+  CUtensorMap g_out;     // Grad's G, 64 × 32
+  CUtensorMap g_in;      // Dw's and Dx's G, 64 × 64
+  CUtensorMap dw;        // 64 × 32
+  CUtensorMap slots, dw_slots;  // fp32, 32 × 32
 };
 
-__device__ __forceinline__ Unit unit_of(int u, int tiles_m, int tiles_n,
-                                        int nk, int splits) {
-  Unit w;
-  const int tiles = tiles_m * tiles_n;
-  w.split = u / tiles;
-  tile_coords<kGroup>(u - w.split * tiles, tiles_m, tiles_n, w.tm, w.tn);
-  w.kb0 = (int)((long long)nk * w.split / splits);
-  w.kb1 = (int)((long long)nk * (w.split + 1) / splits);
-  return w;
-}
+// One sum of a pair: a tile (or, Dx and split Dw, a share of its depth).
+struct Unit {
+  int kind;
+  int tm, tn;
+  int kb0, kb1;
+  int slot;
+};
 
-// A row's entries from column c on: the place of the first with id >= c.
-__device__ __forceinline__ int first_entry(const int* ids, int top, int c) {
-  int lo = 0, hi = top;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ids[mid] < c)
-      lo = mid + 1;
-    else
-      hi = mid;
+// The walk of one pair over its units.  Gradients: dW and dX of the piece
+// before, whose G the last launch has just written, then Grad.
+template <bool FORWARD>
+struct Walk {
+  int stage, j, pair, pairs;
+  int tiles_m, tiles_n, steps;       // Stats or Grad
+  int dw_m, dw_n, dw_steps, splits;  // Dw
+  int dx_m, dx_n, dx_steps, line;    // Dx; line: a whole piece's steps
+  int whole, x, x1, slot;            // whole: tiles before the line's
+
+  __device__ __forceinline__ Walk(const Args& p, const VocabHeader* h,
+                                  int pair_, int pairs_)
+      : stage(FORWARD ? 3 : 0), j(pair_), pair(pair_), pairs(pairs_) {
+    const int learnt = h->learnt;
+    tiles_m = vocab_tiles(learnt);
+    tiles_n = vocab_tiles(FORWARD ? p.V : p.grad_n);
+    steps = vocab_steps(p.D);
+    if (!FORWARD) {
+      dx_n = dw_n = vocab_tiles(p.D);
+      dw_m = vocab_tiles(p.back_n);
+      dw_steps = vocab_steps(learnt);
+      splits = h->dw_splits;
+      dx_m = p.back_n > 0 ? tiles_m : 0;
+      dx_steps = vocab_steps(p.back_n);
+      line = vocab_steps(p.piece);
+      whole = h->dx_rounds * pairs;
+      x = h->share[pair].x0;
+      x1 = p.back_n > 0 ? h->share[pair].x1 : x;
+      slot = h->share[pair].slot;
+    }
   }
-  return lo;
+
+  __device__ __forceinline__ bool next(Unit& u) {
+    if (stage == 0) {
+      const int tiles = dw_m * dw_n;
+      if (j < tiles * splits) {
+        u.kind = kDw;
+        u.slot = j / tiles;
+        tile_coords<kVocabGroup>(j - u.slot * tiles, dw_m, dw_n, u.tm, u.tn);
+        u.kb0 = (int)((long long)dw_steps * u.slot / splits);
+        u.kb1 = (int)((long long)dw_steps * (u.slot + 1) / splits);
+        j += pairs;
+        return true;
+      }
+      stage = 1;
+      j = pair;
+    }
+    if (stage == 1) {
+      if (j < whole && j < dx_m * dx_n) {
+        u.kind = kDx;
+        tile_coords<kVocabGroup>(j, dx_m, dx_n, u.tm, u.tn);
+        u.kb0 = 0;
+        u.kb1 = dx_steps;
+        u.slot = 0;
+        j += pairs;
+        return true;
+      }
+      stage = 2;
+    }
+    if (stage == 2) {
+      if (x < x1) {
+        const int tile = x / line;
+        const int end = min(x1, (tile + 1) * line);
+        u.kind = kDx;
+        tile_coords<kVocabGroup>(whole + tile, dx_m, dx_n, u.tm, u.tn);
+        // a shorter last piece is cut in proportion
+        u.kb0 = (int)((long long)(x - tile * line) * dx_steps / line);
+        u.kb1 = (int)((long long)(end - tile * line) * dx_steps / line);
+        u.slot = slot;
+        slot = 0;
+        x = end;
+        return true;
+      }
+      stage = 3;
+      // the other way round, so that no pair has the last, partly filled
+      // round of both dW and G
+      j = pairs - 1 - pair;
+    }
+    if (j >= tiles_m * tiles_n) return false;
+    u.kind = FORWARD ? kStats : kGrad;
+    tile_coords<kVocabGroup>(j, tiles_m, tiles_n, u.tm, u.tn);
+    u.kb0 = 0;
+    u.kb1 = steps;
+    u.slot = 0;
+    j += pairs;
+    return true;
+  }
+};
+
+// A row's entries from a column on, four of them ahead in registers: the
+// next id is at hand when one is passed.
+struct Entries {
+  const int* ids;
+  const float* weights;
+  int at, top;
+  int id[4];
+  float q[4];
+
+  __device__ __forceinline__ void none() {
+    at = top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = INT_MAX;
+  }
+  template <bool WEIGHTS>
+  __device__ __forceinline__ void start(const VocabTargets& tg, long long t,
+                                        int column) {
+    ids = tg.ids + t * tg.top;
+    weights = tg.weights + t * tg.top;
+    top = tg.top;
+    // the first with id >= column: eight-way steps, as each costs the
+    // latency of its loads
+    int lo = 0;
+    for (int width = top; width > 1;) {
+      const int step = (width + 7) >> 3;
+      int below = 0;
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        const int j = lo + i * step - 1;
+        below += i * step <= width && j < top && ids[j] < column;
+      }
+      lo += below * step;
+      width = step;
+    }
+    at = lo;
+    if (at < top && ids[at] < column) ++at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool here = at + i < top;
+      id[i] = here ? ids[at + i] : INT_MAX;
+      if (WEIGHTS) q[i] = here ? weights[at + i] : 0.f;
+    }
+  }
+  template <bool WEIGHTS>
+  __device__ __forceinline__ void pass() {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      id[i] = id[i + 1];
+      if (WEIGHTS) q[i] = q[i + 1];
+    }
+    const bool here = at + 4 < top;
+    id[3] = here ? ids[at + 4] : INT_MAX;
+    if (WEIGHTS) q[3] = here ? weights[at + 4] : 0.f;
+    ++at;
+  }
+};
+
+// f[i], i < 32 differing by lane: a tree of selections.
+__device__ __forceinline__ float pick(const float* f, int i) {
+  float a[16], b[8], c[4];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) a[j] = (i & 16) ? f[j + 16] : f[j];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = (i & 8) ? a[j + 8] : a[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = (i & 4) ? b[j + 4] : b[j];
+  const float d0 = (i & 2) ? c[2] : c[0], d1 = (i & 2) ? c[3] : c[1];
+  return (i & 1) ? d1 : d0;
 }
 
-template <int AB_TYPE, int PRODUCT>
+template <int AB_TYPE, bool FORWARD>
 __global__ void __launch_bounds__(kThreads, 1)
-    vocab_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
-                      const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_xp,
-                      const __grid_constant__ CUtensorMap map_c, Args p,
-                      WaitCfg wc) {
-  using Sh = Shape<PRODUCT>;
+    vocab_gemm_kernel(const __grid_constant__ Maps maps,
+                      const __grid_constant__ Args p,
+                      const __grid_constant__ WaitCfg wc) {
+  using Sh = Shape<FORWARD>;
   using Control = typename Sh::Control;
   constexpr int kStages = Sh::kStages;
   extern __shared__ unsigned char smem_raw[];
@@ -277,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&map_a);
-    prefetch_tmap(&map_b);
+    prefetch_tmap(&maps.x);
+    prefetch_tmap(&maps.w);
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -293,60 +444,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const VocabHeader* header = p.targets.header;
   const int learnt = header->learnt;
-  const int rows = PRODUCT == kVocabDw ? p.n : learnt;
-  const int cols = Sh::kMnB ? p.D : p.n;
-  const int depth = PRODUCT == kVocabDw   ? learnt
-                    : PRODUCT == kVocabDx ? p.n
-                                          : p.D;
-  const int splits = PRODUCT == kVocabDx ? header->dx_splits : 1;
-  const int tiles_m = (rows + kVocabTile - 1) / kVocabTile;
-  const int tiles_n = (cols + kVocabTile - 1) / kVocabTile;
-  const int nk = (depth + kBK - 1) / kBK;
-  const int units = tiles_m * tiles_n * splits;
+  Walk<FORWARD> walk(p, header, pair, pairs);
+  Unit u;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const bool packed = header->packed != 0;
-      const void* ma = &map_a;
-      const void* mb = &map_b;
-      if (PRODUCT == kVocabDw) {
-        if (packed) mb = &map_xp;
-      } else if (PRODUCT != kVocabDx) {
-        if (packed) ma = &map_xp;
-      }
+    if (lane == 0 && !(wc.debug & kDebugStallProducer)) {
+      const void* mx = header->packed ? &maps.xp : &maps.x;
       int it = 0;
-      if (!(wc.debug & kDebugStallProducer)) {
-        for (int u = pair; u < units && !*abort; u += pairs) {
-          const Unit w = unit_of(u, tiles_m, tiles_n, nk, splits);
-          const int m0 = w.tm * kVocabTile + (int)rank * kHalf;
-          const int n0 = w.tn * kVocabTile + (int)rank * kHalf;
-          for (int kb = w.kb0; kb < w.kb1; ++kb) {
-            const int s = it % kStages;
-            if (it >= kStages &&
-                !bounded_wait(empty(s), ((it / kStages) - 1) & 1, wc.limit,
-                              abort, 0)) {
-              *abort = 1;
-              record_status(wc.status, kStatusTimeoutEmpty);
-              break;
-            }
-            if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
-            const uint32_t bar = cluster_map(full(s), 0);
-            const uint32_t a = sbase + s * kStageBytes, b = a + kPartBytes;
-            if (Sh::kMnA) {
-              tma_load2_2d(a, ma, bar, m0, kb * kBK);
-              tma_load2_2d(a + kPartBytes / 2, ma, bar, m0 + 64, kb * kBK);
-            } else {
-              tma_load2_2d(a, ma, bar, kb * kBK, m0);
-            }
-            if (Sh::kMnB) {
-              tma_load2_2d(b, mb, bar, n0, kb * kBK);
-              tma_load2_2d(b + kPartBytes / 2, mb, bar, n0 + 64, kb * kBK);
-            } else {
-              tma_load2_2d(b, mb, bar, kb * kBK, n0);
-            }
-            ++it;
+      while (!*abort && walk.next(u)) {
+        const int m0 = u.tm * kVocabTile + (int)rank * kHalf;
+        const int n0 = u.tn * kVocabTile + (int)rank * kHalf;
+        // operands K-major: x along the depth; else x along the tile
+        const bool mn_a = u.kind == kDw, mn_b = u.kind == kDw || u.kind == kDx;
+        const void* ma = u.kind == kStats || u.kind == kGrad
+                             ? mx
+                             : (const void*)&maps.g_in;
+        const void* mb = u.kind == kDw ? mx : (const void*)&maps.w;
+        // W's rows: the piece's, or the piece's along the depth
+        const int bn = u.kind == kGrad ? p.grad_v0 + n0 : n0;
+        const int bk = u.kind == kDx ? p.back_v0 : 0;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          const int s = it % kStages;
+          if (it >= kStages &&
+              !bounded_wait(empty(s), ((it / kStages) - 1) & 1, wc.limit,
+                            abort, 0)) {
+            *abort = 1;
+            record_status(wc.status, kStatusTimeoutEmpty);
+            break;
           }
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+          const uint32_t bar = cluster_map(full(s), 0);
+          const uint32_t a = sbase + s * kStageBytes, b = a + kPartBytes;
+          const int k = kb * kBK;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tma_load2_2d(a + i * (kPartBytes / 2), ma, bar,
+                         mn_a ? m0 + 64 * i : k, mn_a ? k : m0 + 64 * i);
+            tma_load2_2d(b + i * (kPartBytes / 2), mb, bar,
+                         mn_b ? bn + 64 * i : k, mn_b ? bk + k : bn + 64 * i);
+          }
+          ++it;
         }
       }
       if (*abort && rank == 0) {  // let the copies still in flight land
@@ -365,45 +503,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         record_status(wc.status, kStatusTimeoutDrain);
     }
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc =
-          idesc_f16(256, 256, AB_TYPE, Sh::kMnB) | (Sh::kMnA ? 1u << 15 : 0u);
-      int it = 0;
+      int it = 0, i = 0;  // steps; sums
       bool ok = true;
-      for (int u = pair, i = 0; ok && u < units; u += pairs, ++i) {
-        const Unit w = unit_of(u, tiles_m, tiles_n, nk, splits);
-        const int b = i & 1;
-        if (i >= 2 && !wait_cluster(acc_empty(b), ((i >> 1) - 1) & 1,
-                                    wc.limit, abort)) {
-          *abort = 1;
-          record_status(wc.status, kStatusTimeoutMma);
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d_tmem = tmem + b * 256;
-        for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!wait_cluster(full(s), (it / kStages) & 1, wc.limit, abort)) {
+      while (ok && walk.next(u)) {
+        const bool mn_a = u.kind == kDw, mn_b = u.kind == kDw || u.kind == kDx;
+        const uint32_t idesc =
+            idesc_f16(256, 256, AB_TYPE, mn_b) | (mn_a ? 1u << 15 : 0u);
+        // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes else
+        const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
+        int kb = u.kb0;
+        do {  // one sum; Stats: several to a tile
+          const int end =
+              FORWARD && u.kb1 - kb > kSumSteps ? kb + kSumSteps : u.kb1;
+          const int b = i & 1;
+          if (i >= 2 && !wait_cluster(acc_empty(b), ((i >> 1) - 1) & 1,
+                                      wc.limit, abort)) {
             *abort = 1;
-            record_status(wc.status, kStatusTimeoutFull);
+            record_status(wc.status, kStatusTimeoutMma);
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a0 = sbase + s * kStageBytes, b0 = a0 + kPartBytes;
+          const uint32_t d_tmem = tmem + b * 256;
+          for (const int k0 = kb; kb < end; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!wait_cluster(full(s), (it / kStages) & 1, wc.limit, abort)) {
+              *abort = 1;
+              record_status(wc.status, kStatusTimeoutFull);
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a0 = sbase + s * kStageBytes, b0 = a0 + kPartBytes;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes else
-            const uint64_t ad =
-                Sh::kMnA ? smem_desc_sw128(a0 + 2048 * kk, kPartBytes / 2, 1024)
-                         : smem_desc_sw128(a0 + 32 * kk, 16, 1024);
-            const uint64_t bd =
-                Sh::kMnB ? smem_desc_sw128(b0 + 2048 * kk, kPartBytes / 2, 1024)
-                         : smem_desc_sw128(b0 + 32 * kk, 16, 1024);
-            mma2_f16_ss(d_tmem, ad, bd, idesc, kb != w.kb0 || kk != 0);
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma2_f16_ss(d_tmem,
+                          smem_desc_sw128(a0 + step_a * kk, kPartBytes / 2,
+                                          1024),
+                          smem_desc_sw128(b0 + step_b * kk, kPartBytes / 2,
+                                          1024),
+                          idesc, kb != k0 || kk != 0);
+            tc_commit2(empty(s));
           }
-          tc_commit2(empty(s));
-        }
-        if (ok) tc_commit2(acc_full(b));
+          if (ok) tc_commit2(acc_full(b));
+          ++i;
+        } while (ok && kb < u.kb1);
       }
       // no MMA may still run when TMEM is freed at the end
       tc_commit2(mma_done);
@@ -414,135 +558,167 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;         // TMEM lane quarter
     const int h = (warp - 2) >> 2;  // column half
-    const uint32_t lane_bits = (uint32_t)(q * 32) << 16;
-    // staging: row (lane) of 128 bytes, its 16-byte chunk j at j ^ (row mod
-    // 8), the layout a 128-byte-swizzle TMA store reads
-    unsigned char* stg = smem + Sh::kOffStaging + (warp - 2) * kStagingBytes;
-    const uint32_t stg_s =
-        sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
+    const uint32_t my_tmem =
+        tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
     const float c2 = p.targets.inv_tau * kLog2e;
-    const float inv_scale = header->inv_scale;
-    const int store_rows = PRODUCT == kVocabGrad ? p.T : rows;
-    for (int u = pair, i = 0; u < units; u += pairs, ++i) {
-      const Unit w = unit_of(u, tiles_m, tiles_n, nk, splits);
+    int i = 0;  // sums
+    // waits for the next sum; its accumulator's address
+    auto arrived = [&](uint32_t& acc) -> bool {
       const int b = i & 1;
-      const int m0 = w.tm * kVocabTile + (int)rank * kHalf + q * 32;
-      const int r = m0 + lane;
-      const int n0 = w.tn * kVocabTile + h * 128;
-
-      // this row's targets, while the tile accumulates
-      const int* ids = nullptr;
-      const float* log_q = nullptr;
-      int at = 0, next = INT_MAX;  // next: id of the next entry, v0 taken off
-      float shift = 0.f, g = 0.f;
-      if (PRODUCT == kVocabStats || PRODUCT == kVocabGrad) {
-        if (r < learnt) {
-          const long long t = p.targets.token[r];
-          ids = p.targets.ids + t * p.targets.top;
-          at = p.targets.top == 1 ? (ids[0] < p.v0 + n0 ? 1 : 0)
-                                  : first_entry(ids, p.targets.top, p.v0 + n0);
-          if (at < p.targets.top) next = ids[at] - p.v0;
-          if (PRODUCT == kVocabGrad) {
-            log_q = p.targets.log_q + t * p.targets.top;
-            shift = p.lse[t] * kLog2e;
-            g = p.grad_loss[t * p.grad_stride] * p.tau * header->scale;
-          }
-        }
-      }
-
       const bool ok =
           bounded_wait(acc_full(b), (i >> 1) & 1, wc.limit, abort, kSleepNs);
       if (!__all_sync(0xffffffffu, ok)) {
         *abort = 1;
         if (lane == 0) record_status(wc.status, kStatusTimeoutMma);
-        break;
+        return false;
       }
       tc_fence_after_sync();
-      float peak = -INFINITY, sum = 0.f;
-#pragma unroll 1
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(tmem + lane_bits + b * 256 + h * 128 + c0, v);
-        tmem_ld_wait();
-        if (c0 == 96) {
-          // all of this warp's part of the accumulator is in registers
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_map(acc_empty(b), 0));
-        }
-        const int n = n0 + c0;
-        if (n >= cols) continue;  // (c0 = 96 is never skipped above)
-        float f[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+      acc = my_tmem + b * 256;
+      return true;
+    };
+    // this warp's part of the accumulator is in registers
+    auto release = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_map(acc_empty(i & 1), 0));
+      ++i;
+    };
 
-        if constexpr (PRODUCT == kVocabStats) {
-          while (__any_sync(0xffffffffu, next < n + 32)) {
-            if (next < n + 32) {
-              float z = 0.f;
+    if constexpr (FORWARD) {
+      while (walk.next(u)) {
+        const int r = u.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
+        const int n0 = u.tn * kVocabTile + h * 128;
+        // this row's targets, while the tile accumulates
+        Entries e;
+        e.none();
+        if (r < learnt)
+          e.start<false>(p.targets,
+                         learnt == p.T ? r : p.targets.token[r], n0);
+        float f[128];
+        uint32_t acc;
+        if (!arrived(acc)) break;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (next == n + j) z = f[j];
-              p.picked[(long long)r * p.targets.top + at] =
-                  z * p.targets.inv_tau;
-              ++at;
-              next = at < p.targets.top ? ids[at] - p.v0 : INT_MAX;
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(acc + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[c + j] = __uint_as_float(v[j]);
+        }
+        release();
+        bool ok = true;
+        for (int kb = u.kb0 + kSumSteps; kb < u.kb1; kb += kSumSteps) {
+          if (!(ok = arrived(acc))) break;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(acc + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
+          }
+          release();
+        }
+        if (!ok) break;
+        if (n0 >= p.V) continue;
+        float peak = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          const int n = n0 + c;
+          if (n >= p.V) continue;
+          while (__any_sync(0xffffffffu, e.id[0] < n + 32)) {
+            if (e.id[0] < n + 32) {
+              p.picked[(long long)r * p.targets.top + e.at] =
+                  pick(f + c, e.id[0] - n) * p.targets.inv_tau;
+              e.pass<false>();
             }
             __syncwarp();
           }
-          if (n + 32 > cols) {
+          if (n + 32 > p.V) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (n + j >= cols) f[j] = -INFINITY;
+              if (n + j >= p.V) f[c + j] = -INFINITY;
           }
-          float top4[4] = {f[0], f[1], f[2], f[3]};
+          float top4[4] = {f[c], f[c + 1], f[c + 2], f[c + 3]};
 #pragma unroll
-          for (int j = 4; j < 32; ++j) top4[j & 3] = fmaxf(top4[j & 3], f[j]);
-          const float here = fmaxf(fmaxf(top4[0], top4[1]),
-                                   fmaxf(top4[2], top4[3]));
+          for (int j = 4; j < 32; ++j)
+            top4[j & 3] = fmaxf(top4[j & 3], f[c + j]);
+          const float here =
+              fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           const float now = fmaxf(peak, here * c2);
           // a stretch of -Inf only: every term is 0, not exp(-Inf + Inf)
           const float ref = now == -INFINITY ? 0.f : now;
           float s4[4] = {sum * exp2_fast(peak - ref), 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            s4[j & 3] += exp2_fast(fmaf(f[j], c2, -ref));
+            s4[j & 3] += exp2_fast(fmaf(f[c + j], c2, -ref));
           sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
           peak = now;
-        } else {
-          if constexpr (PRODUCT == kVocabGrad) {
+        }
+        if (r < learnt)
+          p.stats[(long long)(u.tn * 2 + h) * p.T + r] =
+              make_float2(peak, sum);
+      }
+    } else {
+      // staging: row (lane) of 128 bytes, its 16-byte chunk j at j ^ (row
+      // mod 8), the layout a 128-byte-swizzle TMA store reads; two blocks,
+      // so that one is written while the other is stored
+      unsigned char* stg = smem + Sh::kOffStaging + (warp - 2) * kStagingBytes;
+      uint32_t stg_s = sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
+      auto other_block = [&]() {
+        const uint32_t flip = 4096;
+        stg = reinterpret_cast<unsigned char*>(
+            reinterpret_cast<uintptr_t>(stg) ^ flip);
+        stg_s ^= flip;
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+      };
+      const float inv_scale = header->inv_scale;
+      const bool dw_direct = p.dw != nullptr && header->dw_splits == 1;
+      const int slot_rows = (int)vocab_slot_rows(learnt);
+      while (walk.next(u)) {
+        const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
+        const int r = m0 + lane;
+        const int n0 = u.tn * kVocabTile + h * 128;
+        const int cols = u.kind == kGrad ? p.grad_n : p.D;
+        Entries e;
+        e.none();
+        float shift = 0.f, g = 0.f;
+        if (u.kind == kGrad && r < learnt) {
+          const long long t = learnt == p.T ? r : p.targets.token[r];
+          e.start<true>(p.targets, t, p.grad_v0 + n0);
+          shift = p.lse[t] * kLog2e;
+          g = p.grad_loss[t * p.grad_stride] * p.tau * header->scale;
+        }
+        const bool wide = u.kind == kDx || header->dw_splits > 1;  // fp32
+        uint32_t acc;
+        if (!arrived(acc)) break;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(acc + c0, v);
+          tmem_ld_wait();
+          if (c0 == 96) release();
+          const int n = n0 + c0;
+          if (n >= cols) continue;  // (after the release)
+          float f[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+          if (u.kind == kGrad) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               f[j] = exp2_fast(fmaf(f[j], c2, -shift));
-            while (__any_sync(0xffffffffu, next < n + 32)) {
-              if (next < n + 32) {
-                const float qj = expf(log_q[at]);
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (next == n + j) f[j] -= qj;
-                ++at;
-                next = at < p.targets.top ? ids[at] - p.v0 : INT_MAX;
-              }
-              __syncwarp();
-            }
             // rows past the learnt tokens are zeros: Dw sums over them up
             // to a multiple of 64
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = r < learnt ? f[j] * g : 0.f;
-          }
-          if constexpr (PRODUCT == kVocabDw) {
+          } else if (u.kb0 == u.kb1) {  // an empty sum
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              f[j] = nk > 0 ? f[j] * inv_scale : 0.f;
+            for (int j = 0; j < 32; ++j) f[j] = 0.f;
           }
-          if constexpr (PRODUCT == kVocabDx) {
-            if (w.kb0 == w.kb1) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) f[j] = 0.f;
-            }
+          if (u.kind != kGrad && wide) {
             // fp32, 32 columns: one staged block
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
+            other_block();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               *reinterpret_cast<float4*>(stg + lane * 128 +
@@ -551,27 +727,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                               f[4 * j + 3]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && m0 < learnt) {
-              if (p.add)
-                tma_add_3d(&map_c, stg_s, n, m0, w.split);
-              else
-                tma_store_3d(&map_c, stg_s, n, m0, w.split);
+            if (lane == 0) {
+              if (u.kind == kDx) {
+                if (m0 < learnt) {
+                  if (p.first)
+                    tma_store_2d(&maps.slots, stg_s, n,
+                                 u.slot * slot_rows + m0);
+                  else
+                    tma_add_2d(&maps.slots, stg_s, n,
+                               u.slot * slot_rows + m0);
+                }
+              } else if (m0 < p.back_n) {
+                tma_store_2d(&maps.dw_slots, stg_s, n,
+                             u.slot * p.dw_rows + m0);
+              }
               bulk_commit_group();
-            }
-          } else if (PRODUCT == kVocabDw && p.dw) {
-            if (r < rows) {
-              uint16_t* out = p.dw + (long long)r * p.lddw + n;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n + j < cols)
-                  out[j] = (uint16_t)pack16<AB_TYPE>(f[j], 0.f);
             }
           } else {
             // 16-bit, 64 columns: half a staged block at a time
-            if ((c0 & 32) == 0) {
-              if (lane == 0) bulk_wait_group_read<0>();
-              __syncwarp();
+            if (u.kind == kDw) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
             }
+            if ((c0 & 32) == 0) other_block();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int chunk = (c0 & 32) / 8 + j;
@@ -582,22 +760,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                              pack16<AB_TYPE>(f[8 * j + 4], f[8 * j + 5]),
                              pack16<AB_TYPE>(f[8 * j + 6], f[8 * j + 7]));
             }
+            if (u.kind == kGrad) {
+              // the row's targets in these columns: p - q, in their places
+              const int column = p.grad_v0 + n;
+              float share = 0.f;
+              while (__any_sync(0xffffffffu, e.id[0] < column + 32)) {
+                if (e.id[0] < column + 32) {
+                  const int c = e.id[0] - column;
+                  share += e.q[0];  // an id may come again
+                  e.pass<true>();
+                  if (e.id[0] != column + c) {
+                    const int chunk = (c0 & 32) / 8 + (c >> 3);
+                    *reinterpret_cast<uint16_t*>(
+                        stg + lane * 128 + ((chunk ^ (lane & 7)) << 4) +
+                        (c & 7) * 2) =
+                        (uint16_t)pack16<AB_TYPE>(pick(f, c) - g * share,
+                                                  0.f);
+                    share = 0.f;
+                  }
+                }
+                __syncwarp();
+              }
+            }
             // the block is whole, or its other half lies past the columns
             if ((c0 & 32) || n + 32 >= cols) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && m0 < store_rows) {
-                tma_store_2d(&map_c, stg_s, n - (c0 & 32), m0);
-                bulk_commit_group();
+              const int nb = n - (c0 & 32);
+              if (u.kind == kDw && dw_direct) {
+                // rows on any 2-byte boundary: a warp writes 64 columns of
+                // one row at a time
+                __syncwarp();
+                const int rows = min(32, p.back_n - m0);
+                for (int k = 0; k < rows; ++k) {
+                  const uint32_t two = *reinterpret_cast<const uint32_t*>(
+                      stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) +
+                      (lane & 3) * 4);
+                  uint16_t* to = p.dw +
+                                 (long long)(p.back_v0 + m0 + k) * p.lddw +
+                                 nb + 2 * lane;
+                  if (nb + 2 * lane + 1 < cols &&
+                      (reinterpret_cast<uintptr_t>(to) & 3u) == 0) {
+                    *reinterpret_cast<uint32_t*>(to) = two;
+                  } else {
+                    if (nb + 2 * lane < cols) to[0] = (uint16_t)two;
+                    if (nb + 2 * lane + 1 < cols)
+                      to[1] = (uint16_t)(two >> 16);
+                  }
+                }
+                __syncwarp();
+              } else {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  if (u.kind == kDw) {
+                    if (m0 < p.back_n)
+                      tma_store_2d(&maps.dw, stg_s, nb, p.back_v0 + m0);
+                  } else if (m0 < p.T) {
+                    tma_store_2d(&maps.g_out, stg_s, nb, m0);
+                  }
+                  bulk_commit_group();
+                }
               }
             }
           }
         }
       }
-      if (PRODUCT == kVocabStats && r < learnt && n0 < cols)
-        p.stats[(long long)(w.tn * 2 + h) * p.T + r] = make_float2(peak, sum);
+      if (lane == 0) bulk_wait_group<0>();
     }
-    if (Sh::kStaged && lane == 0) bulk_wait_group<0>();
   }
 
   griddep_launch_dependents();
@@ -611,118 +839,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A row-major 16-bit matrix (x contiguous), 64 × by boxes, 128-byte swizzle.
-bool encode_16(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m,
-               int type, const void* base, long long x, long long y,
-               long long ld, int by) {
+// A row-major matrix (x contiguous), 128-byte-wide boxes of `by` rows in the
+// 128-byte swizzle; elements outside read as zeros and are not written.
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int size,
+            const void* base, long long x, long long y, long long ld, int by) {
   const cuuint64_t dims[2] = {(cuuint64_t)x, (cuuint64_t)y};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)by};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * size)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)by};
   const cuuint32_t estr[2] = {1, 1};
-  return encode(m,
-                type == GEMM_F32_MIXED_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                2, const_cast<void*>(base), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tensor_map_encoder()(
+             m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int AB_TYPE, int PRODUCT>
+template <int AB_TYPE, bool FORWARD>
 cudaError_t launch(const VocabGemm& p, int sm_count, const WaitCfg& wc,
                    cudaStream_t stream) {
-  using Sh = Shape<PRODUCT>;
-  auto encode = tensor_map_encoder();
-  if (!encode) return cudaErrorNotSupported;
-  CUtensorMap a, b, xp, c;
-  std::memset(&c, 0, sizeof(c));
+  using Sh = Shape<FORWARD>;
+  if (!tensor_map_encoder()) return cudaErrorNotSupported;
+  const CUtensorMapDataType t16 = AB_TYPE == 1
+                                      ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapDataType t32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  Maps maps;
+  std::memset(&maps, 0, sizeof(maps));
   Args k = {};
-  k.T = p.T;
-  k.D = p.D;
-  k.n = p.n;
-  k.v0 = p.v0;
+  k.T = p.T, k.V = p.V, k.D = p.D;
   k.targets = p.targets;
-  k.stats = p.stats;
-  k.picked = p.picked;
-  k.lse = p.lse;
-  k.grad_loss = p.grad_loss;
-  k.grad_stride = p.grad_stride;
-  k.tau = p.tau;
-  k.add = p.add;
-  bool ok = true;
+  bool ok = encode(&maps.xp, t16, 2, p.Xp, p.D, p.rows_xp, p.ldxp, 64) &&
+            encode(&maps.w, t16, 2, p.W, p.D, p.V, p.ldw, 64);
   // X as given may have no tensor map (its alignment): then only the packed
   // copy is read
-  const bool x_fits = (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 &&
-                      p.ldx % 8 == 0;
-  auto encode_x = [&](CUtensorMap* as_given, int by) {
-    ok = ok && encode_16(encode, &xp, p.type, p.Xp, p.D, p.rows_xp, p.ldxp, by);
-    if (x_fits)
-      ok = ok && encode_16(encode, as_given, p.type, p.X, p.D, p.T, p.ldx, by);
-    else
-      *as_given = xp;
-  };
-  if (PRODUCT == kVocabStats || PRODUCT == kVocabGrad) {
-    encode_x(&a, kHalf);
-    ok = ok && encode_16(encode, &b, p.type, p.W, p.D, p.n, p.ldw, kHalf);
-    if (PRODUCT == kVocabGrad)
-      ok = ok && encode_16(encode, &c, p.type, p.G, p.n, p.T, p.ldg, 32);
-  } else if (PRODUCT == kVocabDx) {
-    ok = ok && encode_16(encode, &a, p.type, p.G, p.n, p.T, p.ldg, kHalf) &&
-         encode_16(encode, &b, p.type, p.W, p.D, p.n, p.ldw, kBK);
-    xp = a;
-    const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.T,
-                                (cuuint64_t)p.max_splits};
-    const cuuint64_t strides[2] = {(cuuint64_t)p.ld_slot * 4,
-                                   (cuuint64_t)p.ld_slot * 4 * p.T};
-    const cuuint32_t box[3] = {32, 32, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    ok = ok &&
-         encode(&c, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.slots, dims, strides,
-                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if ((reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.ldx % 8 == 0)
+    ok = ok && encode(&maps.x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
+  else
+    maps.x = maps.xp;
+  if (FORWARD) {
+    k.stats = p.stats, k.picked = p.picked;
   } else {
-    ok = ok && encode_16(encode, &a, p.type, p.G, p.n, p.T, p.ldg, kBK);
-    encode_x(&b, kBK);
-    if ((reinterpret_cast<uintptr_t>(p.dW) & 15u) == 0 && p.lddw % 8 == 0) {
-      ok = ok && encode_16(encode, &c, p.type, p.dW, p.D, p.n, p.lddw, 32);
-    } else {
-      k.dw = static_cast<uint16_t*>(p.dW);
-      k.lddw = p.lddw;
+    k.grad_v0 = p.grad.v0, k.grad_n = p.grad.n;
+    k.back_v0 = p.back.v0, k.back_n = p.back.n;
+    k.piece = p.piece, k.first = p.first;
+    k.lse = p.lse, k.grad_loss = p.grad_loss;
+    k.grad_stride = p.grad_stride, k.tau = p.tau;
+    k.dw_rows = (int)p.dw_slot_rows;
+    if (p.grad.n > 0)
+      ok = ok && encode(&maps.g_out, t16, 2, p.grad.G, p.grad.n, p.T, p.ldg,
+                        32);
+    if (p.back.n > 0) {
+      ok = ok &&
+           encode(&maps.g_in, t16, 2, p.back.G, p.back.n, p.T, p.ldg, 64) &&
+           encode(&maps.slots, t32, 4, p.slots, p.D, p.slot_rows, p.ld_slot,
+                  32);
+      if (p.dw_slots)
+        ok = ok && encode(&maps.dw_slots, t32, 4, p.dw_slots, p.D,
+                          p.dw_slot_rows * p.dw_max_splits, p.ld_slot, 32);
+      if ((reinterpret_cast<uintptr_t>(p.dW) & 15u) == 0 && p.lddw % 8 == 0) {
+        ok = ok && encode(&maps.dw, t16, 2, p.dW, p.D, p.V, p.lddw, 32);
+      } else {
+        k.dw = static_cast<uint16_t*>(p.dW);
+        k.lddw = p.lddw;
+      }
     }
   }
   if (!ok) return cudaErrorInvalidValue;
-  auto fn = vocab_gemm_kernel<AB_TYPE, PRODUCT>;
+  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD>;
   cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(fn), Sh::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(fn, dim3(2 * (sm_count / 2)), dim3(kThreads),
-                            Sh::kSmemBytes, stream, 2, a, b, xp, c, k, wc);
-}
-
-template <int PRODUCT>
-cudaError_t launch_typed(const VocabGemm& p, int sm_count, const WaitCfg& wc,
-                         cudaStream_t stream) {
-  return p.type == GEMM_F32_MIXED_BF16
-             ? launch<1, PRODUCT>(p, sm_count, wc, stream)
-             : launch<0, PRODUCT>(p, sm_count, wc, stream);
+  return launch_pdl_cluster(fn, dim3(2 * vocab_pairs(sm_count)),
+                            dim3(kThreads), Sh::kSmemBytes, stream, 2, maps,
+                            k, wc);
 }
 
 }  // namespace vocab
 
-cudaError_t launch_vocab_gemm(VocabProduct product, const VocabGemm& p,
-                              int sm_count, const WaitCfg& wc,
-                              cudaStream_t stream) {
-  switch (product) {
-    case kVocabStats:
-      return vocab::launch_typed<kVocabStats>(p, sm_count, wc, stream);
-    case kVocabGrad:
-      return vocab::launch_typed<kVocabGrad>(p, sm_count, wc, stream);
-    case kVocabDx:
-      return vocab::launch_typed<kVocabDx>(p, sm_count, wc, stream);
-    default:
-      return vocab::launch_typed<kVocabDw>(p, sm_count, wc, stream);
-  }
+cudaError_t launch_vocab_stats(const VocabGemm& p, int sm_count,
+                               const WaitCfg& wc, cudaStream_t stream) {
+  return p.type == GEMM_F32_MIXED_BF16
+             ? vocab::launch<1, true>(p, sm_count, wc, stream)
+             : vocab::launch<0, true>(p, sm_count, wc, stream);
+}
+
+cudaError_t launch_vocab_step(const VocabGemm& p, int sm_count,
+                              const WaitCfg& wc, cudaStream_t stream) {
+  return p.type == GEMM_F32_MIXED_BF16
+             ? vocab::launch<1, false>(p, sm_count, wc, stream)
+             : vocab::launch<0, false>(p, sm_count, wc, stream);
 }
 
 }  // namespace gemm_f32_impl

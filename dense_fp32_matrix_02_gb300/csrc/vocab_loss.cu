@@ -7,7 +7,7 @@
 //   loss_t = τ²·Σ_j q_tj·(log q_tj − (z[t][id_tj]/τ − lse_t)),
 //   dL/dz_t = g_t·τ·(p_t − q_t)
 // (cross entropy: q = 1, τ = 1).  A call runs
-//   1. the targets: entries sorted by id with log q; the tokens that are
+//   1. the targets: entries sorted by id with log q or q; the tokens that are
 //      learnt from, numbered (everything after works on those rows only);
 //   2. forward: the logits piece by piece, each reduced to per-row softmax
 //      statistics and the targets' logits; then loss and lse;
@@ -16,6 +16,7 @@
 //      of that piece).
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <type_traits>
 
 #include "gemm_f32.h"
@@ -26,16 +27,16 @@ namespace gemm_f32_impl {
 namespace {
 
 // ------------------------------------------------------------- targets
-// Distillation: one warp per token.  log q over the entries that count,
-// which are ranked by (id, place) and written in that order.
+// Distillation: one warp per token.  log q (forward) or q over the entries
+// that count, which are ranked by (id, place) and written in that order.
 constexpr int kTargetWarps = 4;
 
 __global__ void __launch_bounds__(32 * kTargetWarps)
     distill_targets_kernel(int T, int V, int top,
                            const float* __restrict__ logits, long long ldt,
                            const int64_t* __restrict__ top_ids, long long ldi,
-                           float inv_tau, int* __restrict__ ids,
-                           float* __restrict__ log_q,
+                           float inv_tau, int logs, int* __restrict__ ids,
+                           float* __restrict__ weights,
                            uint8_t* __restrict__ flags) {
   __shared__ int s_id[kTargetWarps][kVocabMaxTop];
   griddep_wait();
@@ -80,15 +81,15 @@ __global__ void __launch_bounds__(32 * kTargetWarps)
       for (int k = 0; k < top; ++k)
         rank += sid[k] < id || (sid[k] == id && k < j);
       ids[(long long)t * top + rank] = id;
-      log_q[(long long)t * top + rank] =
-          id == INT_MAX ? -INFINITY : (u[i] - peak) - log_sum;
+      const float log_q = (u[i] - peak) - log_sum;
+      weights[(long long)t * top + rank] = logs ? log_q : expf(log_q);
     }
   }
 }
 
 // Numbers the tokens that are learnt from, in order, and packs their rows of
 // X where they are not read in place (some token is not learnt from, or X
-// has no tensor map).  Every block numbers all tokens, 256 a warp at a time
+// has no tensor map); packs W's rows where they have no tensor map.  Every block numbers all tokens, 256 a warp at a time
 // (the flags come from L2; at 8192 tokens this took a single block followed
 // by a packing kernel 17 + 11 us), and writes what belongs to its own share
 // of them.  Forward: loss and lse of the other tokens are 0.  Gradients: the
@@ -108,19 +109,136 @@ struct NumberArgs {
   long long ldx;
   uint16_t* Xp;
   long long ldxp;
-  int D, piece, pairs, max_splits;
+  int D;
   int share;        // tokens of a block
+  const uint16_t* W;  // where it has no tensor map, else null
+  long long ldw;
+  uint16_t* Wp;
+  // gradients
+  int piece, pieces, pairs;
+  long long slot_rows;  // of dX's slots, all together
+  int dw_max_splits;
+  int* tile_slots;      // slots of each tile of dX
 };
 
+// The shares of dX's steps (VocabShare), a pair a thread: each pair's is what
+// its tiles of G and dW leave of an even total, in stretches that keep a
+// tile's slots within the room for them and no share under eight steps.  The
+// first `more_w` pairs have one tile of dW more than the others, the last
+// `more_g` one of G; so the pairs fall into three runs with one room each,
+// and everything has a closed form.  (All step counts are below 2^30: the
+// host checks.)
+struct Shares {
+  int line, left, cut;  // steps of a tile; of the line; of a stretch
+  int end0, end1;       // ends of the first and second run of pairs
+  int room0, room1, room2;
+  __device__ __forceinline__ int end(int p, int pairs) const {
+    // (to the pair's end, inclusive)
+    const int q = p + 1;
+    long long sum = (long long)min(q, end0) * room0 +
+                    (long long)max(0, min(q, end1) - end0) * room1 +
+                    (long long)max(0, q - end1) * room2;
+    if (sum >= left || q == pairs) return left;
+    const int x = (int)sum, tile = x / line, k = x - tile * line;
+    return tile * line + min(line, (k + cut / 2) / cut * cut);
+  }
+};
+
+__device__ void share_out(const NumberArgs& a, int learnt, int dw_splits,
+                          VocabHeader* header) {
+  const int p = threadIdx.x, pairs = a.pairs;
+  if (p >= pairs) return;
+  const int tiles = vocab_tiles(learnt) * vocab_tiles(a.D);
+  const int tall = vocab_tiles(a.piece), line = vocab_steps(a.piece);
+  const int tiles_w = tall * vocab_tiles(a.D) * dw_splits;
+  const int tiles_g = a.pieces > 1 ? vocab_tiles(learnt) * tall : 0;
+  const int cost_w = vocab_tile_cost(vocab_steps(learnt) / dw_splits);
+  const int cost_g = vocab_tile_cost(vocab_steps(a.D));
+  const int more_w = tiles_w % pairs, more_g = tiles_g % pairs;
+  const int base = tiles_w / pairs * cost_w + tiles_g / pairs * cost_g;
+  Shares s;
+  s.end0 = min(more_w, pairs - more_g);
+  s.end1 = max(more_w, pairs - more_g);
+  const bool both = more_w > pairs - more_g;
+  const int c0 = more_w ? cost_w : 0, c2 = more_g ? cost_g : 0;
+  const int c1 = both ? cost_w + cost_g : 0;
+  const int n0 = s.end0, n1 = s.end1 - s.end0, n2 = pairs - s.end1;
+  // the level over `base` at which the room under it holds all steps
+  const long long all = (long long)tiles * line;
+  int level = INT_MAX;
+#pragma unroll 1
+  for (int round = 0; round < 4; ++round) {
+    long long sum = all;
+    int count = 0;
+    if (n0 && c0 < level) sum += (long long)n0 * c0, count += n0;
+    if (n1 && c1 < level) sum += (long long)n1 * c1, count += n1;
+    if (n2 && c2 < level) sum += (long long)n2 * c2, count += n2;
+    const int now = (int)(((double)sum + count - 1) / count);
+    if (now >= level) break;
+    level = now;
+  }
+  s.room0 = max(0, level - c0);
+  s.room1 = max(0, level - c1);
+  s.room2 = max(0, level - c2);
+  // whole rounds: what the fullest pair has room for
+  int least = INT_MAX;
+  if (n0) least = s.room0;
+  if (n1) least = min(least, s.room1);
+  if (n2) least = min(least, s.room2);
+  const int rounds = min(least / line, tiles / pairs), whole = rounds * pairs;
+  s.room0 -= rounds * line;
+  s.room1 -= rounds * line;
+  s.room2 -= rounds * line;
+  s.line = line;
+  s.left = (tiles - whole) * line;
+  const int most = (int)max(
+      1ll, min(1ll << 30, a.slot_rows / vocab_slot_rows(learnt)));
+  s.cut = max((line + most - 1) / most, min(line, 8));
+  if (p == 0) header->dx_rounds = rounds;
+  for (int tile = p; tile < whole; tile += pairs) a.tile_slots[tile] = 1;
+  VocabShare sh;
+  sh.x0 = p ? s.end(p - 1, pairs) : 0;
+  sh.x1 = s.end(p, pairs);
+  sh.slot = 0;
+  if (sh.x1 > sh.x0) {
+    const int first = sh.x0 / line, start = first * line;
+    int next = sh.x0;  // the ends before this pair's, backwards
+#pragma unroll 1
+    for (int j = p - 1; j >= 0 && next > start; --j) {
+      const int begin = j ? s.end(j - 1, pairs) : 0;
+      sh.slot += next > begin;
+      next = begin;
+    }
+    // the tiles that end with this share
+    int slot = sh.slot;
+    for (int tile = first; (tile + 1) * line <= sh.x1; ++tile, slot = 0)
+      a.tile_slots[whole + tile] = slot + 1;
+  }
+  header->share[p] = sh;
+}
+
 // 16-bit row of n elements, then zeros up to a multiple of 8, to a 16-byte
-// aligned row; by one warp.  vec: the source is aligned too.
+// aligned row; by one warp.  vec: the source is 16-byte aligned too; else it
+// is read in the aligned 4-byte words that hold it (a word that lies partly
+// outside the row is read as single elements).
 __device__ __forceinline__ void pack_row(const uint16_t* __restrict__ src,
                                          int n, uint16_t* __restrict__ dst,
                                          bool vec, int lane) {
+  const int odd = (reinterpret_cast<uintptr_t>(src) >> 1) & 1;
   for (int c = 8 * lane; c < n; c += 256) {
     uint4 v;
     if (vec && c + 8 <= n) {
       v = *reinterpret_cast<const uint4*>(src + c);
+    } else if (c >= odd && c + 8 + odd <= n) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(src + c - odd);
+      const uint32_t a = w[0], b = w[1], d = w[2], e = w[3];
+      v = make_uint4(a, b, d, e);
+      if (odd) {
+        v.x = __funnelshift_r(a, b, 16);
+        v.y = __funnelshift_r(b, d, 16);
+        v.z = __funnelshift_r(d, e, 16);
+        v.w = __funnelshift_r(e, w[4], 16);
+      }
     } else {
       uint32_t e[8];
 #pragma unroll
@@ -134,13 +252,18 @@ __device__ __forceinline__ void pack_row(const uint16_t* __restrict__ src,
 
 __global__ void __launch_bounds__(1024)
     number_tokens_kernel(NumberArgs a, int* __restrict__ ids,
-                         float* __restrict__ log_q, int* __restrict__ token,
+                         float* __restrict__ weights, int* __restrict__ token,
                          int* __restrict__ row, VocabHeader* header) {
   __shared__ int s_count[32];
   __shared__ float s_max[32];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.W) {
+    const int warps = gridDim.x * 32;
+    for (long long v = blockIdx.x * 32 + warp; v < a.V; v += warps)
+      pack_row(a.W + v * a.ldw, a.D, a.Wp + v * a.ldxp, false, lane);
+  }
   const long long own0 = (long long)blockIdx.x * a.share;
   const long long own1 = min((long long)a.T, own0 + a.share);
   int base = 0;
@@ -178,7 +301,7 @@ __global__ void __launch_bounds__(1024)
         if (learnt) token[r] = (int)t;
         if (a.targets) {
           ids[t] = learnt ? (int)y[i] : INT_MAX;
-          log_q[t] = learnt ? 0.f : -INFINITY;
+          weights[t] = a.loss ? 0.f : 1.f;  // log q, or q
         }
         if (a.loss && !learnt) {
           a.loss[t] = 0.f;
@@ -227,23 +350,19 @@ __global__ void __launch_bounds__(1024)
       e = min(max(14 - ilogbf(most), -100), 100);
     header->learnt = base;
     header->packed = packed;
-    header->dx_splits = a.grad_loss ? vocab_dx_splits(base, a.D, a.piece,
-                                                      a.pairs, a.max_splits)
-                                    : 1;
     header->scale = ldexpf(1.f, e);
     header->inv_scale = ldexpf(1.f, -e);
   }
-}
-
-// W's rows where they have no tensor map, one warp a row.
-__global__ void __launch_bounds__(256)
-    pack_rows_kernel(const uint16_t* __restrict__ src, long long lds, int cols,
-                     uint16_t* __restrict__ dst, long long ldd, int rows) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warps = gridDim.x * 8;
-  for (long long r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps)
-    pack_row(src + r * lds, cols, dst + r * ldd, false, threadIdx.x & 31);
+  if (!a.grad_loss) return;
+  const int splits =
+      vocab_dw_splits(base, a.piece, a.D, a.pairs, a.dw_max_splits);
+  if (threadIdx.x == 0) header->dw_splits = splits;
+  if (base > 0) {
+    share_out(a, base, splits, header);
+  } else if (threadIdx.x < a.pairs) {
+    header->share[threadIdx.x] = VocabShare{0, 0, 0};
+    header->dx_rounds = 0;
+  }
 }
 
 // ------------------------------------------------------------- results
@@ -253,9 +372,9 @@ __device__ __forceinline__ float2 merge_stats(float2 a, float2 b) {
   return make_float2(m, a.y * exp2f(a.x - ref) + b.y * exp2f(b.x - ref));
 }
 
-// loss and lse of the learnt tokens: 8 rows a block, 128 threads a row that
-// share out its statistics (parts of them, [part][T]) and join them in a
-// fixed order.
+// loss and lse of the learnt tokens: 8 rows a block, blockDim / 8 threads a
+// row that share out its statistics (parts of them, [part][T]) and join them
+// in a fixed order.
 __global__ void __launch_bounds__(1024)
     finish_loss_kernel(VocabTargets tg, int T, int parts,
                        const float2* __restrict__ stats,
@@ -276,28 +395,31 @@ __global__ void __launch_bounds__(1024)
     t = tg.token[r];
     if (lane >> 3 < tg.top) {
       id = tg.ids[t * tg.top + (lane >> 3)];
-      lq = tg.log_q[t * tg.top + (lane >> 3)];
+      lq = tg.weights[t * tg.top + (lane >> 3)];
       at = picked[(long long)r * tg.top + (lane >> 3)];
     }
   }
   float2 st = make_float2(-INFINITY, 0.f);
   if (here) {
 #pragma unroll 4
-    for (int e = slice; e < parts; e += 128)
+    for (int e = slice; e < parts; e += blockDim.x >> 3)
       st = merge_stats(st, stats[(long long)e * T + r]);
   }
   for (int o = 8; o < 32; o <<= 1)
     st = merge_stats(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, o),
                                      __shfl_xor_sync(0xffffffffu, st.y, o)));
-  if (lane < 8) s_part[warp][lane] = st;
-  __syncthreads();
-  if (warp > 0) return;
-  st = make_float2(-INFINITY, 0.f);
-  for (int w = lane >> 3; w < 32; w += 4)
-    st = merge_stats(st, s_part[w][lane & 7]);
-  for (int o = 8; o < 32; o <<= 1)
-    st = merge_stats(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, o),
-                                     __shfl_xor_sync(0xffffffffu, st.y, o)));
+  const int warps = blockDim.x >> 5;
+  if (warps > 1) {
+    if (lane < 8) s_part[warp][lane] = st;
+    __syncthreads();
+    if (warp > 0) return;
+    st = make_float2(-INFINITY, 0.f);
+    for (int w = lane >> 3; w < warps; w += 4)
+      st = merge_stats(st, s_part[w][lane & 7]);
+    for (int o = 8; o < 32; o <<= 1)
+      st = merge_stats(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, o),
+                                       __shfl_xor_sync(0xffffffffu, st.y, o)));
+  }
   const float l = st.x * 0.69314718f + logf(st.y);
   float sum = 0.f;
   for (int j = lane >> 3; id != INT_MAX;) {
@@ -305,7 +427,7 @@ __global__ void __launch_bounds__(1024)
     j += 4;
     if (j >= tg.top) break;
     id = tg.ids[t * tg.top + j];
-    lq = tg.log_q[t * tg.top + j];
+    lq = tg.weights[t * tg.top + j];
     at = picked[(long long)r * tg.top + j];
   }
   for (int o = 8; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -315,31 +437,50 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dX row by row: the slots' sum in order, rounded; zeros for the tokens that
-// are not learnt from.  vec: four columns at a time (dX's rows are 8-byte
-// aligned).
+// dX, four columns a thread: the sum of its tiles' slots in order, rounded;
+// zeros for the tokens that are not learnt from.  vec: dX's rows are 8-byte
+// aligned.
 template <typename T16>
 __global__ void __launch_bounds__(256)
     finish_dx_kernel(int T, int D, const int* __restrict__ row,
-                     const VocabHeader* header,
+                     const VocabHeader* __restrict__ header,
+                     const int* __restrict__ tile_slots,
                      const float* __restrict__ slots, long long ld_slot,
                      T16* __restrict__ dX, long long lddx, int vec) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long t = blockIdx.x;
-  const int r = row[t], splits = header->dx_splits;
+  const int learnt = header->learnt;
   const float inv_scale = header->inv_scale;
-  const float* from = slots + (long long)r * ld_slot;
-  for (int i = 4 * threadIdx.x; i < D; i += 1024) {
+  const long long next = vocab_slot_rows(learnt) * ld_slot;
+  const int chunks = (int)(ld_slot / 4), wide = vocab_tiles(D);
+  const long long total = (long long)T * chunks;
+  for (long long k = blockIdx.x * 256ll + threadIdx.x; k < total;
+       k += gridDim.x * 256ll) {
+    const long long t = k / chunks;
+    const int i = (int)(k - t * chunks) * 4;
+    const int r = learnt == T ? (int)t : row[t];
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r >= 0) {
-      for (int s = 0; s < splits; ++s) {
-        const float4 a = *reinterpret_cast<const float4*>(
-            from + (long long)s * T * ld_slot + i);
-        v.x += a.x;
-        v.y += a.y;
-        v.z += a.z;
-        v.w += a.w;
+      // this tile's place in the order of the line (tile_coords)
+      const int tm = r / kVocabTile, group = tm / kVocabGroup * kVocabGroup;
+      const int high = min(vocab_tiles(learnt) - group, kVocabGroup);
+      const int n =
+          tile_slots[group * wide + i / kVocabTile * high + (tm - group)];
+      const float* from = slots + (long long)r * ld_slot + i;
+      for (int s0 = 0; s0 < n; s0 += 8) {
+        float4 a[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          a[s] = s0 + s < n ? *reinterpret_cast<const float4*>(
+                                  from + (s0 + s) * next)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          v.x += a[s].x;
+          v.y += a[s].y;
+          v.z += a[s].z;
+          v.w += a[s].w;
+        }
       }
     }
     T16 o[4];
@@ -355,6 +496,40 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < 4; ++j)
         if (i + j < D) to[j] = o[j];
     }
+  }
+}
+
+// A piece's rows of dW where they were summed in slots, rounded.
+template <typename T16>
+__global__ void __launch_bounds__(256)
+    finish_dw_kernel(int n, int D, const VocabHeader* __restrict__ header,
+                     const float* __restrict__ slots, long long slot_rows,
+                     long long ld_slot, T16* __restrict__ dW, long long lddw) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int splits = header->dw_splits;
+  if (splits == 1) return;
+  const float inv_scale = header->inv_scale;
+  const int chunks = (int)(ld_slot / 4);
+  for (long long k = blockIdx.x * 256ll + threadIdx.x;
+       k < (long long)n * chunks; k += gridDim.x * 256ll) {
+    const long long r = k / chunks;
+    const int i = (int)(k - r * chunks) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 a = *reinterpret_cast<const float4*>(
+          slots + (s * slot_rows + r) * ld_slot + i);
+      v.x += a.x;
+      v.y += a.y;
+      v.z += a.z;
+      v.w += a.w;
+    }
+    T16* to = dW + r * lddw + i;
+    const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < D) store16(to + j, o[j] * inv_scale);
   }
 }
 
@@ -392,17 +567,23 @@ int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // Where a call's state lies in its workspace, and the pieces of the
 // vocabulary the gradients go through.
 struct VocabLayout {
-  int64_t piece;       // columns of G
-  int64_t max_splits;  // slots of dX
-  int64_t ld_pack;     // row stride of the packed copies
-  int64_t header, token, row, flags, ids, log_q, x_pack, w_pack, total;
-  int64_t stats, picked;  // forward
-  int64_t g, slots;       // gradients
+  int64_t piece, pieces;  // columns of G
+  int64_t ld_pack;        // row stride of the packed copies
+  int64_t ld_slot;        // row stride of the fp32 slots
+  int64_t slot_rows;      // dX's slots, all together
+  int64_t dw_slot_rows, dw_max_splits;  // dW's; 1: none
+  int64_t header, token, row, flags, ids, weights, x_pack, w_pack, total;
+  int64_t stats, picked;                    // forward
+  int64_t g[2], tile_slots, slots, dw_slots;  // gradients
 };
 
 VocabLayout layout(int64_t T, int64_t V, int64_t D, int64_t top, bool grad,
                    bool pack_w) {
-  constexpr int64_t kMostG = 256ll << 20, kMostSlots = 512ll << 20;
+  int64_t kMostG = 128ll << 20;
+  if (const char* env = std::getenv("VOCAB_PIECE_MB"))
+    kMostG = (int64_t)std::atoi(env) << 20;
+  constexpr int64_t kMostSlots = 768ll << 20;
+  constexpr int64_t kMostDwSlots = 128ll << 20;
   VocabLayout l = {};
   const int64_t rows = std::max<int64_t>(T, 1);
   l.ld_pack = up(D, 8);
@@ -417,20 +598,34 @@ VocabLayout layout(int64_t T, int64_t V, int64_t D, int64_t top, bool grad,
   l.row = take(rows * 4);
   l.flags = take(rows);
   l.ids = take(rows * top * 4);
-  l.log_q = take(rows * top * 4);
+  l.weights = take(rows * top * 4);
   l.x_pack = take(up(rows, 64) * l.ld_pack * 2);
   if (pack_w) l.w_pack = take(V * l.ld_pack * 2);
   if (grad) {
     // equal pieces, whole tiles, of at most kMostG bytes of G
     const int64_t widest = std::max<int64_t>(
         kVocabTile, kMostG / (2 * rows) / kVocabTile * kVocabTile);
-    const int64_t pieces = (V + widest - 1) / widest;
-    l.piece = up((V + pieces - 1) / pieces, kVocabTile);
-    const int64_t slot = rows * up(D, 4) * 4;
-    l.max_splits = std::min<int64_t>(
-        64, std::max<int64_t>(1, kMostSlots / slot));
-    l.g = take(rows * l.piece * 2);
-    l.slots = take(l.max_splits * slot);
+    l.pieces = (V + widest - 1) / widest;
+    l.piece = up((V + l.pieces - 1) / l.pieces, kVocabTile);
+    l.pieces = (V + l.piece - 1) / l.piece;
+    l.ld_slot = up(D, 4);
+    const int64_t slot = up(rows, kVocabTile) * l.ld_slot * 4;
+    l.slot_rows = up(rows, kVocabTile) *
+                  std::min<int64_t>(kVocabMaxPairs,
+                                    std::max<int64_t>(1, kMostSlots / slot));
+    l.g[0] = take(rows * l.piece * 2);
+    l.g[1] = l.pieces > 1 ? take(rows * l.piece * 2) : l.g[0];
+    l.tile_slots = take((int64_t)vocab_tiles(rows) * vocab_tiles(D) * 4);
+    l.slots = take(l.slot_rows * l.ld_slot * 4);
+    l.dw_slot_rows = up(std::min(l.piece, V), 32);
+    l.dw_max_splits = 1;
+    if ((int64_t)vocab_tiles(l.piece) * vocab_tiles(D) < kVocabMaxPairs)
+      l.dw_max_splits = std::min<int64_t>(
+          kVocabMaxDwSplits,
+          std::max<int64_t>(
+              1, kMostDwSlots / (l.dw_slot_rows * l.ld_slot * 4)));
+    if (l.dw_max_splits > 1)
+      l.dw_slots = take(l.dw_max_splits * l.dw_slot_rows * l.ld_slot * 4);
   } else {
     l.stats = take((V + 127) / 128 * rows * 8);
     l.picked = take(rows * top * 4);
@@ -483,7 +678,7 @@ cudaError_t run_checked(const VocabCall& c, bool grad, int sms,
   int* token = reinterpret_cast<int*>(ws + l.token);
   int* row = reinterpret_cast<int*>(ws + l.row);
   int* ids = reinterpret_cast<int*>(ws + l.ids);
-  float* log_q = reinterpret_cast<float*>(ws + l.log_q);
+  float* weights = reinterpret_cast<float*>(ws + l.weights);
   const float inv_tau = 1.f / c.tau;
   cudaError_t e;
 
@@ -493,7 +688,7 @@ cudaError_t run_checked(const VocabCall& c, bool grad, int sms,
                    dim3((T + kTargetWarps - 1) / kTargetWarps),
                    dim3(32 * kTargetWarps), 0, s, T, V, top, c.top_logits,
                    (long long)c.ldt, c.top_ids, (long long)c.ldi, inv_tau,
-                   ids, log_q, flags);
+                   grad ? 0 : 1, ids, weights, flags);
     if (e != cudaSuccess) return e;
   }
   NumberArgs na = {};
@@ -506,21 +701,20 @@ cudaError_t run_checked(const VocabCall& c, bool grad, int sms,
   na.always_pack = !x_fits;
   na.X = static_cast<const uint16_t*>(c.X), na.ldx = c.ldx;
   na.Xp = reinterpret_cast<uint16_t*>(ws + l.x_pack), na.ldxp = l.ld_pack;
-  na.D = D, na.piece = (int)std::min(l.piece, c.V);
-  na.pairs = std::max(1, sms / 2), na.max_splits = (int)l.max_splits;
-  const int blocks = std::min(sms, (T + 31) / 32);
+  na.D = D;
+  na.piece = (int)std::min(l.piece, c.V), na.pieces = (int)l.pieces;
+  na.pairs = vocab_pairs(sms), na.slot_rows = l.slot_rows;
+  na.dw_max_splits = (int)l.dw_max_splits;
+  na.tile_slots = reinterpret_cast<int*>(ws + l.tile_slots);
+  if (!w_fits) {
+    na.W = static_cast<const uint16_t*>(c.W), na.ldw = c.ldw;
+    na.Wp = reinterpret_cast<uint16_t*>(ws + l.w_pack);
+  }
+  const int blocks = w_fits ? std::min(sms, (T + 31) / 32) : sms;
   na.share = (T + blocks - 1) / blocks;
   e = launch_pdl(number_tokens_kernel, dim3(blocks), dim3(1024), 0, s, na, ids,
-                 log_q, token, row, header);
+                 weights, token, row, header);
   if (e != cudaSuccess) return e;
-  if (!w_fits) {
-    e = launch_pdl(pack_rows_kernel, dim3(std::min(8 * sms, (V + 7) / 8)),
-                   dim3(256), 0, s, static_cast<const uint16_t*>(c.W),
-                   (long long)c.ldw, D,
-                   reinterpret_cast<uint16_t*>(ws + l.w_pack),
-                   (long long)l.ld_pack, V);
-    if (e != cudaSuccess) return e;
-  }
   const char* W = w_fits ? static_cast<const char*>(c.W) : ws + l.w_pack;
   const int64_t ldw = w_fits ? c.ldw : l.ld_pack;
 
@@ -530,39 +724,57 @@ cudaError_t run_checked(const VocabCall& c, bool grad, int sms,
   p.X = c.X, p.ldx = c.ldx;
   p.Xp = ws + l.x_pack, p.ldxp = l.ld_pack, p.rows_xp = (int)up(c.T, 64);
   p.W = W, p.ldw = ldw;
-  p.v0 = 0, p.n = V;
-  p.targets = VocabTargets{header, token, ids, log_q, top, inv_tau};
+  p.V = V;
+  p.targets = VocabTargets{header, token, ids, weights, top, inv_tau};
   if (!grad) {
     p.stats = reinterpret_cast<float2*>(ws + l.stats);
     p.picked = reinterpret_cast<float*>(ws + l.picked);
-    if ((e = launch_vocab_gemm(kVocabStats, p, sms, wc, s)) != cudaSuccess)
-      return e;
-    return launch_pdl(finish_loss_kernel, dim3((T + 7) / 8), dim3(1024), 0, s,
-                      p.targets, T, (V + 127) / 128, p.stats, p.picked, c.tau,
-                      c.loss, c.lse);
+    if ((e = launch_vocab_stats(p, sms, wc, s)) != cudaSuccess) return e;
+    // a thread's share of a row: about four statistics, in one warp's reach
+    // of 128 threads
+    const int parts = (V + 127) / 128;
+    const int threads = parts <= 16 ? 32 : parts <= 128 ? 256 : 1024;
+    return launch_pdl(finish_loss_kernel, dim3((T + 7) / 8), dim3(threads), 0,
+                      s, p.targets, T, parts, p.stats, p.picked, c.tau, c.loss,
+                      c.lse);
   }
-  p.G = ws + l.g, p.ldg = l.piece;
+  p.piece = na.piece, p.ldg = l.piece;
   p.lse = c.lse_in;
   p.grad_loss = c.grad_loss, p.grad_stride = c.grad_stride, p.tau = c.tau;
   p.slots = reinterpret_cast<float*>(ws + l.slots);
-  p.ld_slot = up(c.D, 4), p.max_splits = (int)l.max_splits;
-  p.lddw = c.lddw;
-  for (int64_t v0 = 0; v0 < c.V; v0 += l.piece) {
-    p.v0 = (int)v0, p.n = (int)std::min(l.piece, c.V - v0);
-    p.W = W + v0 * ldw * 2;
-    p.dW = static_cast<char*>(c.dW) + v0 * c.lddw * 2;
-    p.add = v0 > 0;
-    for (VocabProduct product : {kVocabGrad, kVocabDx, kVocabDw})
-      if ((e = launch_vocab_gemm(product, p, sms, wc, s)) != cudaSuccess)
-        return e;
-  }
-  const int vec = (reinterpret_cast<uintptr_t>(c.dX) & 7u) == 0 &&
-                  c.lddx % 4 == 0;
-  auto finish = [&](auto* dX) {
-    return launch_pdl(
-        finish_dx_kernel<std::remove_pointer_t<decltype(dX)>>, dim3(T),
-        dim3(256), 0, s, T, D, row, header, p.slots, p.ld_slot, dX,
-        (long long)c.lddx, vec);
+  p.slot_rows = l.slot_rows, p.ld_slot = l.ld_slot;
+  if (l.dw_max_splits > 1)
+    p.dw_slots = reinterpret_cast<float*>(ws + l.dw_slots);
+  p.dw_slot_rows = l.dw_slot_rows, p.dw_max_splits = (int)l.dw_max_splits;
+  p.dW = c.dW, p.lddw = c.lddw;
+  auto piece_at = [&](int64_t i) {
+    if (i < 0 || i >= l.pieces) return VocabPiece{0, 0, nullptr};
+    const int64_t v0 = i * l.piece;
+    return VocabPiece{(int)v0, (int)std::min(l.piece, c.V - v0),
+                      ws + l.g[i & 1]};
+  };
+  auto finish = [&](auto* dX) -> cudaError_t {
+    using T16 = std::remove_pointer_t<decltype(dX)>;
+    for (int64_t i = 0; i <= l.pieces; ++i) {
+      p.grad = piece_at(i), p.back = piece_at(i - 1);
+      p.first = i == 1;
+      if ((e = launch_vocab_step(p, sms, wc, s)) != cudaSuccess) return e;
+      if (i > 0 && p.dw_slots) {
+        e = launch_pdl(finish_dw_kernel<T16>, dim3(2 * sms), dim3(256), 0, s,
+                       p.back.n, D, header, p.dw_slots, p.dw_slot_rows,
+                       p.ld_slot,
+                       static_cast<T16*>(c.dW) + p.back.v0 * c.lddw,
+                       (long long)c.lddw);
+        if (e != cudaSuccess) return e;
+      }
+    }
+    const int vec = (reinterpret_cast<uintptr_t>(c.dX) & 7u) == 0 &&
+                    c.lddx % 4 == 0;
+    const int64_t groups = (c.T * (l.ld_slot / 4) + 255) / 256;
+    return launch_pdl(finish_dx_kernel<T16>,
+                      dim3((unsigned)std::min<int64_t>(groups, 8ll * sms)),
+                      dim3(256), 0, s, T, D, row, header, na.tile_slots, p.slots, p.ld_slot, dX,
+                      (long long)c.lddx, vec);
   };
   return c.type == GEMM_F32_MIXED_BF16
              ? finish(static_cast<__nv_bfloat16*>(c.dX))
@@ -575,6 +787,13 @@ int run_vocab(const VocabCall& c, bool grad, bool distill) {
   if (c.T == 0 && !grad) return GEMM_F32_OK;
   const VocabLayout l = layout(c.T, c.V, c.D, c.top, grad,
                                !fits_tensor_map(c.W, c.ldw));
+  // tiles, and all steps of a piece's products, are counted in 32 bits
+  const int64_t wide = up(c.D, kVocabTile) / kVocabTile;
+  const int64_t rows = up(c.T, kVocabTile) / kVocabTile;
+  if ((rows + l.piece) * wide > (1 << 30) ||
+      rows * wide * (l.piece / 64 + 1) > (1 << 30) ||
+      rows * (c.V / kVocabTile + 1) > (1 << 30))
+    return GEMM_F32_ERR_UNSUPPORTED;
   if (!c.ws || (reinterpret_cast<uintptr_t>(c.ws) & 15u) != 0 ||
       c.ws_bytes < l.total)
     return GEMM_F32_ERR_INVALID_ARG;
