@@ -1,6 +1,5 @@
-// What the vocabulary losses' kernels share: the targets as the kernels see
-// them, the state that a call keeps in its workspace, and the products'
-// launch interface.
+// What the vocabulary losses' kernels and their caller share: the call as
+// the kernels see it, where its state lies, and the counts they all make.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,12 +11,18 @@
 namespace gemm_f32_impl {
 
 constexpr int kVocabMaxTop = 256;
-constexpr int kVocabTile = 256;     // rows and columns of an output tile
+constexpr int kVocabTile = 256;      // rows and columns of an output tile
 constexpr int kVocabMaxPairs = 128;  // CTA pairs of a launch
 constexpr int kVocabMaxDwSplits = 16;
 constexpr int kVocabGroup = 16;  // tile rows walked together (L2 reuse)
 
-__host__ __device__ inline int vocab_pairs(int sm_count) {
+__host__ __device__ inline int vocab_tiles(long long n) {
+  return (int)((n + kVocabTile - 1) / kVocabTile);
+}
+__host__ __device__ inline int vocab_steps(long long n) {
+  return (int)((n + 63) / 64);
+}
+inline int vocab_pairs(int sm_count) {
   const int pairs = sm_count / 2;
   return pairs < 1 ? 1 : pairs > kVocabMaxPairs ? kVocabMaxPairs : pairs;
 }
@@ -34,114 +39,109 @@ struct VocabShare {
   int x0, x1, slot;
 };
 
-// Written by the first kernels of a call, read by the later ones.
+// Written by the numbering kernel, read by the later ones.
 struct VocabHeader {
   int learnt;       // tokens that are learnt from
   int packed;       // X is read from its packed copy
   float scale;      // gradients: G is stored times this power of two
   float inv_scale;  // 1 / scale
+  int wide;         // columns of a tile of the logits
+  int dw_wide;      // columns of a tile of dW
   int dw_splits;    // > 1: dW's tiles are summed in that many fp32 slots
   int dx_rounds;    // whole rounds of dX's tiles
   VocabShare share[kVocabMaxPairs];
 };
 
-// The target distributions.  Row t of ids and weights (top entries a row)
-// holds token t's entries that count, sorted by id, then INT_MAX, and log q
-// (forward) or q (gradients) of each.  Tokens that are learnt from are numbered in order: row r
-// of the products' matrices is token token[r].
-struct VocabTargets {
-  const VocabHeader* header;
-  const int* token;
-  const int* ids;
-  const float* weights;
-  int top;
-  float inv_tau;
-};
-
-__host__ __device__ inline int vocab_tiles(long long n) {
-  return (int)((n + kVocabTile - 1) / kVocabTile);
-}
-__host__ __device__ inline int vocab_steps(long long n) {
-  return (int)((n + 63) / 64);
-}
-// A tile's time in 64-deep steps: its own, or its epilogue's where that is
-// longer (about eight steps: 8 warps make 128 × 256 outputs per CTA).
-__host__ __device__ inline int vocab_tile_cost(int steps) {
-  return (steps > 8 ? steps : 8) + 1;
-}
-// Rows between two slots of dX.
-__host__ __device__ inline long long vocab_slot_rows(int learnt) {
-  return (long long)vocab_tiles(learnt) * kVocabTile;
-}
-// Slots that dW's tiles are summed in: 1 (none: dW is written at once)
-// unless so few tiles are left to the pairs that one tile's depth outlasts
-// the whole piece's even share by a quarter.
-__host__ __device__ inline int vocab_dw_splits(int learnt, int n, int D,
-                                               int pairs, int most) {
-  const long long tw = (long long)vocab_tiles(n) * vocab_tiles(D);
-  const long long tx = (long long)vocab_tiles(learnt) * vocab_tiles(D);
-  const long long depth = vocab_steps(learnt);
-  const long long even =
-      (tw * depth + tx * vocab_steps(n) + pairs - 1) / pairs + 1;
-  if (4 * depth <= 5 * even || tw >= pairs) return 1;
-  long long s = (depth + even - 1) / even;
-  if (s > depth / 4) s = depth / 4;
-  if (s > most) s = most;
-  return s > 1 ? (int)s : 1;
+// Columns of a tile: 256, or less where there are so few tiles that more and
+// narrower ones end sooner.  A 64-deep step takes about 8, 5 and 4 units for
+// 256, 128 and 64 columns (below 256 the operands' loads bound it), and the
+// epilogue of a tile about as long as 8 steps of it; it follows the last
+// tile.
+__host__ __device__ inline int vocab_tile_width(int rows, int cols, int steps,
+                                                int narrowest, int pairs) {
+  const int tall = vocab_tiles(rows);
+  int best = kVocabTile, best_time = INT_MAX;
+  if ((long long)tall * vocab_tiles(cols) > 2 * pairs) return best;
+  for (int wide = 256, step = 8, last = 64; wide >= narrowest;
+       wide >>= 1, step = step == 8 ? 5 : 4, last >>= 1) {
+    const int rounds = (tall * ((cols + wide - 1) / wide) + pairs - 1) / pairs;
+    const int one = steps * step > last ? steps * step : last;
+    const int time = rounds * one + last;
+    if (time < best_time) best = wide, best_time = time;
+  }
+  return best;
 }
 
-// The products of the vocabulary losses, with what their epilogues make:
-//   forward: logits X·Wᵀ -> per row and 128 columns the softmax statistics;
-//     the targets' logits;
-//   gradients, one launch: G of piece `grad` (logits made again, 16-bit) and
-//     from G of piece `back` its rows of dW = Gᵀ·X and its share of
-//     dX += G·W.  Either piece may be absent (n = 0).
-struct VocabPiece {
-  int v0, n;  // columns v0 .. v0 + n of the logits
-  void* G;    // [T][ldg]
-};
-struct VocabGemm {
-  int type;       // gemm_f32_mixed_type
+// One call.  Tokens that are learnt from are numbered in order: row r of the
+// products' matrices is token token[r], and row[t] is r or -1.
+struct VocabCall {
+  int type;  // gemm_f32_mixed_type
   int T, V, D;
-  const void* X;  // as given; read where header->packed is 0
+  const void* X;
   long long ldx;
-  const void* Xp;  // packed: rows of the learnt tokens, then zero rows up
-  long long ldxp;  // to a multiple of 64
-  int rows_xp;
   const void* W;
   long long ldw;
-  VocabTargets targets;
+  float tau, inv_tau;
+  // cross entropy: one target a token; else null
+  const int64_t* targets;
+  // distillation
+  int top;
+  const float* top_logits;
+  long long ldt;
+  const int64_t* top_ids;
+  long long ldi;
   // forward
-  float2* stats;  // [columns / 128][T]: (max, sum) in powers of 2
-  float* picked;  // [T][top]: logits / τ of the entries
+  float *loss, *lse_out;
   // gradients
-  VocabPiece grad, back;
-  int piece;      // columns of a whole piece
-  int first;      // back is the first piece: dX's slots start from it
-  long long ldg;
   const float* lse;
   const float* grad_loss;
   long long grad_stride;
-  float tau;
-  float* slots;   // dX: [slot_rows][ld_slot]
-  long long slot_rows, ld_slot;
-  float* dw_slots;  // [dw_max_splits · dw_slot_rows][ld_slot], or null
-  long long dw_slot_rows;
-  int dw_max_splits;
+  void* dX;
+  long long lddx;
   void* dW;
   long long lddw;
+
+  int pairs;  // CTA pairs of the products
+  int wide;   // columns of the logits' tiles if all tokens are learnt from
+
+  // ---- workspace
+  VocabHeader* header;   // null: nothing is numbered or packed, row t is
+  int *token, *row;      // token t (forward, one row of tiles)
+  uint8_t* learnt_flag;  // distillation: whether anything of a token counts
+  int* ids;              // distillation [T][top]: entries that count, by id,
+  float* weights;        // then INT_MAX; log q (forward) or q of each
+  void* Xp;              // X's packed copy: the learnt tokens' rows, then
+  long long ldxp;        // zero rows up to a multiple of 64
+  void* Wp;              // W's packed copy, or null (W has a tensor map)
+  // forward
+  float2* stats;  // [half tiles' columns][learnt]: (max, sum), powers of 2
+  float* picked;  // [T][top]: logits / τ of the entries
+  // gradients
+  int piece, pieces;  // columns of G; the pieces of the vocabulary
+  void* G;            // [2 · g_rows][piece]: two pieces' G in turn
+  int g_rows;
+  int* tile_slots;    // slots of each tile of dX, in the order of the walk
+  float* slots;       // dX: [slot_rows][ld_slot]
+  long long slot_rows, ld_slot;
+  float* dw_slots;    // [dw_max_splits · dw_slot_rows][ld_slot], or null
+  int dw_slot_rows, dw_max_splits;
 };
 
-cudaError_t launch_vocab_stats(const VocabGemm& p, int sm_count,
-                               const WaitCfg& wc, cudaStream_t stream);
-cudaError_t launch_vocab_step(const VocabGemm& p, int sm_count,
-                              const WaitCfg& wc, cudaStream_t stream);
+// The products of a call (vocab_gemm.cu): its tensor maps, made once, and
+// one launch each.
+cudaError_t vocab_forward(const VocabCall& c, const WaitCfg& wc,
+                          cudaStream_t stream);
+cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
+                            cudaStream_t stream);
 
-__device__ __forceinline__ void store16(__nv_bfloat16* p, float v) {
-  *p = __float2bfloat16_rn(v);
+__device__ __forceinline__ bool vocab_maps(const void* p, long long ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
 }
-__device__ __forceinline__ void store16(__half* p, float v) {
-  *p = __float2half_rn(v);
+__device__ __forceinline__ bool vocab_is_learnt(const VocabCall& c,
+                                                long long t) {
+  if (!c.targets) return c.learnt_flag[t] != 0;
+  const int64_t y = c.targets[t];
+  return y >= 0 && y < c.V;
 }
 
 }  // namespace gemm_f32_impl

@@ -1,15 +1,21 @@
-// The products of the vocabulary losses on the 5th-generation tensor cores,
-// one kernel whose epilogue makes what the losses need of each 256 × 256
-// tile, so that no logits are stored:
-//   Stats  z = X·Wᵀ:  per row and 128 columns max and Σ exp, and the logits
-//          of the row's targets;
+// The products of the vocabulary losses (vocab_loss.cu has the formulas) on
+// the 5th-generation tensor cores: one kernel whose epilogue makes what the
+// losses need of each 256 × 256 tile, so that no logits are stored:
+//   Stats  z = X·Wᵀ:  per row and half tile max and Σ exp, and the logits of
+//          the row's targets;
 //   Grad   z = X·W_pᵀ: G = g·τ·(exp(z/τ − lse) − q), rounded to 16 bits;
 //   Dw     Gᵀ·X, rounded to 16 bits (or, few tiles, into fp32 slots);
 //   Dx     G·W_p, added into fp32 slots.
 // Stats is the forward launch.  The gradients take one launch per piece of
-// the vocabulary, which makes Grad of one piece beside Dw and Dx of the one
-// before: they do not depend on each other, and the depth of Dx is cut so
-// that every pair of CTAs ends at the same time (VocabShare).
+// the vocabulary and one more, each of which makes Grad of one piece beside
+// Dw and Dx of the one before: they do not depend on each other, and the
+// depth of Dx is cut so that every pair of CTAs ends at the same time
+// (VocabShare).  One cooperative launch for everything, with grid barriers
+// between the phases, was measured against this: it saves the host about
+// 4 us a launch, but the phases that are not products run on 320 threads an
+// SM, and nothing of a launch overlaps the one before (777 × 9973 × 521
+// distillation step 124 us against 98, 2048 × 50021 × 768 forward 140
+// against 124).
 //
 // Persistent clusters of two CTAs, one pair per two SMs, walk the tiles.  A
 // pair works on one tile by tcgen05.mma.cta_group::2 (M 256, N 256, K 16):
@@ -47,7 +53,7 @@ constexpr int kPartBytes = kHalf * kBK * 2;  // 16 KB: one operand, one stage
 constexpr int kStageBytes = 2 * kPartBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kStagingBytes = 2 * 4096;      // one epilogue warp's two blocks
+constexpr int kStagingBytes = 4096;          // one epilogue warp's block
 constexpr int kTmemCols = 512;
 constexpr long long kDrainNs = 2000000000LL;
 constexpr uint32_t kSleepNs = 100000;
@@ -62,7 +68,7 @@ enum Kind { kStats, kGrad, kDw, kDx };
 
 template <bool FORWARD>
 struct Shape {
-  static constexpr int kStages = FORWARD ? 7 : 5;
+  static constexpr int kStages = FORWARD ? 7 : 6;
   static constexpr int kOffStaging = kStages * kStageBytes;
   static constexpr int kOffCtl =
       kOffStaging + (FORWARD ? 0 : kEpiWarps * kStagingBytes);
@@ -199,40 +205,26 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// What the kernel needs beside the tensor maps.
-struct Args {
-  int T, V, D;
-  VocabTargets targets;
-  float2* stats;
-  float* picked;
-  int grad_v0, grad_n, back_v0, back_n, piece, first;
-  const float* lse;
-  const float* grad_loss;
-  long long grad_stride;
-  float tau;
-  int dw_rows;    // rows between two slots of dW
-  uint16_t* dw;   // dW where it has no tensor map, else null
-  long long lddw;
-};
 
 struct Maps {
-  CUtensorMap x, xp, w;  // operands, 64 × 64 boxes
-  CUtensorMap g_out;     // Grad's G, 64 × 32
-  CUtensorMap g_in;      // Dw's and Dx's G, 64 × 64
-  CUtensorMap dw;        // 64 × 32
+  CUtensorMap x, xp, w;     // operands, 64 × 64 boxes
+  CUtensorMap g_in, g_out;  // G: 64 × 64, 64 × 32
+  CUtensorMap dw;           // 64 × 32
   CUtensorMap slots, dw_slots;  // fp32, 32 × 32
 };
 
+// ------------------------------------------------------------- the walk
 // One sum of a pair: a tile (or, Dx and split Dw, a share of its depth).
 struct Unit {
   int kind;
-  int tm, tn;
+  int tm, tn, wide;  // wide: the tile's columns
   int kb0, kb1;
   int slot;
 };
 
-// The walk of one pair over its units.  Gradients: dW and dX of the piece
-// before, whose G the last launch has just written, then Grad.
+// The walk of one pair over its units of a launch.  Gradients, launch i: dW
+// and dX of piece i - 1, whose G the last launch has just written, then Grad
+// of piece i.
 template <bool FORWARD>
 struct Walk {
   int stage, j, pair, pairs;
@@ -240,25 +232,37 @@ struct Walk {
   int dw_m, dw_n, dw_steps, splits;  // Dw
   int dx_m, dx_n, dx_steps, line;    // Dx; line: a whole piece's steps
   int whole, x, x1, slot;            // whole: tiles before the line's
+  int grad_v0, grad_n, back_v0, back_n;
+  int wide, dw_wide;
 
-  __device__ __forceinline__ Walk(const Args& p, const VocabHeader* h,
+  __device__ __forceinline__ Walk(const VocabCall& p, int learnt, int phase,
                                   int pair_, int pairs_)
       : stage(FORWARD ? 3 : 0), j(pair_), pair(pair_), pairs(pairs_) {
-    const int learnt = h->learnt;
+    const VocabHeader* h = p.header;
+    grad_v0 = phase * p.piece;
+    grad_n = phase < p.pieces ? min(p.piece, p.V - grad_v0) : 0;
+    back_v0 = grad_v0 - p.piece;
+    back_n = phase > 0 ? min(p.piece, p.V - back_v0) : 0;
     tiles_m = vocab_tiles(learnt);
-    tiles_n = vocab_tiles(FORWARD ? p.V : p.grad_n);
+    wide = h ? h->wide : p.wide;
+    tiles_n = ((FORWARD ? p.V : grad_n) + wide - 1) / wide;
     steps = vocab_steps(p.D);
-    if (!FORWARD) {
-      dx_n = dw_n = vocab_tiles(p.D);
-      dw_m = vocab_tiles(p.back_n);
+    if (!FORWARD && phase == 0) {
+      stage = 3;
+      j = pairs - 1 - pair;
+    } else if (!FORWARD) {
+      dx_n = vocab_tiles(p.D);
+      dw_wide = h->dw_wide;
+      dw_n = (p.D + dw_wide - 1) / dw_wide;
+      dw_m = vocab_tiles(back_n);
       dw_steps = vocab_steps(learnt);
       splits = h->dw_splits;
-      dx_m = p.back_n > 0 ? tiles_m : 0;
-      dx_steps = vocab_steps(p.back_n);
+      dx_m = tiles_m;
+      dx_steps = vocab_steps(back_n);
       line = vocab_steps(p.piece);
       whole = h->dx_rounds * pairs;
       x = h->share[pair].x0;
-      x1 = p.back_n > 0 ? h->share[pair].x1 : x;
+      x1 = h->share[pair].x1;
       slot = h->share[pair].slot;
     }
   }
@@ -268,10 +272,12 @@ struct Walk {
       const int tiles = dw_m * dw_n;
       if (j < tiles * splits) {
         u.kind = kDw;
+        u.wide = dw_wide;
         u.slot = j / tiles;
         tile_coords<kVocabGroup>(j - u.slot * tiles, dw_m, dw_n, u.tm, u.tn);
-        u.kb0 = (int)((long long)dw_steps * u.slot / splits);
-        u.kb1 = (int)((long long)dw_steps * (u.slot + 1) / splits);
+        // (a depth of below 2^25 steps, 16 splits at most)
+        u.kb0 = dw_steps * u.slot / splits;
+        u.kb1 = dw_steps * (u.slot + 1) / splits;
         j += pairs;
         return true;
       }
@@ -281,6 +287,7 @@ struct Walk {
     if (stage == 1) {
       if (j < whole && j < dx_m * dx_n) {
         u.kind = kDx;
+        u.wide = kVocabTile;
         tile_coords<kVocabGroup>(j, dx_m, dx_n, u.tm, u.tn);
         u.kb0 = 0;
         u.kb1 = dx_steps;
@@ -295,10 +302,15 @@ struct Walk {
         const int tile = x / line;
         const int end = min(x1, (tile + 1) * line);
         u.kind = kDx;
+        u.wide = kVocabTile;
         tile_coords<kVocabGroup>(whole + tile, dx_m, dx_n, u.tm, u.tn);
         // a shorter last piece is cut in proportion
-        u.kb0 = (int)((long long)(x - tile * line) * dx_steps / line);
-        u.kb1 = (int)((long long)(end - tile * line) * dx_steps / line);
+        u.kb0 = x - tile * line;
+        u.kb1 = end - tile * line;
+        if (dx_steps != line) {
+          u.kb0 = (int)((long long)u.kb0 * dx_steps / line);
+          u.kb1 = (int)((long long)u.kb1 * dx_steps / line);
+        }
         u.slot = slot;
         slot = 0;
         x = end;
@@ -311,6 +323,7 @@ struct Walk {
     }
     if (j >= tiles_m * tiles_n) return false;
     u.kind = FORWARD ? kStats : kGrad;
+    u.wide = wide;
     tile_coords<kVocabGroup>(j, tiles_m, tiles_n, u.tm, u.tn);
     u.kb0 = 0;
     u.kb1 = steps;
@@ -335,11 +348,20 @@ struct Entries {
     for (int i = 0; i < 4; ++i) id[i] = INT_MAX;
   }
   template <bool WEIGHTS>
-  __device__ __forceinline__ void start(const VocabTargets& tg, long long t,
+  __device__ __forceinline__ void start(const VocabCall& p, long long t,
                                         int column) {
-    ids = tg.ids + t * tg.top;
-    weights = tg.weights + t * tg.top;
-    top = tg.top;
+    if (p.targets) {  // one entry of weight 1
+      const int y = (int)p.targets[t];
+      at = y < column;
+      top = 1;
+      id[0] = at ? INT_MAX : y;
+      id[1] = id[2] = id[3] = INT_MAX;
+      q[0] = 1.f;
+      return;
+    }
+    ids = p.ids + t * p.top;
+    weights = p.weights + t * p.top;
+    top = p.top;
     // the first with id >= column: eight-way steps, as each costs the
     // latency of its loads
     int lo = 0;
@@ -390,10 +412,11 @@ __device__ __forceinline__ float pick(const float* f, int i) {
   return (i & 1) ? d1 : d0;
 }
 
+
 template <int AB_TYPE, bool FORWARD>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Maps maps,
-                      const __grid_constant__ Args p,
+                      const __grid_constant__ VocabCall p, const int phase,
                       const __grid_constant__ WaitCfg wc) {
   using Sh = Shape<FORWARD>;
   using Control = typename Sh::Control;
@@ -430,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&maps.x);
     prefetch_tmap(&maps.w);
+    if (!FORWARD) prefetch_tmap(&maps.g_in);
   }
   if (warp == 1) {
     tmem_alloc2(smem_u32(&ctl->tmem_base), kTmemCols);
@@ -440,30 +464,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // the other CTA's barriers are initialised
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
+
   griddep_wait();  // everything read or written may belong to the kernel before
 
-  const VocabHeader* header = p.targets.header;
-  const int learnt = header->learnt;
-  Walk<FORWARD> walk(p, header, pair, pairs);
+  const VocabHeader* header = p.header;
+  const int learnt = header ? header->learnt : p.T;
+  Walk<FORWARD> walk(p, learnt, phase, pair, pairs);
   Unit u;
-
+  int it = 0, i = 0;  // steps and sums so far
+  bool ok = true;
+  // G of this piece, and of the one before
+  const int g_out = (phase & 1) * p.g_rows, g_in = p.g_rows - g_out;
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ---------------------------------------------------------- producer
     if (lane == 0 && !(wc.debug & kDebugStallProducer)) {
-      const void* mx = header->packed ? &maps.xp : &maps.x;
-      int it = 0;
+      const void* mx =
+          header && header->packed ? &maps.xp : &maps.x;
       while (!*abort && walk.next(u)) {
         const int m0 = u.tm * kVocabTile + (int)rank * kHalf;
-        const int n0 = u.tn * kVocabTile + (int)rank * kHalf;
+        const int n0 = u.tn * u.wide + (int)rank * (u.wide >> 1);
+        // B: one box of 64 columns is enough below 256
+        const bool two = u.wide == kVocabTile;
+        const int bytes = two ? 2 * kStageBytes
+                              : 2 * (kStageBytes - kPartBytes / 2);
         // operands K-major: x along the depth; else x along the tile
-        const bool mn_a = u.kind == kDw, mn_b = u.kind == kDw || u.kind == kDx;
+        const bool mn_a = u.kind == kDw;
+        const bool mn_b = u.kind == kDw || u.kind == kDx;
         const void* ma = u.kind == kStats || u.kind == kGrad
                              ? mx
                              : (const void*)&maps.g_in;
         const void* mb = u.kind == kDw ? mx : (const void*)&maps.w;
-        // W's rows: the piece's, or the piece's along the depth
-        const int bn = u.kind == kGrad ? p.grad_v0 + n0 : n0;
-        const int bk = u.kind == kDx ? p.back_v0 : 0;
+        // rows of G start at g_in, W's at the piece's first column
+        const int am = u.kind == kDx ? g_in + m0 : m0;
+        const int ak = u.kind == kDw ? g_in : 0;
+        const int bn = u.kind == kGrad ? walk.grad_v0 + n0 : n0;
+        const int bk = u.kind == kDx ? walk.back_v0 : 0;
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           const int s = it % kStages;
           if (it >= kStages &&
@@ -473,42 +508,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             record_status(wc.status, kStatusTimeoutEmpty);
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
           const uint32_t bar = cluster_map(full(s), 0);
           const uint32_t a = sbase + s * kStageBytes, b = a + kPartBytes;
           const int k = kb * kBK;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            tma_load2_2d(a + i * (kPartBytes / 2), ma, bar,
-                         mn_a ? m0 + 64 * i : k, mn_a ? k : m0 + 64 * i);
-            tma_load2_2d(b + i * (kPartBytes / 2), mb, bar,
-                         mn_b ? bn + 64 * i : k, mn_b ? bk + k : bn + 64 * i);
+          for (int h = 0; h < 2; ++h) {
+            tma_load2_2d(a + h * (kPartBytes / 2), ma, bar,
+                         mn_a ? m0 + 64 * h : k, mn_a ? ak + k : am + 64 * h);
+            if (h == 0 || two)
+              tma_load2_2d(b + h * (kPartBytes / 2), mb, bar,
+                           mn_b ? bn + 64 * h : k,
+                           mn_b ? bk + k : bn + 64 * h);
           }
           ++it;
         }
       }
-      if (*abort && rank == 0) {  // let the copies still in flight land
-        for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
-          if (!bounded_wait(full(k % kStages), (k / kStages) & 1, kDrainNs,
-                            nullptr, 0))
-            record_status(wc.status, kStatusTimeoutDrain);
-      }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank != 0) {
-      // the last arrival from the first CTA's products: nothing of the pair
-      // still signals this CTA when it leaves
-      if (!wait_cluster(mma_done, 0, 2 * wc.limit + kDrainNs, nullptr))
-        record_status(wc.status, kStatusTimeoutDrain);
-    }
+    // -------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
-      int it = 0, i = 0;  // steps; sums
-      bool ok = true;
       while (ok && walk.next(u)) {
-        const bool mn_a = u.kind == kDw, mn_b = u.kind == kDw || u.kind == kDx;
+        const bool mn_a = u.kind == kDw;
+        const bool mn_b = u.kind == kDw || u.kind == kDx;
         const uint32_t idesc =
-            idesc_f16(256, 256, AB_TYPE, mn_b) | (mn_a ? 1u << 15 : 0u);
+            idesc_f16(256, u.wide, AB_TYPE, mn_b) | (mn_a ? 1u << 15 : 0u);
         // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes else
         const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
         int kb = u.kb0;
@@ -527,14 +551,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d_tmem = tmem + b * 256;
           for (const int k0 = kb; kb < end; ++kb, ++it) {
             const int s = it % kStages;
-            if (!wait_cluster(full(s), (it / kStages) & 1, wc.limit, abort)) {
+            if (!wait_cluster(full(s), (it / kStages) & 1, wc.limit,
+                              abort)) {
               *abort = 1;
               record_status(wc.status, kStatusTimeoutFull);
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const uint32_t a0 = sbase + s * kStageBytes, b0 = a0 + kPartBytes;
+            const uint32_t a0 = sbase + s * kStageBytes;
+            const uint32_t b0 = a0 + kPartBytes;
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
               mma2_f16_ss(d_tmem,
@@ -549,27 +575,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++i;
         } while (ok && kb < u.kb1);
       }
-      // no MMA may still run when TMEM is freed at the end
-      tc_commit2(mma_done);
-      if (!wait_cluster(mma_done, 0, kDrainNs, nullptr))
-        record_status(wc.status, kStatusTimeoutDrain);
     }
   } else {
-    // ------------------------------------------------------------ epilogue
+    // ---------------------------------------------------------- epilogue
     const int q = warp & 3;         // TMEM lane quarter
     const int h = (warp - 2) >> 2;  // column half
-    const uint32_t my_tmem =
-        tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
-    const float c2 = p.targets.inv_tau * kLog2e;
-    int i = 0;  // sums
+    const uint32_t my_tmem = tmem + ((uint32_t)(q * 32) << 16);
+    const float c2 = p.inv_tau * kLog2e;
     // waits for the next sum; its accumulator's address
     auto arrived = [&](uint32_t& acc) -> bool {
       const int b = i & 1;
-      const bool ok =
-          bounded_wait(acc_full(b), (i >> 1) & 1, wc.limit, abort, kSleepNs);
-      if (!__all_sync(0xffffffffu, ok)) {
+      const bool here = ok && bounded_wait(acc_full(b), (i >> 1) & 1,
+                                           wc.limit, abort, kSleepNs);
+      if (!__all_sync(0xffffffffu, here)) {
         *abort = 1;
-        if (lane == 0) record_status(wc.status, kStatusTimeoutMma);
+        if (ok && lane == 0) record_status(wc.status, kStatusTimeoutMma);
+        ok = false;
         return false;
       }
       tc_fence_after_sync();
@@ -584,52 +605,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++i;
     };
 
+    // The first pass is a dry run, on whatever TMEM holds and
+    // with nothing stored: it brings the instructions in while the first
+    // tile is being made (which they otherwise hold up by 2-3 us).
+    bool first_pass = true;
     if constexpr (FORWARD) {
-      while (walk.next(u)) {
+      for (;; first_pass = false) {
+        if (first_pass)
+          u = {kStats, 1 << 20, 0, 64, 0, 0, 0};
+        else if (!walk.next(u))
+          break;
         const int r = u.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
-        const int n0 = u.tn * kVocabTile + h * 128;
+        const int half = u.wide >> 1;  // this warp's columns
+        const int n0 = u.tn * u.wide + h * half;
+        uint32_t acc = my_tmem;
+        const bool several = u.kb1 - u.kb0 > kSumSteps;
+        if (several) {
+          // several sums: added here, and put in the last one's place
+          if (!arrived(acc)) break;
+          acc += h * half;
+          float f[128];
+#pragma unroll
+          for (int c = 0; c < 128; ++c) f[c] = 0.f;
+          for (int kb = u.kb0;; kb += kSumSteps) {
+#pragma unroll
+            for (int c = 0; c < 128; c += 16) {
+              if (c >= half) break;
+              uint32_t v[16];
+              tmem_ld16(acc + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
+            }
+            if (kb + kSumSteps >= u.kb1) break;
+            release();
+            if (!arrived(acc)) break;
+            acc += h * half;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            if (c >= half) break;
+            tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(f + c));
+          }
+          tmem_st_wait();
+        }
         // this row's targets, while the tile accumulates
         Entries e;
         e.none();
         if (r < learnt)
-          e.start<false>(p.targets,
-                         learnt == p.T ? r : p.targets.token[r], n0);
-        float f[128];
-        uint32_t acc;
-        if (!arrived(acc)) break;
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(acc + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) f[c + j] = __uint_as_float(v[j]);
+          e.start<false>(p, learnt == p.T ? r : p.token[r], n0);
+        if (!several) {
+          if (!first_pass && !arrived(acc)) break;
+          acc += h * half;
         }
-        release();
-        bool ok = true;
-        for (int kb = u.kb0 + kSumSteps; kb < u.kb1; kb += kSumSteps) {
-          if (!(ok = arrived(acc))) break;
-#pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(acc + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
-          }
-          release();
-        }
-        if (!ok) break;
-        if (n0 >= p.V) continue;
         float peak = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+#pragma unroll 1
+        for (int c = 0; c < half; c += 32) {
           const int n = n0 + c;
-          if (n >= p.V) continue;
+          float f[32];
+          {
+            uint32_t v[32];
+            tmem_ld32(acc + c, v);
+            tmem_ld_wait();
+            if (c + 32 == half && !first_pass) release();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+          }
+          if (n >= p.V) continue;  // (after the release)
           while (__any_sync(0xffffffffu, e.id[0] < n + 32)) {
             if (e.id[0] < n + 32) {
-              p.picked[(long long)r * p.targets.top + e.at] =
-                  pick(f + c, e.id[0] - n) * p.targets.inv_tau;
+              p.picked[(long long)r * p.top + e.at] =
+                  pick(f, e.id[0] - n) * p.inv_tau;
               e.pass<false>();
             }
             __syncwarp();
@@ -637,12 +684,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n + 32 > p.V) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (n + j >= p.V) f[c + j] = -INFINITY;
+              if (n + j >= p.V) f[j] = -INFINITY;
           }
-          float top4[4] = {f[c], f[c + 1], f[c + 2], f[c + 3]};
+          float top4[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
-          for (int j = 4; j < 32; ++j)
-            top4[j & 3] = fmaxf(top4[j & 3], f[c + j]);
+          for (int j = 4; j < 32; ++j) top4[j & 3] = fmaxf(top4[j & 3], f[j]);
           const float here =
               fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           const float now = fmaxf(peak, here * c2);
@@ -651,54 +697,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s4[4] = {sum * exp2_fast(peak - ref), 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            s4[j & 3] += exp2_fast(fmaf(f[c + j], c2, -ref));
+            s4[j & 3] += exp2_fast(fmaf(f[j], c2, -ref));
           sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
           peak = now;
         }
+        if (first_pass || n0 >= p.V) continue;
         if (r < learnt)
-          p.stats[(long long)(u.tn * 2 + h) * p.T + r] =
+          p.stats[(long long)(u.tn * 2 + h) * learnt + r] =
               make_float2(peak, sum);
       }
     } else {
       // staging: row (lane) of 128 bytes, its 16-byte chunk j at j ^ (row
-      // mod 8), the layout a 128-byte-swizzle TMA store reads; two blocks,
-      // so that one is written while the other is stored
-      unsigned char* stg = smem + Sh::kOffStaging + (warp - 2) * kStagingBytes;
-      uint32_t stg_s = sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
-      auto other_block = [&]() {
-        const uint32_t flip = 4096;
-        stg = reinterpret_cast<unsigned char*>(
-            reinterpret_cast<uintptr_t>(stg) ^ flip);
-        stg_s ^= flip;
-        if (lane == 0) bulk_wait_group_read<1>();
-        __syncwarp();
-      };
+      // mod 8), the layout a 128-byte-swizzle TMA store reads
+      unsigned char* stg =
+          smem + Sh::kOffStaging + (warp - 2) * kStagingBytes;
+      const uint32_t stg_s =
+          sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
       const float inv_scale = header->inv_scale;
-      const bool dw_direct = p.dw != nullptr && header->dw_splits == 1;
-      const int slot_rows = (int)vocab_slot_rows(learnt);
-      while (walk.next(u)) {
+      const bool dw_direct = !vocab_maps(p.dW, p.lddw);
+      const int slot_rows = vocab_tiles(learnt) * kVocabTile;
+      for (;; first_pass = false) {
+        if (first_pass)
+          u = {phase == 0 ? kGrad : kDx, 1 << 20, 0, 128, 0, 1, 0};
+        else if (!walk.next(u))
+          break;
         const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
         const int r = m0 + lane;
-        const int n0 = u.tn * kVocabTile + h * 128;
-        const int cols = u.kind == kGrad ? p.grad_n : p.D;
+        const int half = u.wide >> 1;  // this warp's columns
+        const int n0 = u.tn * u.wide + h * half;
+        // G is written to the end of its tiles
+        const int cols = u.kind == kGrad ? INT_MAX : p.D;
         Entries e;
         e.none();
         float shift = 0.f, g = 0.f;
         if (u.kind == kGrad && r < learnt) {
-          const long long t = learnt == p.T ? r : p.targets.token[r];
-          e.start<true>(p.targets, t, p.grad_v0 + n0);
+          const long long t = learnt == p.T ? r : p.token[r];
+          e.start<true>(p, t, walk.grad_v0 + n0);
           shift = p.lse[t] * kLog2e;
           g = p.grad_loss[t * p.grad_stride] * p.tau * header->scale;
         }
-        const bool wide = u.kind == kDx || header->dw_splits > 1;  // fp32
-        uint32_t acc;
-        if (!arrived(acc)) break;
+        // sums in fp32 slots
+        const bool wide =
+            u.kind == kDx || (u.kind == kDw && header->dw_splits > 1);
+        uint32_t acc = my_tmem;
+        if (!first_pass && !arrived(acc)) break;
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+        for (int c0 = 0; c0 < half; c0 += 32) {
           uint32_t v[32];
-          tmem_ld32(acc + c0, v);
+          tmem_ld32(acc + h * half + c0, v);
           tmem_ld_wait();
-          if (c0 == 96) release();
+          if (c0 + 32 == half && !first_pass) release();
           const int n = n0 + c0;
           if (n >= cols) continue;  // (after the release)
           float f[32];
@@ -708,17 +756,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               f[j] = exp2_fast(fmaf(f[j], c2, -shift));
-            // rows past the learnt tokens are zeros: Dw sums over them up
-            // to a multiple of 64
+            // rows past the learnt tokens are zeros, and columns past the
+            // vocabulary: Dw and Dx sum over them up to multiples of 64
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = r < learnt ? f[j] * g : 0.f;
+            if (n + 32 > walk.grad_n) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (n + j >= walk.grad_n) f[j] = 0.f;
+            }
           } else if (u.kb0 == u.kb1) {  // an empty sum
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = 0.f;
           }
-          if (u.kind != kGrad && wide) {
+          if (wide) {
             // fp32, 32 columns: one staged block
-            other_block();
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               *reinterpret_cast<float4*>(stg + lane * 128 +
@@ -730,96 +784,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               if (u.kind == kDx) {
                 if (m0 < learnt) {
-                  if (p.first)
+                  if (phase == 1)  // the first piece
                     tma_store_2d(&maps.slots, stg_s, n,
                                  u.slot * slot_rows + m0);
                   else
                     tma_add_2d(&maps.slots, stg_s, n,
                                u.slot * slot_rows + m0);
                 }
-              } else if (m0 < p.back_n) {
+              } else if (m0 < walk.back_n) {
                 tma_store_2d(&maps.dw_slots, stg_s, n,
-                             u.slot * p.dw_rows + m0);
+                             u.slot * p.dw_slot_rows + m0);
               }
               bulk_commit_group();
             }
-          } else {
-            // 16-bit, 64 columns: half a staged block at a time
-            if (u.kind == kDw) {
+            continue;
+          }
+          // 16-bit, 64 columns: half a staged block at a time
+          if (u.kind == kDw) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
-            }
-            if ((c0 & 32) == 0) other_block();
+            for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
+          }
+          if ((c0 & 32) == 0) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+          }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int chunk = (c0 & 32) / 8 + j;
-              *reinterpret_cast<uint4*>(stg + lane * 128 +
-                                        ((chunk ^ (lane & 7)) << 4)) =
-                  make_uint4(pack16<AB_TYPE>(f[8 * j], f[8 * j + 1]),
-                             pack16<AB_TYPE>(f[8 * j + 2], f[8 * j + 3]),
-                             pack16<AB_TYPE>(f[8 * j + 4], f[8 * j + 5]),
-                             pack16<AB_TYPE>(f[8 * j + 6], f[8 * j + 7]));
-            }
-            if (u.kind == kGrad) {
-              // the row's targets in these columns: p - q, in their places
-              const int column = p.grad_v0 + n;
-              float share = 0.f;
-              while (__any_sync(0xffffffffu, e.id[0] < column + 32)) {
-                if (e.id[0] < column + 32) {
-                  const int c = e.id[0] - column;
-                  share += e.q[0];  // an id may come again
-                  e.pass<true>();
-                  if (e.id[0] != column + c) {
-                    const int chunk = (c0 & 32) / 8 + (c >> 3);
-                    *reinterpret_cast<uint16_t*>(
-                        stg + lane * 128 + ((chunk ^ (lane & 7)) << 4) +
-                        (c & 7) * 2) =
-                        (uint16_t)pack16<AB_TYPE>(pick(f, c) - g * share,
-                                                  0.f);
-                    share = 0.f;
-                  }
+          for (int j = 0; j < 4; ++j) {
+            const int chunk = (c0 & 32) / 8 + j;
+            *reinterpret_cast<uint4*>(stg + lane * 128 +
+                                      ((chunk ^ (lane & 7)) << 4)) =
+                make_uint4(pack16<AB_TYPE>(f[8 * j], f[8 * j + 1]),
+                           pack16<AB_TYPE>(f[8 * j + 2], f[8 * j + 3]),
+                           pack16<AB_TYPE>(f[8 * j + 4], f[8 * j + 5]),
+                           pack16<AB_TYPE>(f[8 * j + 6], f[8 * j + 7]));
+          }
+          if (u.kind == kGrad) {
+            // the row's targets in these columns: p - q, in their places
+            const int column = walk.grad_v0 + n;
+            float part = 0.f;
+            while (__any_sync(0xffffffffu, e.id[0] < column + 32)) {
+              if (e.id[0] < column + 32) {
+                const int c = e.id[0] - column;
+                part += e.q[0];  // an id may come again
+                e.pass<true>();
+                if (e.id[0] != column + c) {
+                  const int chunk = (c0 & 32) / 8 + (c >> 3);
+                  *reinterpret_cast<uint16_t*>(
+                      stg + lane * 128 + ((chunk ^ (lane & 7)) << 4) +
+                      (c & 7) * 2) =
+                      (uint16_t)pack16<AB_TYPE>(pick(f, c) - g * part, 0.f);
+                  part = 0.f;
                 }
-                __syncwarp();
               }
+              __syncwarp();
             }
-            // the block is whole, or its other half lies past the columns
-            if ((c0 & 32) || n + 32 >= cols) {
-              const int nb = n - (c0 & 32);
-              if (u.kind == kDw && dw_direct) {
-                // rows on any 2-byte boundary: a warp writes 64 columns of
-                // one row at a time
-                __syncwarp();
-                const int rows = min(32, p.back_n - m0);
-                for (int k = 0; k < rows; ++k) {
-                  const uint32_t two = *reinterpret_cast<const uint32_t*>(
-                      stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) +
-                      (lane & 3) * 4);
-                  uint16_t* to = p.dw +
-                                 (long long)(p.back_v0 + m0 + k) * p.lddw +
-                                 nb + 2 * lane;
-                  if (nb + 2 * lane + 1 < cols &&
-                      (reinterpret_cast<uintptr_t>(to) & 3u) == 0) {
-                    *reinterpret_cast<uint32_t*>(to) = two;
-                  } else {
-                    if (nb + 2 * lane < cols) to[0] = (uint16_t)two;
-                    if (nb + 2 * lane + 1 < cols)
-                      to[1] = (uint16_t)(two >> 16);
-                  }
-                }
-                __syncwarp();
+          }
+          // the block is whole, or its other half lies past the columns
+          if ((c0 & 32) == 0 && n + 32 < cols) continue;
+          const int nb = n - (c0 & 32);
+          if (u.kind == kDw && dw_direct) {
+            // rows on any 2-byte boundary: a warp writes 64 columns of one
+            // row at a time
+            __syncwarp();
+            const int rows = min(32, walk.back_n - m0);
+            for (int k = 0; k < rows; ++k) {
+              const uint32_t two = *reinterpret_cast<const uint32_t*>(
+                  stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) +
+                  (lane & 3) * 4);
+              uint16_t* to =
+                  static_cast<uint16_t*>(p.dW) +
+                  (long long)(walk.back_v0 + m0 + k) * p.lddw + nb +
+                  2 * lane;
+              if (nb + 2 * lane + 1 < cols &&
+                  (reinterpret_cast<uintptr_t>(to) & 3u) == 0) {
+                *reinterpret_cast<uint32_t*>(to) = two;
               } else {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  if (u.kind == kDw) {
-                    if (m0 < p.back_n)
-                      tma_store_2d(&maps.dw, stg_s, nb, p.back_v0 + m0);
-                  } else if (m0 < p.T) {
-                    tma_store_2d(&maps.g_out, stg_s, nb, m0);
-                  }
-                  bulk_commit_group();
-                }
+                if (nb + 2 * lane < cols) to[0] = (uint16_t)two;
+                if (nb + 2 * lane + 1 < cols) to[1] = (uint16_t)(two >> 16);
               }
+            }
+            __syncwarp();
+          } else {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (u.kind == kGrad) {
+                if (!first_pass)
+                  tma_store_2d(&maps.g_out, stg_s, nb, g_out + m0);
+              } else if (m0 < walk.back_n)
+                tma_store_2d(&maps.dw, stg_s, nb, walk.back_v0 + m0);
+              bulk_commit_group();
             }
           }
         }
@@ -828,6 +882,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (lane == 0 && warp < 2) {
+    if (warp == 0) {
+      if (*abort && rank == 0) {  // let the copies still in flight land
+        for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
+          if (!bounded_wait(full(k % kStages), (k / kStages) & 1, kDrainNs,
+                            nullptr, 0))
+            record_status(wc.status, kStatusTimeoutDrain);
+      }
+    } else {
+      // no product may still run when TMEM is freed, nor signal a CTA that
+      // has left: this is the last arrival in both CTAs
+      if (rank == 0) tc_commit2(mma_done);
+      if (!wait_cluster(mma_done, 0, kDrainNs, nullptr))
+        record_status(wc.status, kStatusTimeoutDrain);
+    }
+  }
   griddep_launch_dependents();
   tc_fence_before_sync();
   __syncwarp();  // reconverge the warps whose roles ran on one lane
@@ -854,80 +924,71 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int AB_TYPE, bool FORWARD>
-cudaError_t launch(const VocabGemm& p, int sm_count, const WaitCfg& wc,
-                   cudaStream_t stream) {
-  using Sh = Shape<FORWARD>;
-  if (!tensor_map_encoder()) return cudaErrorNotSupported;
+bool fits_tensor_map(const void* p, long long ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
+}
+
+template <int AB_TYPE>
+bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   const CUtensorMapDataType t16 = AB_TYPE == 1
                                       ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUtensorMapDataType t32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  if (!tensor_map_encoder()) return false;
+  std::memset(maps, 0, sizeof(*maps));
+  bool ok = p.Wp ? encode(&maps->w, t16, 2, p.Wp, p.D, p.V, p.ldxp, 64)
+                 : encode(&maps->w, t16, 2, p.W, p.D, p.V, p.ldw, 64);
+  if (p.header)
+    ok = ok && encode(&maps->xp, t16, 2, p.Xp, p.D, (p.T + 63) / 64 * 64,
+                      p.ldxp, 64);
+  // X as given may have no tensor map: then only the packed copy is read
+  if (fits_tensor_map(p.X, p.ldx))
+    ok = ok && encode(&maps->x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
+  if (!grad) return ok;
+  ok = ok &&
+       encode(&maps->g_in, t16, 2, p.G, p.piece, 2ll * p.g_rows, p.piece,
+              64) &&
+       encode(&maps->g_out, t16, 2, p.G, p.piece, 2ll * p.g_rows, p.piece,
+              32) &&
+       encode(&maps->slots, t32, 4, p.slots, p.D, p.slot_rows, p.ld_slot, 32);
+  if (p.dw_slots)
+    ok = ok && encode(&maps->dw_slots, t32, 4, p.dw_slots, p.D,
+                      (long long)p.dw_slot_rows * p.dw_max_splits, p.ld_slot,
+                      32);
+  if (fits_tensor_map(p.dW, p.lddw))
+    ok = ok && encode(&maps->dw, t16, 2, p.dW, p.D, p.V, p.lddw, 32);
+  return ok;
+}
+
+template <int AB_TYPE, bool FORWARD>
+cudaError_t launch(const VocabCall& p, const WaitCfg& wc,
+                   cudaStream_t stream) {
+  using Sh = Shape<FORWARD>;
   Maps maps;
-  std::memset(&maps, 0, sizeof(maps));
-  Args k = {};
-  k.T = p.T, k.V = p.V, k.D = p.D;
-  k.targets = p.targets;
-  bool ok = encode(&maps.xp, t16, 2, p.Xp, p.D, p.rows_xp, p.ldxp, 64) &&
-            encode(&maps.w, t16, 2, p.W, p.D, p.V, p.ldw, 64);
-  // X as given may have no tensor map (its alignment): then only the packed
-  // copy is read
-  if ((reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 && p.ldx % 8 == 0)
-    ok = ok && encode(&maps.x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
-  else
-    maps.x = maps.xp;
-  if (FORWARD) {
-    k.stats = p.stats, k.picked = p.picked;
-  } else {
-    k.grad_v0 = p.grad.v0, k.grad_n = p.grad.n;
-    k.back_v0 = p.back.v0, k.back_n = p.back.n;
-    k.piece = p.piece, k.first = p.first;
-    k.lse = p.lse, k.grad_loss = p.grad_loss;
-    k.grad_stride = p.grad_stride, k.tau = p.tau;
-    k.dw_rows = (int)p.dw_slot_rows;
-    if (p.grad.n > 0)
-      ok = ok && encode(&maps.g_out, t16, 2, p.grad.G, p.grad.n, p.T, p.ldg,
-                        32);
-    if (p.back.n > 0) {
-      ok = ok &&
-           encode(&maps.g_in, t16, 2, p.back.G, p.back.n, p.T, p.ldg, 64) &&
-           encode(&maps.slots, t32, 4, p.slots, p.D, p.slot_rows, p.ld_slot,
-                  32);
-      if (p.dw_slots)
-        ok = ok && encode(&maps.dw_slots, t32, 4, p.dw_slots, p.D,
-                          p.dw_slot_rows * p.dw_max_splits, p.ld_slot, 32);
-      if ((reinterpret_cast<uintptr_t>(p.dW) & 15u) == 0 && p.lddw % 8 == 0) {
-        ok = ok && encode(&maps.dw, t16, 2, p.dW, p.D, p.V, p.lddw, 32);
-      } else {
-        k.dw = static_cast<uint16_t*>(p.dW);
-        k.lddw = p.lddw;
-      }
-    }
-  }
-  if (!ok) return cudaErrorInvalidValue;
+  if (!make_maps<AB_TYPE>(p, !FORWARD, &maps)) return cudaErrorInvalidValue;
   auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD>;
   cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(fn), Sh::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(fn, dim3(2 * vocab_pairs(sm_count)),
-                            dim3(kThreads), Sh::kSmemBytes, stream, 2, maps,
-                            k, wc);
+  const int phases = FORWARD ? 1 : p.pieces + 1;
+  for (int phase = 0; phase < phases && e == cudaSuccess; ++phase)
+    e = launch_pdl_cluster(fn, dim3(2 * p.pairs), dim3(kThreads),
+                           Sh::kSmemBytes, stream, 2, maps, p, phase, wc);
+  return e;
 }
 
 }  // namespace vocab
 
-cudaError_t launch_vocab_stats(const VocabGemm& p, int sm_count,
-                               const WaitCfg& wc, cudaStream_t stream) {
-  return p.type == GEMM_F32_MIXED_BF16
-             ? vocab::launch<1, true>(p, sm_count, wc, stream)
-             : vocab::launch<0, true>(p, sm_count, wc, stream);
+cudaError_t vocab_forward(const VocabCall& c, const WaitCfg& wc,
+                          cudaStream_t stream) {
+  return c.type == GEMM_F32_MIXED_BF16 ? vocab::launch<1, true>(c, wc, stream)
+                                       : vocab::launch<0, true>(c, wc, stream);
 }
 
-cudaError_t launch_vocab_step(const VocabGemm& p, int sm_count,
-                              const WaitCfg& wc, cudaStream_t stream) {
-  return p.type == GEMM_F32_MIXED_BF16
-             ? vocab::launch<1, false>(p, sm_count, wc, stream)
-             : vocab::launch<0, false>(p, sm_count, wc, stream);
+cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
+                            cudaStream_t stream) {
+  return c.type == GEMM_F32_MIXED_BF16
+             ? vocab::launch<1, false>(c, wc, stream)
+             : vocab::launch<0, false>(c, wc, stream);
 }
 
 }  // namespace gemm_f32_impl
