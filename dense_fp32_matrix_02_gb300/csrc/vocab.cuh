@@ -110,6 +110,8 @@ struct VocabCall {
   uint8_t* learnt_flag;  // distillation: whether anything of a token counts
   int* ids;              // distillation [T][top]: entries that count, by id,
   float* weights;        // then INT_MAX; log q (forward) or q of each
+  uint16_t* starts;      // distillation [T][columns / 128]: the row's first
+  int blocks;            // entry in each block of 128 columns, or after it
   void* Xp;              // X's packed copy: the learnt tokens' rows, then
   long long ldxp;        // zero rows up to a multiple of 64
   void* Wp;              // W's packed copy, or null (W has a tensor map)

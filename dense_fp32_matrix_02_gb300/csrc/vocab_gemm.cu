@@ -333,6 +333,14 @@ struct Walk {
   }
 };
 
+// What of a row's targets is read a tile ahead: the target itself, or where
+// the teacher's entries for its columns start.
+__device__ __forceinline__ int peek(const VocabCall& p, long long t,
+                                    int column) {
+  return p.targets ? (int)p.targets[t]
+                   : p.starts[t * p.blocks + (column >> 7)];
+}
+
 // A row's entries from a column on, four of them ahead in registers: the
 // next id is at hand when one is passed.
 struct Entries {
@@ -347,14 +355,14 @@ struct Entries {
 #pragma unroll
     for (int i = 0; i < 4; ++i) id[i] = INT_MAX;
   }
+  // seen: what peek found for them
   template <bool WEIGHTS>
   __device__ __forceinline__ void start(const VocabCall& p, long long t,
-                                        int column) {
+                                        int column, int seen) {
     if (p.targets) {  // one entry of weight 1
-      const int y = (int)p.targets[t];
-      at = y < column;
+      at = 0;
       top = 1;
-      id[0] = at ? INT_MAX : y;
+      id[0] = seen >= column ? seen : INT_MAX;
       id[1] = id[2] = id[3] = INT_MAX;
       q[0] = 1.f;
       return;
@@ -362,28 +370,14 @@ struct Entries {
     ids = p.ids + t * p.top;
     weights = p.weights + t * p.top;
     top = p.top;
-    // the first with id >= column: eight-way steps, as each costs the
-    // latency of its loads
-    int lo = 0;
-    for (int width = top; width > 1;) {
-      const int step = (width + 7) >> 3;
-      int below = 0;
-#pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        const int j = lo + i * step - 1;
-        below += i * step <= width && j < top && ids[j] < column;
-      }
-      lo += below * step;
-      width = step;
-    }
-    at = lo;
-    if (at < top && ids[at] < column) ++at;
+    at = seen;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool here = at + i < top;
       id[i] = here ? ids[at + i] : INT_MAX;
       if (WEIGHTS) q[i] = here ? weights[at + i] : 0.f;
     }
+    while (id[0] < column) pass<WEIGHTS>();  // (columns inside a block)
   }
   template <bool WEIGHTS>
   __device__ __forceinline__ void pass() {
@@ -609,12 +603,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // with nothing stored: it brings the instructions in while the first
     // tile is being made (which they otherwise hold up by 2-3 us).
     bool first_pass = true;
+    // The next tile, and of this row's targets in it what costs a load to
+    // find: read while the tile before is worked on.
+    Unit nu;
+    int n_token = 0, n_seen = 0;
+    float n_lse = 0.f, n_grad = 0.f;
+    auto look_ahead = [&]() -> bool {
+      if (!walk.next(nu)) return false;
+      const int r = nu.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
+      if ((nu.kind == kStats || nu.kind == kGrad) && r < learnt) {
+        n_token = learnt == p.T ? r : p.token[r];
+        const int n0 = nu.tn * nu.wide + h * (nu.wide >> 1);
+        n_seen = peek(p, n_token, FORWARD ? n0 : walk.grad_v0 + n0);
+        if (!FORWARD) {
+          n_lse = p.lse[n_token];
+          n_grad = p.grad_loss[n_token * p.grad_stride];
+        }
+      }
+      return true;
+    };
+    bool more = look_ahead();
     if constexpr (FORWARD) {
       for (;; first_pass = false) {
-        if (first_pass)
+        int token = 0, seen = 0;
+        if (first_pass) {
           u = {kStats, 1 << 20, 0, 64, 0, 0, 0};
-        else if (!walk.next(u))
-          break;
+        } else {
+          if (!more) break;
+          u = nu;
+          token = n_token;
+          seen = n_seen;
+        }
         const int r = u.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
         const int half = u.wide >> 1;  // this warp's columns
         const int n0 = u.tn * u.wide + h * half;
@@ -650,11 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st_wait();
         }
-        // this row's targets, while the tile accumulates
+        if (!first_pass) more = look_ahead();
         Entries e;
         e.none();
-        if (r < learnt)
-          e.start<false>(p, learnt == p.T ? r : p.token[r], n0);
+        if (r < learnt) e.start<false>(p, token, n0, seen);
         if (!several) {
           if (!first_pass && !arrived(acc)) break;
           acc += h * half;
@@ -714,13 +732,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t stg_s =
           sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
       const float inv_scale = header->inv_scale;
+      const float grad_scale = p.tau * header->scale;
       const bool dw_direct = !vocab_maps(p.dW, p.lddw);
       const int slot_rows = vocab_tiles(learnt) * kVocabTile;
       for (;; first_pass = false) {
-        if (first_pass)
+        int token = 0, seen = 0;
+        float shift = 0.f, g = 0.f;
+        if (first_pass) {
           u = {phase == 0 ? kGrad : kDx, 1 << 20, 0, 128, 0, 1, 0};
-        else if (!walk.next(u))
-          break;
+        } else {
+          if (!more) break;
+          u = nu;
+          token = n_token;
+          seen = n_seen;
+          shift = n_lse * kLog2e;
+          g = n_grad * grad_scale;
+          more = look_ahead();
+        }
         const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
         const int r = m0 + lane;
         const int half = u.wide >> 1;  // this warp's columns
@@ -729,13 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cols = u.kind == kGrad ? INT_MAX : p.D;
         Entries e;
         e.none();
-        float shift = 0.f, g = 0.f;
-        if (u.kind == kGrad && r < learnt) {
-          const long long t = learnt == p.T ? r : p.token[r];
-          e.start<true>(p, t, walk.grad_v0 + n0);
-          shift = p.lse[t] * kLog2e;
-          g = p.grad_loss[t * p.grad_stride] * p.tau * header->scale;
-        }
+        if (u.kind == kGrad && r < learnt)
+          e.start<true>(p, token, walk.grad_v0 + n0, seen);
         // sums in fp32 slots
         const bool wide =
             u.kind == kDx || (u.kind == kDw && header->dw_splits > 1);

@@ -83,12 +83,23 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
     const int j = in + 32 * i;
     if (j < p.top && here) {
       const int id = mine[j];
-      int rank = 0;
-      for (int k = 0; k < p.top; ++k)
-        rank += mine[k] < id || (mine[k] == id && k < j);
+      int rank = 0, prev = -1;  // prev: the id of the rank before
+      for (int k = 0; k < p.top; ++k) {
+        const int other = mine[k];
+        if (other < id || (other == id && k < j)) {
+          ++rank;
+          prev = max(prev, other);
+        }
+      }
       const float log_q = (u[i] - peak) - log_sum;
       p.ids[t * p.top + rank] = id;
       p.weights[t * p.top + rank] = logs ? log_q : expf(log_q);
+      // the blocks of 128 columns that start behind the entry before
+      uint16_t* starts = p.starts + t * p.blocks;
+      const int last = id == INT_MAX ? p.blocks - 1 : id >> 7;
+      for (int b = (prev >> 7) + 1; b <= last; ++b) starts[b] = (uint16_t)rank;
+      if (rank == p.top - 1)
+        for (int b = last + 1; b < p.blocks; ++b) starts[b] = (uint16_t)p.top;
     }
   }
 }
@@ -572,6 +583,8 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   take(&c->learnt_flag, rows);
   take(&c->ids, rows * top * 4);
   take(&c->weights, rows * top * 4);
+  c->blocks = (int)((V + 127) / 128);
+  take(&c->starts, rows * c->blocks * 2);
   c->ldxp = up(D, 8);
   char* bytes = nullptr;
   take(&bytes, up(rows, 64) * c->ldxp * 2);
