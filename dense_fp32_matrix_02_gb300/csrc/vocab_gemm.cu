@@ -140,40 +140,13 @@ __device__ __forceinline__ void tma_load2_2d(uint32_t dst, const void* tmap,
       : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile(
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(
-          bar)
-      : "memory");
-}
-
-// As mbar_try_wait, acquiring what threads of the other CTA released.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar,
-                                                      uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
-      "%2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity,
-                                             long long limit_ns,
-                                             volatile int* abort) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 15u) == 0) {
-      if (abort && *abort) return false;
-      if ((long long)(globaltimer_ns() - t0) > limit_ns) return false;
-    }
-  }
+// One arrival on a barrier of either CTA.  What it orders, the reads of
+// TMEM, has completed before it (tcgen05.wait::ld); no other memory is handed
+// over, so neither it nor the wait for it needs the scope of the cluster (a
+// release and acquire of that scope held up every step and every tile).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar)
+               : "memory");
 }
 
 // Adds a block in memory (c0 innermost).
@@ -534,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int end =
               FORWARD && u.kb1 - kb > kSumSteps ? kb + kSumSteps : u.kb1;
           const int b = i & 1;
-          if (i >= 2 && !wait_cluster(acc_empty(b), ((i >> 1) - 1) & 1,
-                                      wc.limit, abort)) {
+          if (i >= 2 && !bounded_wait(acc_empty(b), ((i >> 1) - 1) & 1, wc.limit,
+                                      abort, 0)) {
             *abort = 1;
             record_status(wc.status, kStatusTimeoutMma);
             ok = false;
@@ -545,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d_tmem = tmem + b * 256;
           for (const int k0 = kb; kb < end; ++kb, ++it) {
             const int s = it % kStages;
-            if (!wait_cluster(full(s), (it / kStages) & 1, wc.limit,
-                              abort)) {
+            if (!bounded_wait(full(s), (it / kStages) & 1, wc.limit, abort,
+                              0)) {
               *abort = 1;
               record_status(wc.status, kStatusTimeoutFull);
               ok = false;
@@ -595,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto release = [&]() {
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_map(acc_empty(i & 1), 0));
+      if (lane == 0) mbar_arrive_pair(cluster_map(acc_empty(i & 1), 0));
       ++i;
     };
 
@@ -917,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no product may still run when TMEM is freed, nor signal a CTA that
       // has left: this is the last arrival in both CTAs
       if (rank == 0) tc_commit2(mma_done);
-      if (!wait_cluster(mma_done, 0, kDrainNs, nullptr))
+      if (!bounded_wait(mma_done, 0, kDrainNs, nullptr, 0))
         record_status(wc.status, kStatusTimeoutDrain);
     }
   }
