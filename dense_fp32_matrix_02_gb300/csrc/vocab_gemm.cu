@@ -207,6 +207,7 @@ struct Walk {
   int whole, x, x1, slot;            // whole: tiles before the line's
   int grad_v0, grad_n, back_v0, back_n;
   int wide, dw_wide;
+  bool dx_first;
 
   __device__ __forceinline__ Walk(const VocabCall& p, int learnt, int phase,
                                   int pair_, int pairs_)
@@ -220,6 +221,7 @@ struct Walk {
     wide = h ? h->wide : p.wide;
     tiles_n = ((FORWARD ? p.V : grad_n) + wide - 1) / wide;
     steps = vocab_steps(p.D);
+    dx_first = false;
     if (!FORWARD && phase == 0) {
       stage = 3;
       j = pairs - 1 - pair;
@@ -237,10 +239,46 @@ struct Walk {
       x = h->share[pair].x0;
       x1 = h->share[pair].x1;
       slot = h->share[pair].slot;
+      dx_first = tiles_m == 1 && (pair & 1);
+      if (dx_first) stage = 1;
     }
   }
 
+  // dX's whole tiles, then its share of the line
+  __device__ __forceinline__ bool next_dx(Unit& u) {
+    u.kind = kDx;
+    u.wide = kVocabTile;
+    if (j < whole) {
+      tile_coords<kVocabGroup>(j, dx_m, dx_n, u.tm, u.tn);
+      u.kb0 = 0;
+      u.kb1 = dx_steps;
+      u.slot = 0;
+      j += pairs;
+      return true;
+    }
+    if (x >= x1) return false;
+    const int tile = x / line;
+    const int end = min(x1, (tile + 1) * line);
+    tile_coords<kVocabGroup>(whole + tile, dx_m, dx_n, u.tm, u.tn);
+    // a shorter last piece is cut in proportion
+    u.kb0 = x - tile * line;
+    u.kb1 = end - tile * line;
+    if (dx_steps != line) {
+      u.kb0 = (int)((long long)u.kb0 * dx_steps / line);
+      u.kb1 = (int)((long long)u.kb1 * dx_steps / line);
+    }
+    u.slot = slot;
+    slot = 0;
+    x = end;
+    return true;
+  }
+
   __device__ __forceinline__ bool next(Unit& u) {
+    if (dx_first && stage == 1) {
+      if (next_dx(u)) return true;
+      stage = 0;
+      j = pair;
+    }
     if (stage == 0) {
       const int tiles = dw_m * dw_n;
       if (j < tiles * splits) {
@@ -254,41 +292,14 @@ struct Walk {
         j += pairs;
         return true;
       }
-      stage = 1;
+      stage = dx_first ? 2 : 1;
       j = pair;
     }
     if (stage == 1) {
-      if (j < whole && j < dx_m * dx_n) {
-        u.kind = kDx;
-        u.wide = kVocabTile;
-        tile_coords<kVocabGroup>(j, dx_m, dx_n, u.tm, u.tn);
-        u.kb0 = 0;
-        u.kb1 = dx_steps;
-        u.slot = 0;
-        j += pairs;
-        return true;
-      }
+      if (next_dx(u)) return true;
       stage = 2;
     }
     if (stage == 2) {
-      if (x < x1) {
-        const int tile = x / line;
-        const int end = min(x1, (tile + 1) * line);
-        u.kind = kDx;
-        u.wide = kVocabTile;
-        tile_coords<kVocabGroup>(whole + tile, dx_m, dx_n, u.tm, u.tn);
-        // a shorter last piece is cut in proportion
-        u.kb0 = x - tile * line;
-        u.kb1 = end - tile * line;
-        if (dx_steps != line) {
-          u.kb0 = (int)((long long)u.kb0 * dx_steps / line);
-          u.kb1 = (int)((long long)u.kb1 * dx_steps / line);
-        }
-        u.slot = slot;
-        slot = 0;
-        x = end;
-        return true;
-      }
       stage = 3;
       // the other way round, so that no pair has the last, partly filled
       // round of both dW and G
