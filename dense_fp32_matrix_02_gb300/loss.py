@@ -26,6 +26,7 @@ __all__ = ["cross_entropy", "cross_entropy_grad", "distill", "distill_grad",
            "workspace_size"]
 
 _TYPES = {torch.bfloat16: _g.MIXED_BF16, torch.float16: _g.MIXED_F16}
+_FLOAT, _INT = (torch.float32,), (torch.int64,)
 _STAY = contextlib.nullcontext()
 
 
@@ -83,21 +84,35 @@ def _vector(t, name, n, dtype, device, expand=False):
     return t.data_ptr() or None, stride
 
 
-def _targets(targets, T, device):
-    """The C arguments of cross entropy's targets, with top = 1."""
-    return 1, (_vector(targets, "targets", T, torch.int64, device)[0],)
-
-
-def _teacher(top_logits, top_ids, temperature, T, device):
-    """The C arguments of a teacher's entries, with their number a token."""
-    rows, top, up, ldt = _matrix(top_logits, "top_logits", (torch.float32,),
-                                 device)
-    rows2, top2, ip, ldi = _matrix(top_ids, "top_ids", (torch.int64,), device)
+def _teacher(top_logits, top_ids, T, device):
+    """(entries a token, logits pointer, ldt, ids pointer, ldi)."""
+    rows, top, up, ldt = _matrix(top_logits, "top_logits", _FLOAT, device)
+    rows2, top2, ip, ldi = _matrix(top_ids, "top_ids", _INT, device)
     if rows != T or rows2 != T:
         raise ValueError("top_logits and top_ids must have one row per token")
     if top != top2:
         raise ValueError("top_logits and top_ids have different widths")
-    return top, (top, up, ldt, ip, ldi, float(temperature))
+    return top, up, ldt, ip, ldi
+
+
+def _operands(x, w):
+    """(type, T, V, D, x pointer, ldx, w pointer, ldw) and whether both have
+    the alignment that needs no copies."""
+    T, D, xp, ldx = _matrix(x, "x", _TYPES)
+    V, D2, wp, ldw = _matrix(w, "w", _TYPES, x.device)
+    if x.dtype != w.dtype:
+        raise TypeError("x and w must have the same 16-bit dtype")
+    if D != D2:
+        raise ValueError(f"widths differ: x {tuple(x.shape)}, w "
+                         f"{tuple(w.shape)}")
+    aligned = ((xp or 0) | (wp or 0)) % 16 == 0 and (ldx | ldw) % 8 == 0
+    return (_TYPES[x.dtype], T, V, D, xp, ldx, wp, ldw), int(aligned)
+
+
+def _on(device):
+    """The device made current, where it is not already."""
+    return _STAY if torch.cuda.current_device() == device.index else \
+        torch.cuda.device(device)
 
 
 def _new(shape, dtype, device, stream):
@@ -119,68 +134,68 @@ def _out(t, shape, dtype, device, name, stream):
     return t, p, ld
 
 
-def _call(name, entry, make_targets, x, w, finish, grad, workspace, stream):
-    """One library call: x, w and the targets' arguments, then what
-    finish(T, V, D, device) returns as (results, C arguments)."""
-    T, D, xp, ldx = _matrix(x, "x", _TYPES)
-    device = x.device
-    V, D2, wp, ldw = _matrix(w, "w", _TYPES, device)
-    if x.dtype != w.dtype:
-        raise TypeError("x and w must have the same 16-bit dtype")
-    if D != D2:
-        raise ValueError(f"widths differ: x {tuple(x.shape)}, w "
-                         f"{tuple(w.shape)}")
-    top, target_args = make_targets(T, device)
-    with _STAY if torch.cuda.current_device() == device.index else \
-            torch.cuda.device(device):
-        results, args = finish(T, V, D, device)
-        if workspace is None:
-            aligned = ((xp or 0) | (wp or 0)) % 16 == 0 and \
-                (ldx | ldw) % 8 == 0
-            n = _size(T, V, D, top, grad, int(aligned))
-            workspace = _new(n, torch.uint8, device, stream)
-        else:
-            if workspace.device != device:
-                raise ValueError("workspace must live on x's device")
-            n = workspace.numel() * workspace.element_size()
-        st = entry(_TYPES[x.dtype], T, V, D, xp, ldx, wp, ldw, *target_args,
-                   *args, workspace.data_ptr() or None, n,
-                   _g._handle(stream, device) or None)
-    if st:
-        _g._check(st, name)
-    return results
+def _scratch(workspace, head, top, grad, aligned, device, stream):
+    """(workspace, pointer, bytes), allocated when not given."""
+    if workspace is None:
+        n = _size(head[1], head[2], head[3], top, grad, aligned)
+        workspace = _new(n, torch.uint8, device, stream)
+    else:
+        if workspace.device != device:
+            raise ValueError("workspace must live on x's device")
+        n = workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr() or None, n
 
 
-def _forward(name, make_targets, x, w, workspace, stream):
-    def outputs(T, V, D, device):
+def _stream(stream, device):
+    """The stream's handle, or NULL (the current stream's without the object
+    that torch.cuda.current_stream makes: 2 us of a call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index) or None
+    return (stream.cuda_stream if hasattr(stream, "cuda_stream") else
+            int(stream)) or None
+
+
+def _forward(name, x, w, head, aligned, top, target_args, workspace, stream):
+    device, T = x.device, head[1]
+    with _on(device):
         loss = _new(T, torch.float32, device, stream)
         lse = _new(T, torch.float32, device, stream)
-        return (loss, lse), (loss.data_ptr() or None, lse.data_ptr() or None)
+        workspace, wp, n = _scratch(workspace, head, top, 0, aligned, device,
+                                    stream)
+        st = getattr(_g.lib(), name)(
+            *head, *target_args, loss.data_ptr() or None,
+            lse.data_ptr() or None, wp, n, _stream(stream, device))
+    if st:
+        _g._check(st, name)
+    return loss, lse
 
-    return _call(name, getattr(_g.lib(), name), make_targets, x, w, outputs,
-                 0, workspace, stream)
 
-
-def _backward(name, make_targets, x, w, lse, grad_loss, dx, dw, workspace,
-              stream):
-    def outputs(T, V, D, device):
-        lp, _ = _vector(lse, "lse", T, torch.float32, device)
-        gp, gs = _vector(grad_loss, "grad_loss", T, torch.float32, device,
-                         expand=True)
-        a, ap, lda = _out(dx, (T, D), x.dtype, device, "dx", stream)
-        b, bp, ldb = _out(dw, (V, D), x.dtype, device, "dw", stream)
-        return (a, b), (lp, gp, gs, ap, lda, bp, ldb)
-
-    return _call(name, getattr(_g.lib(), name), make_targets, x, w, outputs,
-                 1, workspace, stream)
+def _backward(name, x, w, head, aligned, top, target_args, lse, grad_loss, dx,
+              dw, workspace, stream):
+    device, (_, T, V, D) = x.device, head[:4]
+    lp, _ = _vector(lse, "lse", T, torch.float32, device)
+    gp, gs = _vector(grad_loss, "grad_loss", T, torch.float32, device,
+                     expand=True)
+    with _on(device):
+        dx, dxp, lddx = _out(dx, (T, D), x.dtype, device, "dx", stream)
+        dw, dwp, lddw = _out(dw, (V, D), x.dtype, device, "dw", stream)
+        workspace, wp, n = _scratch(workspace, head, top, 1, aligned, device,
+                                    stream)
+        st = getattr(_g.lib(), name)(
+            *head, *target_args, lp, gp, gs, dxp, lddx, dwp, lddw, wp, n,
+            _stream(stream, device))
+    if st:
+        _g._check(st, name)
+    return dx, dw
 
 
 def cross_entropy(x, w, targets, workspace=None, stream=None):
     """(loss, lse), float32, one value per token: lse = log Σ exp(logits),
     loss = lse − logits[targets].  targets: int64; a target outside
     [0, vocab) marks a token that is not learnt from (loss and lse 0)."""
-    return _forward("gemm_f32_vocab_ce",
-                    lambda T, device: _targets(targets, T, device), x, w,
+    head, aligned = _operands(x, w)
+    y, _ = _vector(targets, "targets", head[1], torch.int64, x.device)
+    return _forward("gemm_f32_vocab_ce", x, w, head, aligned, 1, (y,),
                     workspace, stream)
 
 
@@ -189,8 +204,9 @@ def cross_entropy_grad(x, w, targets, lse, grad_loss, dx=None, dw=None,
     """(dx, dw) in x's dtype from the gradient of each token's loss
     (float32; an expanded scalar is taken as it is); lse as cross_entropy
     returned it."""
-    return _backward("gemm_f32_vocab_ce_grad",
-                     lambda T, device: _targets(targets, T, device), x, w,
+    head, aligned = _operands(x, w)
+    y, _ = _vector(targets, "targets", head[1], torch.int64, x.device)
+    return _backward("gemm_f32_vocab_ce_grad", x, w, head, aligned, 1, (y,),
                      lse, grad_loss, dx, dw, workspace, stream)
 
 
@@ -200,17 +216,19 @@ def distill(x, w, top_logits, top_ids, temperature=1.0, workspace=None,
     of softmax(logits/τ) from softmax(top_logits/τ) over the teacher's
     entries (float32 logits and int64 ids, tokens × top; an id outside
     [0, vocab) or a logit of −inf: no entry)."""
-    return _forward("gemm_f32_vocab_distill",
-                    lambda T, device: _teacher(top_logits, top_ids,
-                                               temperature, T, device),
-                    x, w, workspace, stream)
+    head, aligned = _operands(x, w)
+    teacher = _teacher(top_logits, top_ids, head[1], x.device)
+    return _forward("gemm_f32_vocab_distill", x, w, head, aligned,
+                    teacher[0], (*teacher, float(temperature)), workspace,
+                    stream)
 
 
 def distill_grad(x, w, top_logits, top_ids, lse, grad_loss, temperature=1.0,
                  dx=None, dw=None, workspace=None, stream=None):
     """(dx, dw) in x's dtype from the gradient of each token's loss; lse as
     distill returned it."""
-    return _backward("gemm_f32_vocab_distill_grad",
-                     lambda T, device: _teacher(top_logits, top_ids,
-                                                temperature, T, device),
-                     x, w, lse, grad_loss, dx, dw, workspace, stream)
+    head, aligned = _operands(x, w)
+    teacher = _teacher(top_logits, top_ids, head[1], x.device)
+    return _backward("gemm_f32_vocab_distill_grad", x, w, head, aligned,
+                     teacher[0], (*teacher, float(temperature)), lse,
+                     grad_loss, dx, dw, workspace, stream)
