@@ -11,6 +11,7 @@
 namespace gemm_f32_impl {
 
 constexpr int kVocabMaxTop = 256;
+constexpr uint32_t kVocabNone = 0xffff;
 constexpr int kVocabTile = 256;      // rows and columns of an output tile
 constexpr int kVocabMaxPairs = 128;  // CTA pairs of a launch
 constexpr int kVocabMaxDwSplits = 16;
@@ -110,8 +111,10 @@ struct VocabCall {
   uint8_t* learnt_flag;  // distillation: whether anything of a token counts
   int* ids;              // distillation [T][top]: entries that count, by id,
   float* weights;        // then INT_MAX; log q (forward) or q of each
-  uint16_t* starts;      // distillation [T][columns / 128]: the row's first
-  int blocks;            // entry in each block of 128 columns, or after it
+  uint32_t* starts;      // distillation [T][blocks of 128 columns]: in the
+  int blocks;            // low half the number of the row's first entry in
+                         // the block or after it, in the high half its column
+                         // in the block (kVocabNone: it is after it)
   void* Xp;              // X's packed copy: the learnt tokens' rows, then
   long long ldxp;        // zero rows up to a multiple of 64
   void* Wp;              // W's packed copy, or null (W has a tensor map)

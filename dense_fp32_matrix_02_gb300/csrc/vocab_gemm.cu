@@ -167,6 +167,38 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// f[i] = f[i]·m + a for 32 values, two to an instruction.
+__device__ __forceinline__ void scale_add_32(float* f, float m, float a) {
+  uint64_t mm, aa;
+  asm("mov.b64 %0, {%1, %1};\n" : "=l"(mm) : "f"(m));
+  asm("mov.b64 %0, {%1, %1};\n" : "=l"(aa) : "f"(a));
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(f[j]), "f"(f[j + 1]));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;\n" : "+l"(x) : "l"(mm), "l"(aa));
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f[j]), "=f"(f[j + 1]) : "l"(x));
+  }
+}
+
+// The sum of 32 values, two additions to an instruction, in four runs.
+__device__ __forceinline__ float sum_32(const float* f) {
+  uint64_t s[2];
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(f[j]), "f"(f[j + 1]));
+    if (j < 4)
+      s[j >> 1] = x;
+    else
+      asm("add.rn.f32x2 %0, %0, %1;\n" : "+l"(s[(j >> 1) & 1]) : "l"(x));
+  }
+  asm("add.rn.f32x2 %0, %0, %1;\n" : "+l"(s[0]) : "l"(s[1]));
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(s[0]));
+  return a + b;
+}
+
 template <int AB_TYPE>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (AB_TYPE == 1) {
@@ -322,7 +354,7 @@ struct Walk {
 __device__ __forceinline__ int peek(const VocabCall& p, long long t,
                                     int column) {
   return p.targets ? (int)p.targets[t]
-                   : p.starts[t * p.blocks + (column >> 7)];
+                   : (int)p.starts[t * p.blocks + (column >> 7)];
 }
 
 // A row's entries from a column on, four of them ahead in registers: the
@@ -339,7 +371,7 @@ struct Entries {
 #pragma unroll
     for (int i = 0; i < 4; ++i) id[i] = INT_MAX;
   }
-  // seen: what peek found for them
+  // from a column on; seen: what peek found there
   template <bool WEIGHTS>
   __device__ __forceinline__ void start(const VocabCall& p, long long t,
                                         int column, int seen) {
@@ -351,14 +383,17 @@ struct Entries {
       q[0] = 1.f;
       return;
     }
+    // (columns are looked at 128 at most at a time, all of one block)
+    const uint32_t first = (uint32_t)seen >> 16;
     ids = p.ids + t * p.top;
     weights = p.weights + t * p.top;
-    top = p.top;
-    at = seen;
+    at = seen & 0xffff;
+    top = first == kVocabNone ? 0 : p.top;
+    id[0] = first == kVocabNone ? INT_MAX : (column & ~127) + (int)first;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool here = at + i < top;
-      id[i] = here ? ids[at + i] : INT_MAX;
+      if (i > 0) id[i] = here ? ids[at + i] : INT_MAX;
       if (WEIGHTS) q[i] = here ? weights[at + i] : 0.f;
     }
     while (id[0] < column) pass<WEIGHTS>();  // (columns inside a block)
@@ -707,11 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float now = fmaxf(peak, here * c2);
           // a stretch of -Inf only: every term is 0, not exp(-Inf + Inf)
           const float ref = now == -INFINITY ? 0.f : now;
-          float s4[4] = {sum * exp2_fast(peak - ref), 0.f, 0.f, 0.f};
+          scale_add_32(f, c2, -ref);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            s4[j & 3] += exp2_fast(fmaf(f[j], c2, -ref));
-          sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          for (int j = 0; j < 32; ++j) f[j] = exp2_fast(f[j]);
+          sum = sum * exp2_fast(peak - ref) + sum_32(f);
           peak = now;
         }
         if (first_pass || n0 >= p.V) continue;
@@ -740,8 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           u = nu;
           token = n_token;
           seen = n_seen;
-          shift = n_lse * kLog2e;
+          // g·p is one exponential, 2^(z·c2 + log2 |g| - lse·log2 e), with
+          // g's sign (g = 0: the exponent is -Inf)
           g = n_grad * grad_scale;
+          shift = log2f(fabsf(g)) - n_lse * kLog2e;
           more = look_ahead();
         }
         const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
@@ -771,13 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
           if (u.kind == kGrad) {
+            scale_add_32(f, c2, shift);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              f[j] = exp2_fast(fmaf(f[j], c2, -shift));
-            // rows past the learnt tokens are zeros, and columns past the
-            // vocabulary: Dw and Dx sum over them up to multiples of 64
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = r < learnt ? f[j] * g : 0.f;
+            for (int j = 0; j < 32; ++j) f[j] = exp2_fast(f[j]);
+            // columns past the vocabulary are zeros, and (below) rows past
+            // the learnt tokens: Dw and Dx sum over them up to multiples of
+            // 64
             if (n + 32 > walk.grad_n) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -826,15 +861,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
           }
+          uint32_t keep = 0xffffffffu, flip = 0;
+          if (u.kind == kGrad) {
+            keep = r < learnt ? 0xffffffffu : 0u;
+            flip = g < 0.f ? 0x80008000u : 0u;
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int chunk = (c0 & 32) / 8 + j;
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = (pack16<AB_TYPE>(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]) ^
+                      flip) & keep;
             *reinterpret_cast<uint4*>(stg + lane * 128 +
                                       ((chunk ^ (lane & 7)) << 4)) =
-                make_uint4(pack16<AB_TYPE>(f[8 * j], f[8 * j + 1]),
-                           pack16<AB_TYPE>(f[8 * j + 2], f[8 * j + 3]),
-                           pack16<AB_TYPE>(f[8 * j + 4], f[8 * j + 5]),
-                           pack16<AB_TYPE>(f[8 * j + 6], f[8 * j + 7]));
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
           if (u.kind == kGrad) {
             // the row's targets in these columns: p - q, in their places
@@ -850,7 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *reinterpret_cast<uint16_t*>(
                       stg + lane * 128 + ((chunk ^ (lane & 7)) << 4) +
                       (c & 7) * 2) =
-                      (uint16_t)pack16<AB_TYPE>(pick(f, c) - g * part, 0.f);
+                      (uint16_t)pack16<AB_TYPE>(
+                          copysignf(pick(f, c), g) - g * part, 0.f);
                   part = 0.f;
                 }
               }

@@ -95,11 +95,14 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
       p.ids[t * p.top + rank] = id;
       p.weights[t * p.top + rank] = logs ? log_q : expf(log_q);
       // the blocks of 128 columns that start behind the entry before
-      uint16_t* starts = p.starts + t * p.blocks;
+      uint32_t* starts = p.starts + t * p.blocks;
       const int last = id == INT_MAX ? p.blocks - 1 : id >> 7;
-      for (int b = (prev >> 7) + 1; b <= last; ++b) starts[b] = (uint16_t)rank;
+      for (int b = (prev >> 7) + 1; b <= last; ++b)
+        starts[b] = rank | (id != INT_MAX && b == last ? id & 127
+                                                       : kVocabNone) << 16;
       if (rank == p.top - 1)
-        for (int b = last + 1; b < p.blocks; ++b) starts[b] = (uint16_t)p.top;
+        for (int b = last + 1; b < p.blocks; ++b)
+          starts[b] = p.top | kVocabNone << 16;
     }
   }
 }
@@ -584,7 +587,7 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   take(&c->ids, rows * top * 4);
   take(&c->weights, rows * top * 4);
   c->blocks = (int)((V + 127) / 128);
-  take(&c->starts, rows * c->blocks * 2);
+  take(&c->starts, rows * c->blocks * 4);
   c->ldxp = up(D, 8);
   char* bytes = nullptr;
   take(&bytes, up(rows, 64) * c->ldxp * 2);
