@@ -350,11 +350,13 @@ struct Walk {
 };
 
 // What of a row's targets is read a tile ahead: the target itself, or where
-// the teacher's entries for its columns start.
+// the teacher's entries for its columns start (a tile's second half may lie
+// in a block of columns past the vocabulary, where no entry is).
 __device__ __forceinline__ int peek(const VocabCall& p, long long t,
                                     int column) {
-  return p.targets ? (int)p.targets[t]
-                   : (int)p.starts[t * p.blocks + (column >> 7)];
+  if (p.targets) return (int)p.targets[t];
+  if (column >= p.V) return (int)(kVocabNone << 16);
+  return (int)p.starts[t * p.blocks + (column >> 7)];
 }
 
 // A row's entries from a column on, four of them ahead in registers: the

@@ -379,3 +379,119 @@ def test_offsets_past_32_bits():
                base * X.abs()).sum(0)
     assert bool(((got["dw"][cold].double() - want).abs() <= lim).all())
     assert G.device_status() == 0
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+def test_pieces_of_the_vocabulary(op):
+    """More logits than one piece of G holds: several launches, a shorter
+    last piece, dX added up over them, some tokens ignored."""
+    T, V, D = 8200, 20011, 72
+    if op == "ce":
+        x, w, y, g = ce_case(T, V, D, BF16, ignored=0.1)
+        got, want = run_ce(x, w, y, g), want_ce(x, w, y, g)
+    else:
+        x, w, u, ids, g = kd_case(T, V, D, 7, F16)
+        got = run_kd(x, w, u, ids, g, 2.0)
+        want = want_kd(x, w, u, ids, g, 2.0)
+    check(got, want, ALL)
+
+
+@pytest.mark.parametrize("T,V", [(8200, 7000), (2100, 6500), (1500, 20011)])
+def test_entries_stay_inside_the_vocabulary(T, V):
+    """Whole tiles whose second half lies past an odd number of blocks of 128
+    columns: no entry there."""
+    x, w, u, ids, g = kd_case(T, V, 72, 7, F16)
+    check(run_kd(x, w, u, ids, g, 2.0), want_kd(x, w, u, ids, g, 2.0), ALL)
+
+
+@pytest.mark.parametrize("T,V,D", [(9000, 600, 40), (5000, 260, 520),
+                                   (20, 12000, 72), (600, 9000, 264),
+                                   (257, 40000, 64)])
+def test_cuts_of_the_gradients(T, V, D):
+    """Deep sums over tokens (dW in slots) and over the vocabulary (dX in
+    many slots), with one and several rows of tiles."""
+    x, w, y, g = ce_case(T, V, D, BF16, ignored=0.05)
+    check(run_ce(x, w, y, g), want_ce(x, w, y, g), ALL)
+
+
+def test_close_ids_of_one_token():
+    """All entries of a token in a few neighbouring columns, and at the ends
+    of the vocabulary."""
+    T, V, D, top = 300, 1111, 72, 40
+    x, w, _, g = ce_case(T, V, D, BF16)
+    at = torch.arange(top, device=DEV)
+    first = torch.randint(0, V - top, (T, 1), device=DEV)
+    first[:100] = V - top
+    first[100:200] = 0
+    ids = first + at.flip(0)
+    u = torch.randn(T, top, device=DEV)
+    check(run_kd(x, w, u, ids, g, 1.0), want_kd(x, w, u, ids, g, 1.0), ALL)
+
+
+def test_negative_gradients():
+    x, w, u, ids, g = kd_case(200, 700, 72, 9, F16)
+    g = torch.where(torch.arange(200, device=DEV) % 2 == 0, g, -g)
+    check(run_kd(x, w, u, ids, g, 2.0), want_kd(x, w, u, ids, g, 2.0), ALL)
+    x, w, y, g = ce_case(200, 700, 72, BF16, ignored=0.2)
+    check(run_ce(x, w, y, -g), want_ce(x, w, y, -g), ALL)
+
+
+def test_masked_columns():
+    """Rows of w that put whole stretches of the vocabulary at -inf."""
+    T, V, D = 100, 900, 64
+    x, w, y, g = ce_case(T, V, D, BF16)
+    x[:, 0] = 1.0
+    y = y % 200
+    w[300:700] = 0
+    w[300:700, 0] = -math.inf
+    loss, lse = L.cross_entropy(x, w, y)
+    live = torch.cat([w[:300], w[700:]])
+    want = want_ce(x, live, y, None)
+    check({"loss": loss, "lse": lse}, want, ("loss", "lse"))
+
+
+def test_a_wait_that_runs_out_is_reported():
+    x, w, y, g = ce_case(300, 600, 72, BF16)
+    run_ce(x, w, y, g)
+    torch.cuda.synchronize()
+    old = G.set_wait_timeout_ns(20_000_000)
+    G.set_debug_flags(G.DEBUG_STALL_PRODUCER)
+    try:
+        run_ce(x, w, y, g)
+        torch.cuda.synchronize()
+        assert G.device_status() == 4
+    finally:
+        G.set_debug_flags(0)
+        G.set_wait_timeout_ns(old)
+    assert G.device_status() == 0
+    check(run_ce(x, w, y, g), want_ce(x, w, y, g), ALL)
+
+
+def test_two_streams():
+    cases = [ce_case(300, 5000, 136, BF16, seed) for seed in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        got = []
+        for case, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(run_ce(*case))
+    torch.cuda.synchronize()
+    for g, case in zip(got, cases):
+        check(g, want_ce(*case), ALL)
+
+
+def test_example_learns():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(__file__), "..", "examples",
+                        "train_head.py")
+    spec = importlib.util.spec_from_file_location("train_head", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    history = module.train(steps=6, tokens=512, vocab=1500, width=128)
+    first, last = history[0], history[-1]
+    assert abs(first[0] - math.log(1500)) < 1e-3  # a matrix of zeros
+    assert last[0] < first[0] and last[1] < first[1]
+    assert G.device_status() == 0
