@@ -19,7 +19,6 @@
 //   3. the results from the products' partial ones.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 #include "gemm_f32.h"
@@ -568,9 +567,12 @@ bool fits_tensor_map(const void* p, int64_t ld) {
 // `ws` and only numbers where it is null.
 int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
                 int64_t top, bool grad, bool pack_w) {
-  int64_t kMostG = 128ll << 20;
-  if (const char* env = std::getenv("VOCAB_PIECE_MB"))
-    kMostG = (int64_t)std::atoi(env) << 20;
+  // A piece's G: small enough that it and its part of W stay near the L2
+  // they are read from again (1800 learnt tokens of 6000, 65537 × 2048: 32,
+  // 64, 128, 256 MB 1560, 1400, 1350, 1500 us a step), large enough that a
+  // launch's ends do not count (4096 × 128000 × 4096: within 2 % from 64 MB
+  // on).  dX's slots: five of the largest dX (8192 × 4096) in question.
+  constexpr int64_t kMostG = 128ll << 20;
   constexpr int64_t kMostSlots = 768ll << 20;
   constexpr int64_t kMostDwSlots = 128ll << 20;
   const int64_t rows = std::max<int64_t>(T, 1);
