@@ -58,11 +58,17 @@ constexpr int kTmemCols = 512;
 constexpr long long kDrainNs = 2000000000LL;
 constexpr uint32_t kSleepNs = 100000;
 constexpr float kLog2e = 1.4426950408889634f;
-// Stats: steps summed in the tensor cores before the epilogue adds them to
-// its own fp32 sums.  The accumulator drops bits below its last at every
-// step, always towards zero; at a depth of 2048 to 4096 the losses' error
-// against 64 bits was 1-3e-6 without this.
-constexpr int kSumSteps = 16;
+// Stats: steps that an accumulator in tensor memory sums before the epilogue
+// adds them to its own fp32 sums.  It drops bits below its last at every
+// step, towards zero: 2048 to 4096 deep, the losses' error against 64 bits
+// was 1-3e-6 with one sum.  At 2048 × 50021 × 768 (12 steps) it is 2.1e-7,
+// with 8, 4 and 2 steps a sum 1.5e-7, 1.3e-7 and 1.2e-7 at 6, 26 and 60 % more
+// time.  One row of tiles sums 8: few tokens' errors do not average out, and
+// it waits for W (one token, 32000 × 768, median of 24: 4.1e-7 with 16,
+// 2.4e-7 with 8, 1.5e-7 with 4; 21.3, 22.6 and 24.1 us).
+__device__ __forceinline__ int sum_steps(int tiles_m) {
+  return tiles_m == 1 ? 8 : 16;
+}
 
 enum Kind { kStats, kGrad, kDw, kDx };
 
@@ -562,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes else
         const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
         int kb = u.kb0;
+        const int most = FORWARD ? sum_steps(walk.tiles_m) : INT_MAX;
         do {  // one sum; Stats: several to a tile
-          const int end =
-              FORWARD && u.kb1 - kb > kSumSteps ? kb + kSumSteps : u.kb1;
+          const int end = u.kb1 - kb > most ? kb + most : u.kb1;
           const int b = i & 1;
           if (i >= 2 && !bounded_wait(acc_empty(b), ((i >> 1) - 1) & 1, wc.limit,
                                       abort, 0)) {
@@ -656,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool more = look_ahead();
     if constexpr (FORWARD) {
+      const int most = sum_steps(walk.tiles_m);
       for (;; first_pass = false) {
         int token = 0, seen = 0;
         if (first_pass) {
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = u.wide >> 1;  // this warp's columns
         const int n0 = u.tn * u.wide + h * half;
         uint32_t acc = my_tmem;
-        const bool several = u.kb1 - u.kb0 > kSumSteps;
+        const bool several = u.kb1 - u.kb0 > most;
         if (several) {
           // several sums: added here, and put in the last one's place
           if (!arrived(acc)) break;
@@ -678,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float f[128];
 #pragma unroll
           for (int c = 0; c < 128; ++c) f[c] = 0.f;
-          for (int kb = u.kb0;; kb += kSumSteps) {
+          for (int kb = u.kb0;; kb += most) {
 #pragma unroll
             for (int c = 0; c < 128; c += 16) {
               if (c >= half) break;
@@ -688,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
             }
-            if (kb + kSumSteps >= u.kb1) break;
+            if (kb + most >= u.kb1) break;
             release();
             if (!arrived(acc)) break;
             acc += h * half;
