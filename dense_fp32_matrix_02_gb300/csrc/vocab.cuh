@@ -104,6 +104,7 @@ struct VocabCall {
 
   int pairs;  // CTA pairs of the products
   int wide;   // columns of the logits' tiles if all tokens are learnt from
+  unsigned int* status;  // where a bounds check reports
 
   // ---- workspace
   VocabHeader* header;   // null: nothing is numbered or packed, row t is

@@ -687,13 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 128; ++c) f[c] = 0.f;
           for (int kb = u.kb0;; kb += most) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 16) {
+            for (int c = 0; c < 128; c += 8) {
               if (c >= half) break;
-              uint32_t v[16];
-              tmem_ld16(acc + c, v);
+              uint32_t v[8];
+              if (tmem_span_ok(acc + c, 8, tmem, kTmemCols, q, wc.status))
+                tmem_ld8(acc + c, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 8; ++j) f[c + j] += __uint_as_float(v[j]);
             }
             if (kb + most >= u.kb1) break;
             release();
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!first_pass) more = look_ahead();
         Entries e;
         e.none();
-        if (r < learnt) e.start<false>(p, token, n0, seen);
+        if (!first_pass && r < learnt) e.start<false>(p, token, n0, seen);
         if (!several) {
           if (!first_pass && !arrived(acc)) break;
           acc += h * half;
@@ -723,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float f[32];
           {
             uint32_t v[32];
-            tmem_ld32(acc + c, v);
+            if (tmem_span_ok(acc + c, 32, tmem, kTmemCols, q, wc.status))
+              tmem_ld32(acc + c, v);
             tmem_ld_wait();
             if (c + 32 == half && !first_pass) release();
 #pragma unroll
@@ -732,8 +734,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n >= p.V) continue;  // (after the release)
           while (__any_sync(0xffffffffu, e.id[0] < n + 32)) {
             if (e.id[0] < n + 32) {
-              p.picked[(long long)r * p.top + e.at] =
-                  pick(f, e.id[0] - n) * p.inv_tau;
+              float* to = p.picked + (long long)r * p.top + e.at;
+              if (span_ok(to, 4, p.picked, 4ll * p.T * p.top, wc.status))
+                *to = pick(f, e.id[0] - n) * p.inv_tau;
               e.pass<false>();
             }
             __syncwarp();
@@ -758,9 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           peak = now;
         }
         if (first_pass || n0 >= p.V) continue;
-        if (r < learnt)
-          p.stats[(long long)(u.tn * 2 + h) * learnt + r] =
-              make_float2(peak, sum);
+        float2* to = p.stats + (long long)(u.tn * 2 + h) * learnt + r;
+        if (r < learnt &&
+            span_ok(to, 8, p.stats,
+                    8ll * ((2ll * p.V + u.wide - 1) / u.wide) * learnt,
+                    wc.status))
+          *to = make_float2(peak, sum);
       }
     } else {
       // staging: row (lane) of 128 bytes, its 16-byte chunk j at j ^ (row
@@ -797,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cols = u.kind == kGrad ? INT_MAX : p.D;
         Entries e;
         e.none();
-        if (u.kind == kGrad && r < learnt)
+        if (!first_pass && u.kind == kGrad && r < learnt)
           e.start<true>(p, token, walk.grad_v0 + n0, seen);
         // sums in fp32 slots
         const bool wide =
@@ -807,7 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c0 = 0; c0 < half; c0 += 32) {
           uint32_t v[32];
-          tmem_ld32(acc + h * half + c0, v);
+          if (tmem_span_ok(acc + h * half + c0, 32, tmem, kTmemCols, q,
+                           wc.status))
+            tmem_ld32(acc + h * half + c0, v);
           tmem_ld_wait();
           if (c0 + 32 == half && !first_pass) release();
           const int n = n0 + c0;
@@ -845,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
               if (u.kind == kDx) {
-                if (m0 < learnt) {
+                if (!first_pass && m0 < learnt) {
                   if (phase == 1)  // the first piece
                     tma_store_2d(&maps.slots, stg_s, n,
                                  u.slot * slot_rows + m0);
@@ -898,11 +906,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e.pass<true>();
                 if (e.id[0] != column + c) {
                   const int chunk = (c0 & 32) / 8 + (c >> 3);
-                  *reinterpret_cast<uint16_t*>(
-                      stg + lane * 128 + ((chunk ^ (lane & 7)) << 4) +
-                      (c & 7) * 2) =
-                      (uint16_t)pack16<AB_TYPE>(
-                          copysignf(pick(f, c), g) - g * part, 0.f);
+                  unsigned char* to = stg + lane * 128 +
+                                      ((chunk ^ (lane & 7)) << 4) +
+                                      (c & 7) * 2;
+                  if (span_ok(to, 2, stg, kStagingBytes, wc.status))
+                    *reinterpret_cast<uint16_t*>(to) =
+                        (uint16_t)pack16<AB_TYPE>(
+                            copysignf(pick(f, c), g) - g * part, 0.f);
                   part = 0.f;
                 }
               }
@@ -925,11 +935,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   static_cast<uint16_t*>(p.dW) +
                   (long long)(walk.back_v0 + m0 + k) * p.lddw + nb +
                   2 * lane;
+              if (nb + 2 * lane >= cols ||
+                  !span_ok(to, min(4, 2 * (cols - nb - 2 * lane)), p.dW,
+                           2 * ((p.V - 1) * p.lddw + p.D), wc.status))
+                continue;
               if (nb + 2 * lane + 1 < cols &&
                   (reinterpret_cast<uintptr_t>(to) & 3u) == 0) {
                 *reinterpret_cast<uint32_t*>(to) = two;
               } else {
-                if (nb + 2 * lane < cols) to[0] = (uint16_t)two;
+                to[0] = (uint16_t)two;
                 if (nb + 2 * lane + 1 < cols) to[1] = (uint16_t)(two >> 16);
               }
             }

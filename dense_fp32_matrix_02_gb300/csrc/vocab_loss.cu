@@ -91,6 +91,9 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
         }
       }
       const float log_q = (u[i] - peak) - log_sum;
+      if (!span_ok(p.ids + t * p.top + rank, 4, p.ids, 4ll * p.T * p.top,
+                   p.status))
+        continue;
       p.ids[t * p.top + rank] = id;
       p.weights[t * p.top + rank] = logs ? log_q : expf(log_q);
       // the blocks of 128 columns that start behind the entry before
@@ -493,9 +496,14 @@ __device__ __forceinline__ void store16(__half* p, float v) {
   *p = __float2half_rn(v);
 }
 
+// (to: column i of a row of n, in a matrix at `base` of `rows` rows)
 template <typename T16>
 __device__ __forceinline__ void store_4(T16* to, float4 v, float scale, int i,
-                                        int n) {
+                                        int n, const void* base,
+                                        long long rows, long long ld,
+                                        unsigned int* status) {
+  if (!span_ok(to, 2 * min(4, n - i), base, 2 * ((rows - 1) * ld + n), status))
+    return;
   T16 o[4];
   store16(o, v.x * scale);
   store16(o + 1, v.y * scale);
@@ -541,7 +549,8 @@ __global__ void __launch_bounds__(256)
           p.tile_slots[group * wide + i / kVocabTile * high + (tm - group)];
       v = sum_slots<AHEAD>(p.slots + (long long)r * p.ld_slot + i, next, n);
     }
-    store_4(static_cast<T16*>(p.dX) + t * p.lddx + i, v, inv_scale, i, p.D);
+    store_4(static_cast<T16*>(p.dX) + t * p.lddx + i, v, inv_scale, i, p.D,
+            p.dX, p.T, p.lddx, p.status);
   }
   const int splits = h->dw_splits;
   if (splits == 1) return;
@@ -551,7 +560,8 @@ __global__ void __launch_bounds__(256)
     const int i = (int)(k - r * chunks) * 4;
     const float4 v = sum_slots<AHEAD>(
         p.dw_slots + 4 * k, (long long)p.dw_slot_rows * p.ld_slot, splits);
-    store_4(static_cast<T16*>(p.dW) + r * p.lddw + i, v, inv_scale, i, p.D);
+    store_4(static_cast<T16*>(p.dW) + r * p.lddw + i, v, inv_scale, i, p.D,
+            p.dW, p.V, p.lddw, p.status);
   }
 }
 
@@ -798,6 +808,7 @@ int run(const Request& r) {
   c.dX = r.dX, c.lddx = r.lddx;
   c.dW = r.dW, c.lddw = r.lddw;
   c.pairs = vocab_pairs(sms);
+  c.status = wc.status;
   c.wide = c.pieces > 1 ? kVocabTile
                         : vocab_tile_width(c.T, c.V, vocab_steps(c.D),
                                            r.grad ? 128 : 64, c.pairs);

@@ -495,3 +495,23 @@ def test_example_learns():
     assert abs(first[0] - math.log(1500)) < 1e-3  # a matrix of zeros
     assert last[0] < first[0] and last[1] < first[1]
     assert G.device_status() == 0
+
+
+def test_checked_build_runs_clean():
+    """The checked build, in a process of its own: no index leaves its
+    buffer, and every result is in its tolerance."""
+    import os
+    import subprocess
+    import sys
+
+    from dense_fp32_matrix_02_gb300 import build
+    path = build.build(checked=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    which = ("sizes or tokens or distillation or strides or inside or pieces"
+             " or cuts or close")
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k", which,
+         os.path.join(here, "test_gpu_loss.py")],
+        env=dict(os.environ, GEMM_F32_LIBRARY=path), cwd=here,
+        capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
