@@ -233,6 +233,49 @@ struct Unit {
   int slot;
 };
 
+// Division by a number known early, in four instructions: the compiler's own
+// takes some 150 cycles, and what finds a warp's next tile lies between two
+// epilogues, where nothing hides it (a tile of dW, 16 tokens: 5500 cycles,
+// 4900 with it; that step 363 -> 350 us, 8192 × 65536 × 1024 forward 669 ->
+// 664).
+struct Divisor {
+  unsigned d, m;
+  __device__ __forceinline__ void set(int by) {
+    d = by > 1 ? by : 1;
+    m = 0xffffffffu / d;
+  }
+  // (m is less than one below 2^32 / d, so the first quotient is right or one
+  // too small)
+  __device__ __forceinline__ int quotient(int n, int& rest) const {
+    unsigned q = __umulhi((unsigned)n, m), r = (unsigned)n - q * d;
+    if (r >= d) r -= d, ++q;
+    rest = (int)r;
+    return (int)q;
+  }
+};
+
+// The order of m × n tiles: tile_coords.
+struct Tiles {
+  int m;
+  Divisor group;  // tiles of a group of rows
+  __device__ __forceinline__ void set(int m_, int n) {
+    m = m_;
+    group.set(kVocabGroup * n);
+  }
+  __device__ __forceinline__ void coords(int j, int& tm, int& tn) const {
+    int in;
+    const int first = group.quotient(j, in) * kVocabGroup;
+    if (first + kVocabGroup <= m) {
+      tm = first + in % kVocabGroup;
+      tn = in / kVocabGroup;
+    } else {
+      const int rows = m - first;
+      tn = in / rows;
+      tm = first + in % rows;
+    }
+  }
+};
+
 // The walk of one pair over its units of a launch.  Gradients, launch i: dW
 // and dX of piece i - 1, whose G the last launch has just written, then Grad
 // of piece i.
@@ -246,6 +289,7 @@ struct Walk {
   int grad_v0, grad_n, back_v0, back_n;
   int wide, dw_wide;
   bool dx_first;
+  Tiles tiles, dw_tiles, dx_tiles;
 
   __device__ __forceinline__ Walk(const VocabCall& p, int learnt, int phase,
                                   int pair_, int pairs_)
@@ -259,6 +303,7 @@ struct Walk {
     wide = h ? h->wide : p.wide;
     tiles_n = ((FORWARD ? p.V : grad_n) + wide - 1) / wide;
     steps = vocab_steps(p.D);
+    tiles.set(tiles_m, tiles_n);
     dx_first = false;
     if (!FORWARD && phase == 0) {
       stage = 3;
@@ -270,7 +315,9 @@ struct Walk {
       dw_m = vocab_tiles(back_n);
       dw_steps = vocab_steps(learnt);
       splits = h->dw_splits;
+      dw_tiles.set(dw_m, dw_n);
       dx_m = tiles_m;
+      dx_tiles.set(dx_m, dx_n);
       dx_steps = vocab_steps(back_n);
       line = vocab_steps(p.piece);
       whole = h->dx_rounds * pairs;
@@ -287,7 +334,7 @@ struct Walk {
     u.kind = kDx;
     u.wide = kVocabTile;
     if (j < whole) {
-      tile_coords<kVocabGroup>(j, dx_m, dx_n, u.tm, u.tn);
+      dx_tiles.coords(j, u.tm, u.tn);
       u.kb0 = 0;
       u.kb1 = dx_steps;
       u.slot = 0;
@@ -297,7 +344,7 @@ struct Walk {
     if (x >= x1) return false;
     const int tile = x / line;
     const int end = min(x1, (tile + 1) * line);
-    tile_coords<kVocabGroup>(whole + tile, dx_m, dx_n, u.tm, u.tn);
+    dx_tiles.coords(whole + tile, u.tm, u.tn);
     // a shorter last piece is cut in proportion
     u.kb0 = x - tile * line;
     u.kb1 = end - tile * line;
@@ -318,15 +365,20 @@ struct Walk {
       j = pair;
     }
     if (stage == 0) {
-      const int tiles = dw_m * dw_n;
-      if (j < tiles * splits) {
+      const int all = dw_m * dw_n;
+      if (j < all * splits) {
         u.kind = kDw;
         u.wide = dw_wide;
-        u.slot = j / tiles;
-        tile_coords<kVocabGroup>(j - u.slot * tiles, dw_m, dw_n, u.tm, u.tn);
-        // (a depth of below 2^25 steps, 16 splits at most)
-        u.kb0 = dw_steps * u.slot / splits;
-        u.kb1 = dw_steps * (u.slot + 1) / splits;
+        u.slot = 0;
+        u.kb0 = 0;
+        u.kb1 = dw_steps;
+        if (splits > 1) {
+          u.slot = j / all;
+          // (a depth of below 2^25 steps, 16 splits at most)
+          u.kb0 = dw_steps * u.slot / splits;
+          u.kb1 = dw_steps * (u.slot + 1) / splits;
+        }
+        dw_tiles.coords(j - u.slot * all, u.tm, u.tn);
         j += pairs;
         return true;
       }
@@ -346,7 +398,7 @@ struct Walk {
     if (j >= tiles_m * tiles_n) return false;
     u.kind = FORWARD ? kStats : kGrad;
     u.wide = wide;
-    tile_coords<kVocabGroup>(j, tiles_m, tiles_n, u.tm, u.tn);
+    tiles.coords(j, u.tm, u.tn);
     u.kb0 = 0;
     u.kb1 = steps;
     u.slot = 0;
@@ -713,6 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Entries e;
         e.none();
         if (!first_pass && r < learnt) e.start<false>(p, token, n0, seen);
+        // the warp's first entry: most stretches of columns have none
+        int next = __reduce_min_sync(0xffffffffu, e.id[0]);
         if (!several) {
           if (!first_pass && !arrived(acc)) break;
           acc += h * half;
@@ -732,14 +786,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
           }
           if (n >= p.V) continue;  // (after the release)
-          while (__any_sync(0xffffffffu, e.id[0] < n + 32)) {
+          while (next < n + 32) {
             if (e.id[0] < n + 32) {
               float* to = p.picked + (long long)r * p.top + e.at;
               if (span_ok(to, 4, p.picked, 4ll * p.T * p.top, wc.status))
                 *to = pick(f, e.id[0] - n) * p.inv_tau;
               e.pass<false>();
             }
-            __syncwarp();
+            next = __reduce_min_sync(0xffffffffu, e.id[0]);
           }
           if (n + 32 > p.V) {
 #pragma unroll
@@ -805,11 +859,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         e.none();
         if (!first_pass && u.kind == kGrad && r < learnt)
           e.start<true>(p, token, walk.grad_v0 + n0, seen);
+        int next = __reduce_min_sync(0xffffffffu, e.id[0]);
         // sums in fp32 slots
         const bool wide =
             u.kind == kDx || (u.kind == kDw && header->dw_splits > 1);
         uint32_t acc = my_tmem;
         if (!first_pass && !arrived(acc)) break;
+        if (u.kind == kDw && !wide && !dw_direct) {
+          // Nothing to work out: 64 columns at a time, packed and stored.  With
+          // few tokens a tile is its epilogue alone, which waits for itself
+          // more than for anything else (16 tokens, 100000 × 2048: a step in
+          // 330 us, 352 with 32 columns at a time as below).
+#pragma unroll 1
+          for (int c0 = 0; c0 < half; c0 += 64) {
+            uint32_t v[64];
+            if (tmem_span_ok(acc + h * half + c0, 64, tmem, kTmemCols, q,
+                             wc.status)) {
+              tmem_ld32(acc + h * half + c0, v);
+              tmem_ld32(acc + h * half + c0 + 32, v + 32);
+            }
+            tmem_ld_wait();
+            if (c0 + 64 == half) release();
+            const int n = n0 + c0;
+            if (n >= p.D) continue;  // (after the release)
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+            const bool empty = u.kb0 == u.kb1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float lo = __uint_as_float(v[8 * j + 2 * k]);
+                float hi = __uint_as_float(v[8 * j + 2 * k + 1]);
+                if (AB_TYPE == 0) lo *= inv_scale, hi *= inv_scale;
+                w[k] = empty ? 0u : pack16<AB_TYPE>(lo, hi);
+              }
+              *reinterpret_cast<uint4*>(stg + lane * 128 +
+                                        ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (m0 < walk.back_n)
+                tma_store_2d(&maps.dw, stg_s, n, walk.back_v0 + m0);
+              bulk_commit_group();
+            }
+          }
+          continue;
+        }
 #pragma unroll 1
         for (int c0 = 0; c0 < half; c0 += 32) {
           uint32_t v[32];
@@ -870,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           // 16-bit, 64 columns: half a staged block at a time
-          if (u.kind == kDw) {
+          if (AB_TYPE == 0 && u.kind == kDw) {  // (bfloat16: 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
           }
@@ -899,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the row's targets in these columns: p - q, in their places
             const int column = walk.grad_v0 + n;
             float part = 0.f;
-            while (__any_sync(0xffffffffu, e.id[0] < column + 32)) {
+            while (next < column + 32) {
               if (e.id[0] < column + 32) {
                 const int c = e.id[0] - column;
                 part += e.q[0];  // an id may come again
@@ -916,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   part = 0.f;
                 }
               }
-              __syncwarp();
+              next = __reduce_min_sync(0xffffffffu, e.id[0]);
             }
           }
           // the block is whole, or its other half lies past the columns
