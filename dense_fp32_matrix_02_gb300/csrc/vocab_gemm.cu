@@ -63,11 +63,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // step, towards zero: 2048 to 4096 deep, the losses' error against 64 bits
 // was 1-3e-6 with one sum.  At 2048 × 50021 × 768 (12 steps) it is 2.1e-7,
 // with 8, 4 and 2 steps a sum 1.5e-7, 1.3e-7 and 1.2e-7 at 6, 26 and 60 % more
-// time.  One row of tiles sums 8: few tokens' errors do not average out, and
-// it waits for W (one token, 32000 × 768, median of 24: 4.1e-7 with 16,
-// 2.4e-7 with 8, 1.5e-7 with 4; 21.3, 22.6 and 24.1 us).
-__device__ __forceinline__ int sum_steps(int tiles_m) {
-  return tiles_m == 1 ? 8 : 16;
+// time.  The fewer the tokens, the less their errors average out, and one row
+// of tiles waits for W anyway: it sums 8 steps, or 4 for a few tokens (one
+// token, 32000 × 768, median of 24: 4.1e-7 with 16, 2.4e-7 with 8, 1.5e-7
+// with 4; 21.3, 22.8 and 24.4 us.  64 tokens, 100000 × 2048: 78 us with 8, 86
+// with 4).
+__device__ __forceinline__ int sum_steps(int learnt) {
+  return learnt <= 8 ? 4 : learnt <= kVocabTile ? 8 : 16;
 }
 
 enum Kind { kStats, kGrad, kDw, kDx };
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes else
         const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
         int kb = u.kb0;
-        const int most = FORWARD ? sum_steps(walk.tiles_m) : INT_MAX;
+        const int most = FORWARD ? sum_steps(learnt) : INT_MAX;
         do {  // one sum; Stats: several to a tile
           const int end = u.kb1 - kb > most ? kb + most : u.kb1;
           const int b = i & 1;
@@ -714,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool more = look_ahead();
     if constexpr (FORWARD) {
-      const int most = sum_steps(walk.tiles_m);
+      const int most = sum_steps(learnt);
       for (;; first_pass = false) {
         int token = 0, seen = 0;
         if (first_pass) {
@@ -739,14 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 128; ++c) f[c] = 0.f;
           for (int kb = u.kb0;; kb += most) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 8) {
+            for (int c = 0; c < 128; c += 16) {
               if (c >= half) break;
-              uint32_t v[8];
-              if (tmem_span_ok(acc + c, 8, tmem, kTmemCols, q, wc.status))
-                tmem_ld8(acc + c, v);
+              uint32_t v[16];
+              if (tmem_span_ok(acc + c, 16, tmem, kTmemCols, q, wc.status))
+                tmem_ld16(acc + c, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) f[c + j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
             }
             if (kb + most >= u.kb1) break;
             release();
