@@ -449,8 +449,8 @@ GEMM_F32_API int gemm_f32_host_chunks(int64_t M, int64_t N, int sm_count,
  * Tokens that are not learnt from.  A target outside [0, V) marks one; so
  * does a distillation row in which no entry counts (an entry counts unless
  * its id is outside [0, V) or its logit is −Inf).  Their loss and lse are 0,
- * they add nothing to dW and their row of dX is 0; their row of X is never
- * read (it may hold NaN), and no work is done for it.
+ * they add nothing to dW and their row of dX is 0; nothing depends on what
+ * their row of X holds (it may be NaN).
  *
  * The _grad forms take lse as the forward call returned it and the gradient
  * of each token's loss, g_t = grad_loss[t·grad_stride] (grad_stride 0: one
