@@ -16,6 +16,10 @@ constexpr int kVocabTile = 256;      // rows and columns of an output tile
 constexpr int kVocabMaxPairs = 128;  // CTA pairs of a launch
 constexpr int kVocabMaxDwSplits = 16;
 constexpr int kVocabGroup = 16;  // tile rows walked together (L2 reuse)
+// The most tokens, words and columns a call may have: rows and columns are
+// 32-bit numbers, and so is what lies past the last of them, up to one piece
+// of the vocabulary (2^18 words at most) and a tile.
+constexpr long long kVocabMost = (1ll << 31) - (1ll << 20);
 
 __host__ __device__ inline int vocab_tiles(long long n) {
   return (int)((n + kVocabTile - 1) / kVocabTile);

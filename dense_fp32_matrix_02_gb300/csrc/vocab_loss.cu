@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(1024)
   const int lane = threadIdx.x & 31, j0 = lane >> 3;
   const int learnt = p.header ? p.header->learnt : p.T;
   const int wide = p.header ? p.header->wide : p.wide;
-  const int parts = (2 * p.V + wide - 1) / wide;  // half tiles
+  const int parts = (int)((2ll * p.V + wide - 1) / wide);  // half tiles
   bool here = r < learnt;
   // the first warp's later loads, ahead of the statistics'
   long long t = r;
@@ -702,7 +702,7 @@ int check(const Request& r) {
     if (r.grad ? (!r.lse || !r.grad_loss || !r.dX) : (!r.loss || !r.lse_out))
       return GEMM_F32_ERR_INVALID_ARG;
   }
-  if (r.T > 0x7fffffff || r.V > 0x7fffffff || r.D > 0x7fffffff)
+  if (r.T > kVocabMost || r.V > kVocabMost || r.D > kVocabMost)
     return GEMM_F32_ERR_UNSUPPORTED;
   return GEMM_F32_OK;
 }
@@ -900,7 +900,7 @@ int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V, int64_t D,
   if (T < 0 || V < 1 || D < 1 || top < 1 || top > kVocabMaxTop ||
       (grad != 0 && grad != 1) || (aligned != 0 && aligned != 1))
     return -GEMM_F32_ERR_INVALID_ARG;
-  if (T > 0x7fffffff || V > 0x7fffffff || D > 0x7fffffff)
+  if (T > kVocabMost || V > kVocabMost || D > kVocabMost)
     return -GEMM_F32_ERR_UNSUPPORTED;
   VocabCall c = {};
   return lay_out(&c, nullptr, T, V, D, top, grad != 0, aligned == 0);

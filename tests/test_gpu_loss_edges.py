@@ -1,0 +1,68 @@
+"""The vocabulary losses on the GPU at the ends of their ranges: sizes,
+values and lengths at which counts overflow, terms vanish or sums run deep.
+
+Tolerances follow tests/vocab_reference.py where a test does not derive its
+own."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU-only machines
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from dense_fp32_matrix_02_gb300 import gemm as G  # noqa: E402
+from dense_fp32_matrix_02_gb300 import loss as L  # noqa: E402
+
+DEV = torch.device("cuda:0")
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def test_words_past_2_to_the_30():
+    """2^30 + 300 words: a tile's two halves are counted past 2^31.
+
+    All rows of w are 0 but a few, whose logits are 20 (a third of the
+    probability) and -3.  Sums of ones are exact in fp32 here; lse is allowed
+    1e-6 of itself and 2e-5, G one rounding to bfloat16 (2^-8) and lse's
+    error, the products' results another 2^-8 and 1e-5."""
+    V, D = 2**30 + 300, 8
+    w = torch.zeros(V, D, dtype=BF16, device=DEV)
+    hot = torch.tensor([3, 2**29 + 77, V - 1], device=DEV)
+    w[hot[0]] = 2.5
+    w[hot[1]] = -0.375
+    w[hot[2]] = 2.5
+    x = torch.ones(2, D, dtype=BF16, device=DEV)
+    x[1] = -1.0  # logits of -20, 3 and -20
+    y = torch.tensor([V - 1, 2**29 + 77], device=DEV)
+    g = torch.tensor([1.0, 2.0], device=DEV)
+    loss, lse = L.cross_entropy(x, w, y)
+    dx, dw = L.cross_entropy_grad(x, w, y, lse, g)
+
+    z = x.double() @ w[hot].double().t()
+    want = torch.log(torch.exp(z).sum(1) + (V - 3))
+    tol = 1e-6 * want + 2e-5
+    assert bool(((lse.double() - want).abs() <= tol).all()), lse
+    at = torch.stack([z[0, 2], z[1, 1]])
+    assert bool(((loss.double() - (want - at)).abs() <= 2 * tol).all())
+    p = torch.exp(z - want[:, None])
+    Q = torch.zeros_like(p)
+    Q[0, 2] = Q[1, 1] = 1.0
+    P = g.double()[:, None] * (p - Q)
+    dP = 2.0**-8 * P.abs() + g.double()[:, None] * p * (tol + 2e-5)[:, None]
+    for got, dG, GG, other in ((dx, dP, P, w[hot].double()),
+                               (dw[hot], dP.t(), P.t(), x.double())):
+        ref = GG @ other
+        lim = (dG @ other.abs() + (2.0**-8 + 1e-5) * ref.abs()
+               + 1e-5 * (GG.abs() @ other.abs()))
+        assert bool(((got.double() - ref).abs() <= lim).all()), (got, ref)
+    base = g.double() / torch.exp(want)  # every other row of dw
+    ref = (base[:, None] * x.double()).sum(0)
+    lim = (base * (2.0**-7 + tol + 3e-5)).sum() + 2.0**-8 * ref.abs()
+    cold = torch.tensor([0, 2**29, 2**30 + 17, V - 2], device=DEV)
+    assert bool(((dw[cold].double() - ref).abs() <= lim).all())
+    assert G.device_status() == 0
