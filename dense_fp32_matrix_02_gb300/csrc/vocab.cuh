@@ -20,6 +20,9 @@ constexpr int kVocabGroup = 16;  // tile rows walked together (L2 reuse)
 // 32-bit numbers, and so is what lies past the last of them, up to one piece
 // of the vocabulary (2^18 words at most) and a tile.
 constexpr long long kVocabMost = (1ll << 31) - (1ll << 20);
+// The most elements of X or W (no device holds more, and bytes of workspace
+// stay far inside 64 bits).
+constexpr long long kVocabMostElements = 1ll << 48;
 
 __host__ __device__ inline int vocab_tiles(long long n) {
   return (int)((n + kVocabTile - 1) / kVocabTile);

@@ -681,6 +681,12 @@ struct Request {
   gemm_f32_stream_t stream;
 };
 
+// Sizes (none negative) that the kernels and the workspace's bytes can count.
+bool countable(int64_t T, int64_t V, int64_t D) {
+  return T <= kVocabMost && V <= kVocabMost && D <= kVocabMost &&
+         T * D <= kVocabMostElements && V * D <= kVocabMostElements;
+}
+
 int check(const Request& r) {
   if (r.type != GEMM_F32_MIXED_BF16 && r.type != GEMM_F32_MIXED_F16)
     return GEMM_F32_ERR_INVALID_ARG;
@@ -702,13 +708,12 @@ int check(const Request& r) {
     if (r.grad ? (!r.lse || !r.grad_loss || !r.dX) : (!r.loss || !r.lse_out))
       return GEMM_F32_ERR_INVALID_ARG;
   }
-  if (r.T > kVocabMost || r.V > kVocabMost || r.D > kVocabMost)
-    return GEMM_F32_ERR_UNSUPPORTED;
+  if (!countable(r.T, r.V, r.D)) return GEMM_F32_ERR_UNSUPPORTED;
   return GEMM_F32_OK;
 }
 
 // Tiles, and the steps of a piece's products, are counted in 32 bits.
-bool countable(const VocabCall& c, const Request& r) {
+bool tiles_countable(const VocabCall& c, const Request& r) {
   const int64_t most = 1 << 30;
   const int64_t rows = vocab_tiles(r.T), wide = vocab_tiles(r.D);
   if (rows * (r.V / kVocabTile + 1) > most) return false;
@@ -782,7 +787,7 @@ int run(const Request& r) {
   if (!r.ws || (reinterpret_cast<uintptr_t>(r.ws) & 15u) != 0 ||
       r.ws_bytes < need)
     return GEMM_F32_ERR_INVALID_ARG;
-  if (!countable(c, r)) return GEMM_F32_ERR_UNSUPPORTED;
+  if (!tiles_countable(c, r)) return GEMM_F32_ERR_UNSUPPORTED;
   int sms = 0, cc = 0;
   WaitCfg wc;
   cudaError_t e = device_facts(&sms, &cc, &wc);
@@ -900,8 +905,7 @@ int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V, int64_t D,
   if (T < 0 || V < 1 || D < 1 || top < 1 || top > kVocabMaxTop ||
       (grad != 0 && grad != 1) || (aligned != 0 && aligned != 1))
     return -GEMM_F32_ERR_INVALID_ARG;
-  if (T > kVocabMost || V > kVocabMost || D > kVocabMost)
-    return -GEMM_F32_ERR_UNSUPPORTED;
+  if (!countable(T, V, D)) return -GEMM_F32_ERR_UNSUPPORTED;
   VocabCall c = {};
   return lay_out(&c, nullptr, T, V, D, top, grad != 0, aligned == 0);
 }

@@ -470,8 +470,9 @@ GEMM_F32_API int gemm_f32_host_chunks(int64_t M, int64_t N, int sm_count,
  * value and nothing is kept in it between calls.  T = 0: forward launches
  * nothing, the gradients write dW = 0.  V, D >= 1.
  * GEMM_F32_ERR_UNSUPPORTED on a GPU without tcgen05 (not sm_10x), for T, V
- * or D above 2^31 - 2^20, and where the tiles of T×V logits (256 × 256), or
- * the steps of a gradient's product over them, number more than 2^30;
+ * or D above 2^31 - 2^20, T·D or V·D above 2^48, and where the tiles of T×V
+ * logits (256 × 256), or the steps of a gradient's product over them, number
+ * more than 2^30;
  * GEMM_F32_ERR_INVALID_ARG also for an unknown type, a temperature that is
  * not a positive finite number, top outside [1, 256], leading dimensions
  * below the row widths, grad_stride < 0, and NULL operands.

@@ -29,3 +29,25 @@ def test_sizes_past_the_limit_are_unsupported(built_lib, name):  # noqa: F811
     for grad in (0, 1):
         assert lib.gemm_f32_vocab_workspace_size(
             sizes["T"], sizes["V"], sizes["D"], 1, grad, 1) > 0
+
+
+def test_workspace_bytes_do_not_overflow(built_lib):  # noqa: F811
+    """Operands of more than 2^48 elements are refused: their bytes of
+    workspace, 2^64 and more, came out as small or negative numbers."""
+    from dense_fp32_matrix_02_gb300 import gemm
+    size = gemm.lib().gemm_f32_vocab_workspace_size
+    for T, V, D in ((MOST, MOST, MOST), (MOST, 8, MOST), (8, MOST, MOST),
+                    (2**30, 8, 2**19), (8, 2**30, 2**19)):
+        for grad in (0, 1):
+            for aligned in (0, 1):
+                assert size(T, V, D, 256, grad, aligned) == -NO, (T, V, D)
+        wide = {"ldx": D, "ldw": D}
+        assert ce(gemm.lib(), T=T, V=V, D=D, n=2**62, **wide) == NO
+        assert ce_grad(gemm.lib(), T=T, V=V, D=D, n=2**62, **wide, lddx=D,
+                       lddw=D) == NO
+    # the largest that are left: at least X's copy, W's and the targets'
+    for T, V, D in ((2**30, 8, 2**18), (8, 2**30, 2**18), (MOST, MOST, 2**16),
+                    (MOST, MOST, 1)):
+        for grad in (0, 1):
+            got = size(T, V, D, 256, grad, 0)
+            assert 2 * (T + V) * D + 8 * T * 256 < got < 2**60, (T, V, D)
