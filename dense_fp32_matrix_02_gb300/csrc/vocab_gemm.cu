@@ -1067,26 +1067,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  if (lane == 0 && warp < 2) {
-    if (warp == 0) {
-      if (*abort && rank == 0) {  // let the copies still in flight land
-        for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
-          if (!bounded_wait(full(k % kStages), (k / kStages) & 1, kDrainNs,
-                            nullptr, 0))
-            record_status(wc.status, kStatusTimeoutDrain);
-      }
-    } else {
-      // no product may still run when TMEM is freed, nor signal a CTA that
-      // has left: this is the last arrival in both CTAs
-      if (rank == 0) tc_commit2(mma_done);
-      if (!bounded_wait(mma_done, 0, kDrainNs, nullptr, 0))
+  if (lane == 0 && rank == 0 && warp == 0 && *abort) {
+    // let the copies still in flight land
+    for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
+      if (!bounded_wait(full(k % kStages), (k / kStages) & 1, kDrainNs,
+                        nullptr, 0))
         record_status(wc.status, kStatusTimeoutDrain);
-    }
   }
+  // the last arrival in both CTAs
+  if (lane == 0 && rank == 0 && warp == 1) tc_commit2(mma_done);
   griddep_launch_dependents();
   tc_fence_before_sync();
   __syncwarp();  // reconverge the warps whose roles ran on one lane
   __syncthreads();
+  // No product may still run when TMEM is freed, nor signal a CTA that has
+  // left.  Waited for here, when this CTA's epilogues are over and the last
+  // products with them: the second CTA's warp 1 has no other role, and a limit
+  // that began with the kernel would bound the whole launch.
+  if (warp == 1 && lane == 0 &&
+      !bounded_wait(mma_done, 0, kDrainNs, nullptr, 0))
+    record_status(wc.status, kStatusTimeoutDrain);
+  __syncwarp();
   cluster_sync_all();  // the pair's products and copies are over
   if (warp == 1) {
     tc_fence_after_sync();

@@ -66,3 +66,18 @@ def test_words_past_2_to_the_30():
     cold = torch.tensor([0, 2**29, 2**30 + 17, V - 2], device=DEV)
     assert bool(((dw[cold].double() - ref).abs() <= lim).all())
     assert G.device_status() == 0
+
+
+def test_a_launch_longer_than_a_wait_is_no_timeout():
+    """One launch of about five seconds, 2.5 times the limit of any one wait:
+    no wait of it lasts long, and none is reported.  All logits are 0, so
+    that lse is log V, within 2 ulp."""
+    n, D = 2**18, 49152
+    x = torch.zeros(n, D, dtype=BF16, device=DEV)
+    y = torch.zeros(n, dtype=torch.int64, device=DEV)
+    loss, lse = L.cross_entropy(x, x, y)
+    torch.cuda.synchronize()
+    assert G.device_status() == 0
+    want = math.log(n)
+    assert bool(((loss.double() - want).abs() <= 2.0**-19).all())
+    assert bool(((lse.double() - want).abs() <= 2.0**-19).all())
