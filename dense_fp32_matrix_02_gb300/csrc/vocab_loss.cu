@@ -432,11 +432,23 @@ __global__ void __launch_bounds__(1024)
       at = p.picked[(long long)r * p.top + j0];
     }
   }
+  // This thread's share, with what each addition rounds off kept (`lost`):
+  // 2^30 words are 65536 sums in a row, whose roundings, all one way where the
+  // sums are alike, left lse wrong by 4e-4.
   float2 st = make_float2(-INFINITY, 0.f);
+  float lost = 0.f;
   if (here) {
 #pragma unroll 4
-    for (int e = slice; e < parts; e += blockDim.x >> 3)
-      st = merge_stats(st, p.stats[(long long)e * learnt + r]);
+    for (int e = slice; e < parts; e += blockDim.x >> 3) {
+      const float2 b = p.stats[(long long)e * learnt + r];
+      const float m = fmaxf(st.x, b.x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float keep = exp2f(st.x - ref);
+      const float was = st.y * keep;
+      const float more = b.y * exp2f(b.x - ref) - lost * keep;
+      st = make_float2(m, was + more);
+      lost = (st.y - was) - more;
+    }
   }
   st = merge_over(st, 8);
   const int warps = blockDim.x >> 5;
