@@ -32,7 +32,9 @@ namespace {
 // Distillation: a token to a group of lanes, the smallest power of two that
 // gives each entry one (32 lanes for more).  log q (forward) or q over the
 // entries that count, which are ranked by (id, place) and written in that
-// order.
+// order.  The largest logit is subtracted before the division by τ: a logit
+// that stands for a mask, the type's lowest value, would overflow in it
+// (τ < 1) and count as no entry here, but as one where ids are read.
 constexpr int kTeacherWarps = 4;
 
 __global__ void __launch_bounds__(32 * kTeacherWarps)
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
       const int64_t id = p.top_ids[t * p.ldi + j];
       const bool counts = id >= 0 && id < p.V && l != -INFINITY;
       mine[j] = counts ? (int)id : INT_MAX;
-      if (counts) u[i] = l * p.inv_tau;
+      if (counts) u[i] = l;
       peak = fmaxf(peak, u[i]);
     }
   }
@@ -69,8 +71,11 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
     peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)  // u = -Inf (no entry) adds nothing
-    if (u[i] != -INFINITY) sum += expf(u[i] - peak);
+  for (int i = 0; i < kPer; ++i)
+    if (u[i] != -INFINITY) {  // (no entry)
+      u[i] = (u[i] - peak) * p.inv_tau;
+      sum += expf(u[i]);
+    }
   for (int o = wide >> 1; o; o >>= 1)
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float log_sum = logf(sum);
@@ -90,7 +95,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
           prev = max(prev, other);
         }
       }
-      const float log_q = (u[i] - peak) - log_sum;
+      const float log_q = u[i] - log_sum;
       if (!span_ok(p.ids + t * p.top + rank, 4, p.ids, 4ll * p.T * p.top,
                    p.status))
         continue;
@@ -464,7 +469,8 @@ __global__ void __launch_bounds__(1024)
   const float l = st.x * 0.69314718056f + logf(st.y);
   float sum = 0.f;
   for (int j = j0; id != INT_MAX;) {
-    sum += expf(lq) * (lq - (at - l));
+    const float q = expf(lq);
+    if (q != 0.f) sum += q * (lq - (at - l));  // 0·log 0 = 0
     j += 4;
     if (j >= p.top) break;
     id = p.ids[t * p.top + j];

@@ -16,6 +16,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover - CPU-only machines
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
+import vocab_reference as ref  # noqa: E402
 from dense_fp32_matrix_02_gb300 import gemm as G  # noqa: E402
 from dense_fp32_matrix_02_gb300 import loss as L  # noqa: E402
 
@@ -81,3 +82,50 @@ def test_a_launch_longer_than_a_wait_is_no_timeout():
     want = math.log(n)
     assert bool(((loss.double() - want).abs() <= 2.0**-19).all())
     assert bool(((lse.double() - want).abs() <= 2.0**-19).all())
+
+
+@pytest.mark.parametrize("tau", [0.25, 0.5, 1.0, 2.0])
+@pytest.mark.parametrize("T", [8, 300])
+def test_teacher_logits_of_the_lowest_value(T, tau):
+    """Masks that are the type's lowest value, not -inf: entries of weight 0
+    beside others; alone in their row, equal ones.  (At a temperature below 1
+    they overflowed and gave NaN, or took the token for one without entries.)
+    One word's own logit is -inf where a teacher's weight is 0."""
+    V, D = 300, 64
+    gen = torch.Generator(device=DEV).manual_seed(T)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device=DEV)
+
+    x, w = normal(T, D).to(BF16), (normal(V, D) / 4).to(BF16)
+    x[:, 0] = 1.0
+    w[299] = 0
+    w[299, 0] = -math.inf
+    low = torch.finfo(torch.float32).min
+    u = normal(T, 6)
+    ids = torch.randint(0, 299, (T, 6), generator=gen, device=DEV)
+    u[0::4, 2:] = low
+    u[1::4] = low
+    u[1, 3:] = -math.inf
+    u[2::4, 1] = -2e5
+    u[3::4, 5] = low
+    ids[3::4, 5] = 299
+    g = torch.rand(T, generator=gen, device=DEV) + 0.5
+
+    loss, lse = L.distill(x, w, u, ids, tau)
+    dx, dw = L.distill_grad(x, w, u, ids, lse, g, tau)
+    live = w[:299]  # word 299 has no probability and no weight
+    # (less each row's largest, beside which float64 would lose log 6)
+    ud = u.double() - u.double().amax(1, keepdim=True)
+    targets = ref.distill_targets(ud, ids.clamp(max=298), tau, 299)
+    want = ref.loss_and_grads(x, live, *targets, tau, g)
+    # its 0·(-Inf) in dx is no part of this: nor is it of the loss
+    got = {"loss": loss, "lse": lse, "dw": dw[:299]}
+    for name in got:
+        a, b, tol = got[name].double(), want[name], want[name + "_tol"]
+        assert bool(((a - b).abs() <= tol).all()), (name, a, b)
+    assert G.device_status() == 0
+    # and dx, without that word
+    loss, lse = L.distill(x, live, u, ids.clamp(max=298), tau)
+    dx, dw = L.distill_grad(x, live, u, ids.clamp(max=298), lse, g, tau)
+    assert bool(((dx.double() - want["dx"]).abs() <= want["dx_tol"]).all())
