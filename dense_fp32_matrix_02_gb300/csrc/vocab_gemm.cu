@@ -39,6 +39,7 @@
 #include <cudaTypedefs.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -58,18 +59,22 @@ constexpr int kTmemCols = 512;
 constexpr long long kDrainNs = 2000000000LL;
 constexpr uint32_t kSleepNs = 100000;
 constexpr float kLog2e = 1.4426950408889634f;
-// Stats: steps that an accumulator in tensor memory sums before the epilogue
-// adds them to its own fp32 sums.  It drops bits below its last at every
-// step, towards zero: 2048 to 4096 deep, the losses' error against 64 bits
+// Steps of a logit that an accumulator in tensor memory sums before the
+// epilogue adds them to its own fp32 sums.  It drops bits below its last at
+// every step, towards zero: 2048 to 4096 deep, the losses' error against 64 bits
 // was 1-3e-6 with one sum.  At 2048 × 50021 × 768 (12 steps) it is 2.1e-7,
 // with 8, 4 and 2 steps a sum 1.5e-7, 1.3e-7 and 1.2e-7 at 6, 26 and 60 % more
 // time.  The fewer the tokens, the less their errors average out, and one row
 // of tiles waits for W anyway: it sums 8 steps, or 4 for a few tokens (one
 // token, 32000 × 768, median of 24: 4.1e-7 with 16, 2.4e-7 with 8, 1.5e-7
 // with 4; 21.3, 22.8 and 24.4 us.  64 tokens, 100000 × 2048: 78 us with 8, 86
-// with 4).
-__device__ __forceinline__ int sum_steps(int learnt) {
-  return learnt <= 8 ? 4 : learnt <= kVocabTile ? 8 : 16;
+// with 4).  Grad sums as Stats does, to the bit: a token learnt by heart has
+// G = p - 1 at its target, all of it the difference of that logit and lse, and
+// is wrong by whatever the two calls' logits differ (by 1e-4, some times G
+// itself, with one sum in Grad 2048 to 4096 deep).  So the rule goes by what
+// both calls see: all tokens where the forward call may number none.
+__device__ __forceinline__ int sum_steps(const VocabCall& p, int learnt) {
+  return p.T <= 8 ? 4 : learnt <= kVocabTile ? 8 : 16;
 }
 
 enum Kind { kStats, kGrad, kDw, kDx };
@@ -397,6 +402,11 @@ struct Walk {
       // round of both dW and G
       j = pairs - 1 - pair;
     }
+    return next_logits(u);
+  }
+
+  // The logits' tiles, the last of a launch.
+  __device__ __forceinline__ bool next_logits(Unit& u) {
     if (j >= tiles_m * tiles_n) return false;
     u.kind = FORWARD ? kStats : kGrad;
     u.wide = wide;
@@ -622,8 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes else
         const uint32_t step_a = mn_a ? 2048 : 32, step_b = mn_b ? 2048 : 32;
         int kb = u.kb0;
-        const int most = FORWARD ? sum_steps(learnt) : INT_MAX;
-        do {  // one sum; Stats: several to a tile
+        const int most = u.kind == kStats || u.kind == kGrad
+                             ? sum_steps(p, learnt)
+                             : INT_MAX;
+        do {  // one sum; logits: several to a tile
           const int end = u.kb1 - kb > most ? kb + most : u.kb1;
           const int b = i & 1;
           if (i >= 2 && !bounded_wait(acc_empty(b), ((i >> 1) - 1) & 1, wc.limit,
@@ -691,6 +703,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++i;
     };
 
+    // Several sums of a tile: added here, and put in the last one's place.
+    // (acc: its address, this warp's columns.)
+    auto join_sums = [&](int half, int steps, int most,
+                         uint32_t& acc) -> bool {
+      if (!arrived(acc)) return false;
+      acc += h * half;
+      float f[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) f[c] = 0.f;
+      for (;; steps -= most) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (c >= half) break;
+          uint32_t v[16];
+          if (tmem_span_ok(acc + c, 16, tmem, kTmemCols, q, wc.status))
+            tmem_ld16(acc + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
+        }
+        if (steps <= most) break;
+        release();
+        if (!arrived(acc)) return false;
+        acc += h * half;
+      }
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {
+        if (c >= half) break;
+        tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(f + c));
+      }
+      tmem_st_wait();
+      return true;
+    };
+
     // The first pass is a dry run, on whatever TMEM holds and
     // with nothing stored: it brings the instructions in while the first
     // tile is being made (which they otherwise hold up by 2-3 us).
@@ -700,8 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit nu;
     int n_token = 0, n_seen = 0;
     float n_lse = 0.f, n_grad = 0.f;
-    auto look_ahead = [&]() -> bool {
-      if (!walk.next(nu)) return false;
+    auto look_ahead = [&](auto in_logits) -> bool {
+      if (!(decltype(in_logits)::value ? walk.next_logits(nu) : walk.next(nu)))
+        return false;
       const int r = nu.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
       if ((nu.kind == kStats || nu.kind == kGrad) && r < learnt) {
         n_token = learnt == p.T ? r : p.token[r];
@@ -714,9 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    bool more = look_ahead();
+    bool more = look_ahead(std::false_type());
     if constexpr (FORWARD) {
-      const int most = sum_steps(learnt);
+      const int most = sum_steps(p, learnt);
       for (;; first_pass = false) {
         int token = 0, seen = 0;
         if (first_pass) {
@@ -731,39 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = u.wide >> 1;  // this warp's columns
         const int n0 = u.tn * u.wide + h * half;
         uint32_t acc = my_tmem;
-        const bool several = u.kb1 - u.kb0 > most;
-        if (several) {
-          // several sums: added here, and put in the last one's place
-          if (!arrived(acc)) break;
-          acc += h * half;
-          float f[128];
-#pragma unroll
-          for (int c = 0; c < 128; ++c) f[c] = 0.f;
-          for (int kb = u.kb0;; kb += most) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 16) {
-              if (c >= half) break;
-              uint32_t v[16];
-              if (tmem_span_ok(acc + c, 16, tmem, kTmemCols, q, wc.status))
-                tmem_ld16(acc + c, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[c + j] += __uint_as_float(v[j]);
-            }
-            if (kb + most >= u.kb1) break;
-            release();
-            if (!arrived(acc)) break;
-            acc += h * half;
-          }
-          if (!ok) break;
-#pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            if (c >= half) break;
-            tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(f + c));
-          }
-          tmem_st_wait();
-        }
-        if (!first_pass) more = look_ahead();
+        const bool several = u.kb1 > most;
+        if (several && !join_sums(half, u.kb1, most, acc)) break;
+        if (!first_pass) more = look_ahead(std::true_type());
         Entries e;
         e.none();
         if (!first_pass && r < learnt) e.start<false>(p, token, n0, seen);
@@ -835,234 +852,248 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float grad_scale = p.tau * header->scale;
       const bool dw_direct = !vocab_maps(p.dW, p.lddw);
       const int slot_rows = vocab_tiles(learnt) * kVocabTile;
-      for (;; first_pass = false) {
-        int token = 0, seen = 0;
-        float shift = 0.f, g = 0.f;
-        if (first_pass) {
-          u = {phase == 0 ? kGrad : kDx, 1 << 20, 0, 128, 0, 1, 0};
-        } else {
-          if (!more) break;
-          u = nu;
-          token = n_token;
-          seen = n_seen;
-          // g·p is one exponential, 2^(z·c2 + log2 |g| - lse·log2 e), with
-          // g's sign (g = 0: the exponent is -Inf)
-          g = n_grad * grad_scale;
-          shift = log2f(fabsf(g)) - n_lse * kLog2e;
-          more = look_ahead();
-        }
-        const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
-        const int r = m0 + lane;
-        const int half = u.wide >> 1;  // this warp's columns
-        const int n0 = u.tn * u.wide + h * half;
-        // G is written to the end of its tiles
-        const int cols = u.kind == kGrad ? INT_MAX : p.D;
-        Entries e;
-        e.none();
-        if (!first_pass && u.kind == kGrad && r < learnt)
-          e.start<true>(p, token, walk.grad_v0 + n0, seen);
-        int next = __reduce_min_sync(0xffffffffu, e.id[0]);
-        // sums in fp32 slots
-        const bool wide =
-            u.kind == kDx || (u.kind == kDw && header->dw_splits > 1);
-        uint32_t acc = my_tmem;
-        if (!first_pass && !arrived(acc)) break;
-        if (u.kind == kDw && !wide && !dw_direct) {
-          // Nothing to work out: 64 columns at a time, packed and stored.  With
-          // few tokens a tile is its epilogue alone, which waits for itself
-          // more than for anything else (16 tokens, 100000 × 2048: a step in
-          // 330 us, 352 with 32 columns at a time as below).
+      const int most = sum_steps(p, learnt);
+      // dW's and dX's tiles, then the logits': a loop each, so that the sums
+      // of the logits share their registers with little else.
+      auto epilogues = [&](auto in_logits) {
+        constexpr bool LOGITS = decltype(in_logits)::value;
+        for (;; first_pass = false) {
+          int token = 0, seen = 0;
+          float shift = 0.f, g = 0.f;
+          if (first_pass) {
+            u = {LOGITS ? kGrad : kDx, 1 << 20, 0, 128, 0, 1, 0};
+          } else {
+            if (!more || (nu.kind == kGrad) != LOGITS) break;
+            u = nu;
+            token = n_token;
+            seen = n_seen;
+            // g·p is one exponential, 2^(z·c2 + log2 |g| - lse·log2 e), with
+            // g's sign (g = 0: the exponent is -Inf)
+            g = n_grad * grad_scale;
+            shift = log2f(fabsf(g)) - n_lse * kLog2e;
+          }
+          uint32_t acc = my_tmem;
+          const int wide_here = LOGITS && !first_pass ? walk.wide : u.wide;
+          const int half = wide_here >> 1;  // this warp's columns
+          const bool several = LOGITS && !first_pass && walk.steps > most;
+          if (several && !join_sums(half, walk.steps, most, acc)) break;
+          if (!first_pass) more = look_ahead(in_logits);
+          const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
+          const int r = m0 + lane;
+          const int n0 = u.tn * wide_here + h * half;
+          // G is written to the end of its tiles
+          const int cols = LOGITS ? INT_MAX : p.D;
+          Entries e;
+          e.none();
+          if (LOGITS && !first_pass && r < learnt)
+            e.start<true>(p, token, walk.grad_v0 + n0, seen);
+          int next = __reduce_min_sync(0xffffffffu, e.id[0]);
+          // sums in fp32 slots
+          const bool wide =
+              !LOGITS && (u.kind == kDx || header->dw_splits > 1);
+          if (!several) {
+            if (!first_pass && !arrived(acc)) break;
+            acc += h * half;
+          }
+          if (!LOGITS && u.kind == kDw && !wide && !dw_direct) {
+            // Nothing to work out: 64 columns at a time, packed and stored.  With
+            // few tokens a tile is its epilogue alone, which waits for itself
+            // more than for anything else (16 tokens, 100000 × 2048: a step in
+            // 330 us, 352 with 32 columns at a time as below).
 #pragma unroll 1
-          for (int c0 = 0; c0 < half; c0 += 64) {
-            uint32_t v[64];
-            if (tmem_span_ok(acc + h * half + c0, 64, tmem, kTmemCols, q,
-                             wc.status)) {
-              tmem_ld32(acc + h * half + c0, v);
-              tmem_ld32(acc + h * half + c0 + 32, v + 32);
-            }
-            tmem_ld_wait();
-            if (c0 + 64 == half) release();
-            const int n = n0 + c0;
-            if (n >= p.D) continue;  // (after the release)
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-            const bool empty = u.kb0 == u.kb1;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float lo = __uint_as_float(v[8 * j + 2 * k]);
-                float hi = __uint_as_float(v[8 * j + 2 * k + 1]);
-                if (AB_TYPE == 0) lo *= inv_scale, hi *= inv_scale;
-                w[k] = empty ? 0u : pack16<AB_TYPE>(lo, hi);
+            for (int c0 = 0; c0 < half; c0 += 64) {
+              uint32_t v[64];
+              if (tmem_span_ok(acc + c0, 64, tmem, kTmemCols, q,
+                               wc.status)) {
+                tmem_ld32(acc + c0, v);
+                tmem_ld32(acc + c0 + 32, v + 32);
               }
-              *reinterpret_cast<uint4*>(stg + lane * 128 +
-                                        ((j ^ (lane & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (m0 < walk.back_n)
-                tma_store_2d(&maps.dw, stg_s, n, walk.back_v0 + m0);
-              bulk_commit_group();
-            }
-          }
-          continue;
-        }
-#pragma unroll 1
-        for (int c0 = 0; c0 < half; c0 += 32) {
-          uint32_t v[32];
-          if (tmem_span_ok(acc + h * half + c0, 32, tmem, kTmemCols, q,
-                           wc.status))
-            tmem_ld32(acc + h * half + c0, v);
-          tmem_ld_wait();
-          if (c0 + 32 == half && !first_pass) release();
-          const int n = n0 + c0;
-          if (n >= cols) continue;  // (after the release)
-          float f[32];
+              tmem_ld_wait();
+              if (c0 + 64 == half) release();
+              const int n = n0 + c0;
+              if (n >= p.D) continue;  // (after the release)
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+              const bool empty = u.kb0 == u.kb1;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-          if (u.kind == kGrad) {
-            scale_add_32(f, c2, shift);
+              for (int j = 0; j < 8; ++j) {
+                uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = exp2_fast(f[j]);
-            // columns past the vocabulary are zeros, and (below) rows past
-            // the learnt tokens: Dw and Dx sum over them up to multiples of
-            // 64
-            if (n + 32 > walk.grad_n) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n + j >= walk.grad_n) f[j] = 0.f;
-            }
-          } else if (u.kb0 == u.kb1) {  // an empty sum
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = 0.f;
-          }
-          if (wide) {
-            // fp32, 32 columns: one staged block
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4*>(stg + lane * 128 +
-                                         ((j ^ (lane & 7)) << 4)) =
-                  make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2],
-                              f[4 * j + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (u.kind == kDx) {
-                if (!first_pass && m0 < learnt) {
-                  if (phase == 1)  // the first piece
-                    tma_store_2d(&maps.slots, stg_s, n,
-                                 u.slot * slot_rows + m0);
-                  else
-                    tma_add_2d(&maps.slots, stg_s, n,
-                               u.slot * slot_rows + m0);
+                for (int k = 0; k < 4; ++k) {
+                  float lo = __uint_as_float(v[8 * j + 2 * k]);
+                  float hi = __uint_as_float(v[8 * j + 2 * k + 1]);
+                  if (AB_TYPE == 0) lo *= inv_scale, hi *= inv_scale;
+                  w[k] = empty ? 0u : pack16<AB_TYPE>(lo, hi);
                 }
-              } else if (m0 < walk.back_n) {
-                tma_store_2d(&maps.dw_slots, stg_s, n,
-                             u.slot * p.dw_slot_rows + m0);
+                *reinterpret_cast<uint4*>(stg + lane * 128 +
+                                          ((j ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
               }
-              bulk_commit_group();
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (m0 < walk.back_n)
+                  tma_store_2d(&maps.dw, stg_s, n, walk.back_v0 + m0);
+                bulk_commit_group();
+              }
             }
             continue;
           }
-          // 16-bit, 64 columns: half a staged block at a time
-          if (AB_TYPE == 0 && u.kind == kDw) {  // (bfloat16: 1)
+#pragma unroll 1
+          for (int c0 = 0; c0 < half; c0 += 32) {
+            uint32_t v[32];
+            if (tmem_span_ok(acc + c0, 32, tmem, kTmemCols, q,
+                             wc.status))
+              tmem_ld32(acc + c0, v);
+            tmem_ld_wait();
+            if (c0 + 32 == half && !first_pass) release();
+            const int n = n0 + c0;
+            if (n >= cols) continue;  // (after the release)
+            float f[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
-          }
-          if ((c0 & 32) == 0) {
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-          }
-          uint32_t keep = 0xffffffffu, flip = 0;
-          if (u.kind == kGrad) {
-            keep = r < learnt ? 0xffffffffu : 0u;
-            flip = g < 0.f ? 0x80008000u : 0u;
-          }
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+            if (LOGITS) {
+              scale_add_32(f, c2, shift);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int chunk = (c0 & 32) / 8 + j;
-            uint32_t w[4];
+              for (int j = 0; j < 32; ++j) f[j] = exp2_fast(f[j]);
+              // columns past the vocabulary are zeros, and (below) rows past
+              // the learnt tokens: Dw and Dx sum over them up to multiples of
+              // 64
+              if (n + 32 > walk.grad_n) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = (pack16<AB_TYPE>(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]) ^
-                      flip) & keep;
-            *reinterpret_cast<uint4*>(stg + lane * 128 +
-                                      ((chunk ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          if (u.kind == kGrad) {
-            // the row's targets in these columns: p - q, in their places
-            const int column = walk.grad_v0 + n;
-            float part = 0.f;
-            while (next < column + 32) {
-              if (e.id[0] < column + 32) {
-                const int c = e.id[0] - column;
-                part += e.q[0];  // an id may come again
-                e.pass<true>();
-                if (e.id[0] != column + c) {
-                  const int chunk = (c0 & 32) / 8 + (c >> 3);
-                  unsigned char* to = stg + lane * 128 +
-                                      ((chunk ^ (lane & 7)) << 4) +
-                                      (c & 7) * 2;
-                  if (span_ok(to, 2, stg, kStagingBytes, wc.status))
-                    *reinterpret_cast<uint16_t*>(to) =
-                        (uint16_t)pack16<AB_TYPE>(
-                            copysignf(pick(f, c), g) - g * part, 0.f);
-                  part = 0.f;
+                for (int j = 0; j < 32; ++j)
+                  if (n + j >= walk.grad_n) f[j] = 0.f;
+              }
+            } else if (u.kb0 == u.kb1) {  // an empty sum
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = 0.f;
+            }
+            if (wide) {
+              // fp32, 32 columns: one staged block
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4*>(stg + lane * 128 +
+                                           ((j ^ (lane & 7)) << 4)) =
+                    make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2],
+                                f[4 * j + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (u.kind == kDx) {
+                  if (!first_pass && m0 < learnt) {
+                    if (phase == 1)  // the first piece
+                      tma_store_2d(&maps.slots, stg_s, n,
+                                   u.slot * slot_rows + m0);
+                    else
+                      tma_add_2d(&maps.slots, stg_s, n,
+                                 u.slot * slot_rows + m0);
+                  }
+                } else if (m0 < walk.back_n) {
+                  tma_store_2d(&maps.dw_slots, stg_s, n,
+                               u.slot * p.dw_slot_rows + m0);
+                }
+                bulk_commit_group();
+              }
+              continue;
+            }
+            // 16-bit, 64 columns: half a staged block at a time
+            if (AB_TYPE == 0 && !LOGITS) {  // (bfloat16: 1)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
+            }
+            if ((c0 & 32) == 0) {
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+            }
+            uint32_t keep = 0xffffffffu, flip = 0;
+            if (LOGITS) {
+              keep = r < learnt ? 0xffffffffu : 0u;
+              flip = g < 0.f ? 0x80008000u : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int chunk = (c0 & 32) / 8 + j;
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = (pack16<AB_TYPE>(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]) ^
+                        flip) & keep;
+              *reinterpret_cast<uint4*>(stg + lane * 128 +
+                                        ((chunk ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (LOGITS) {
+              // the row's targets in these columns: p - q, in their places
+              const int column = walk.grad_v0 + n;
+              float part = 0.f;
+              while (next < column + 32) {
+                if (e.id[0] < column + 32) {
+                  const int c = e.id[0] - column;
+                  part += e.q[0];  // an id may come again
+                  e.pass<true>();
+                  if (e.id[0] != column + c) {
+                    const int chunk = (c0 & 32) / 8 + (c >> 3);
+                    unsigned char* to = stg + lane * 128 +
+                                        ((chunk ^ (lane & 7)) << 4) +
+                                        (c & 7) * 2;
+                    if (span_ok(to, 2, stg, kStagingBytes, wc.status))
+                      *reinterpret_cast<uint16_t*>(to) =
+                          (uint16_t)pack16<AB_TYPE>(
+                              copysignf(pick(f, c), g) - g * part, 0.f);
+                    part = 0.f;
+                  }
+                }
+                next = __reduce_min_sync(0xffffffffu, e.id[0]);
+              }
+            }
+            // the block is whole, or its other half lies past the columns
+            if ((c0 & 32) == 0 && n + 32 < cols) continue;
+            const int nb = n - (c0 & 32);
+            if (!LOGITS && dw_direct) {
+              // rows on any 2-byte boundary: a warp writes 64 columns of one
+              // row at a time
+              __syncwarp();
+              const int rows = min(32, walk.back_n - m0);
+              for (int k = 0; k < rows; ++k) {
+                const uint32_t two = *reinterpret_cast<const uint32_t*>(
+                    stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) +
+                    (lane & 3) * 4);
+                uint16_t* to =
+                    static_cast<uint16_t*>(p.dW) +
+                    (long long)(walk.back_v0 + m0 + k) * p.lddw + nb +
+                    2 * lane;
+                if (nb + 2 * lane >= cols ||
+                    !span_ok(to, min(4, 2 * (cols - nb - 2 * lane)), p.dW,
+                             2 * ((p.V - 1) * p.lddw + p.D), wc.status))
+                  continue;
+                if (nb + 2 * lane + 1 < cols &&
+                    (reinterpret_cast<uintptr_t>(to) & 3u) == 0) {
+                  *reinterpret_cast<uint32_t*>(to) = two;
+                } else {
+                  to[0] = (uint16_t)two;
+                  if (nb + 2 * lane + 1 < cols) to[1] = (uint16_t)(two >> 16);
                 }
               }
-              next = __reduce_min_sync(0xffffffffu, e.id[0]);
-            }
-          }
-          // the block is whole, or its other half lies past the columns
-          if ((c0 & 32) == 0 && n + 32 < cols) continue;
-          const int nb = n - (c0 & 32);
-          if (u.kind == kDw && dw_direct) {
-            // rows on any 2-byte boundary: a warp writes 64 columns of one
-            // row at a time
-            __syncwarp();
-            const int rows = min(32, walk.back_n - m0);
-            for (int k = 0; k < rows; ++k) {
-              const uint32_t two = *reinterpret_cast<const uint32_t*>(
-                  stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) +
-                  (lane & 3) * 4);
-              uint16_t* to =
-                  static_cast<uint16_t*>(p.dW) +
-                  (long long)(walk.back_v0 + m0 + k) * p.lddw + nb +
-                  2 * lane;
-              if (nb + 2 * lane >= cols ||
-                  !span_ok(to, min(4, 2 * (cols - nb - 2 * lane)), p.dW,
-                           2 * ((p.V - 1) * p.lddw + p.D), wc.status))
-                continue;
-              if (nb + 2 * lane + 1 < cols &&
-                  (reinterpret_cast<uintptr_t>(to) & 3u) == 0) {
-                *reinterpret_cast<uint32_t*>(to) = two;
-              } else {
-                to[0] = (uint16_t)two;
-                if (nb + 2 * lane + 1 < cols) to[1] = (uint16_t)(two >> 16);
+              __syncwarp();
+            } else {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (LOGITS) {
+                  if (!first_pass)
+                    tma_store_2d(&maps.g_out, stg_s, nb, g_out + m0);
+                } else if (m0 < walk.back_n)
+                  tma_store_2d(&maps.dw, stg_s, nb, walk.back_v0 + m0);
+                bulk_commit_group();
               }
-            }
-            __syncwarp();
-          } else {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (u.kind == kGrad) {
-                if (!first_pass)
-                  tma_store_2d(&maps.g_out, stg_s, nb, g_out + m0);
-              } else if (m0 < walk.back_n)
-                tma_store_2d(&maps.dw, stg_s, nb, walk.back_v0 + m0);
-              bulk_commit_group();
             }
           }
         }
-      }
+      };
+      if (phase > 0) epilogues(std::false_type());
+      if (phase < p.pieces) epilogues(std::true_type());
       if (lane == 0) bulk_wait_group<0>();
     }
   }

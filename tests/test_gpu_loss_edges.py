@@ -129,3 +129,59 @@ def test_teacher_logits_of_the_lowest_value(T, tau):
     loss, lse = L.distill(x, live, u, ids.clamp(max=298), tau)
     dx, dw = L.distill_grad(x, live, u, ids.clamp(max=298), lse, g, tau)
     assert bool(((dx.double() - want["dx"]).abs() <= want["dx_tol"]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,D", [(5, 4096), (64, 1024), (64, 4096),
+                                 (600, 2048), (600, 4096)])
+def test_gradients_of_tokens_learnt_by_heart(T, D, dtype):
+    """G = p - 1 at the target of a token whose p is nearly 1 is the
+    difference of a logit and lse: the two calls have to make the logits
+    alike.  Seen in dw's row of each target (no two are the same), along its
+    token's x.
+
+    p's error: lse is rounded to fp32 below 32 (2^-20), and again where it is
+    made of a power of 2 and where it is turned into one (2^-19 each); the
+    exponential's argument (2^-19 of 32·log2 e < 64) and value (2^-22): 8e-6.
+    Then G's rounding to 16 bits and dw's, u each, binary16's smallest step
+    under the scale 2^14, and the other tokens' parts of the row, each rounded
+    likewise."""
+    V, u = 8000, 2.0**-8 if dtype == BF16 else 2.0**-11
+    gen = torch.Generator(device=DEV).manual_seed(D + T)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device=DEV)
+
+    w = (normal(V, D) * 2 / math.sqrt(D)).to(dtype)
+    y = torch.randperm(V, generator=gen, device=DEV)[:T]
+    lean = 4.0 + 2.0 * torch.rand(T, 1, generator=gen, device=DEV)
+    x = (normal(T, D) + lean * w[y].float()).to(dtype)
+    g = torch.ones(T, device=DEV)
+    _, lse = L.cross_entropy(x, w, y)
+    _, dw = L.cross_entropy_grad(x, w, y, lse, g)
+
+    X = x.double()
+    z = X @ w.double().t()
+    want = torch.logsumexp(z, 1)
+    assert float(want.max()) < 32 and float(z.amax()) < 32
+    P = (z - want[:, None]).exp()
+    z.scatter_(1, y[:, None], -math.inf)
+    left = torch.exp(torch.logsumexp(z, 1) - want)  # 1 - p, with all its bits
+    assert bool((left < 1e-4).any())
+    P.scatter_(1, y[:, None], -left[:, None])
+    along = X / (X * X).sum(1, keepdim=True)
+    cross = along @ X.t()
+    mine = P[:, y]  # [token, target's row]
+    ref_g = (mine.t() * cross).sum(1)
+    got = (dw[y].double() * along).sum(1)
+    step = 0.0 if dtype == BF16 else 2.0**-24 / 2.0**13
+    dG = u * mine.abs() + step
+    dG = dG + 8e-6 * torch.where(
+        torch.eye(T, device=DEV, dtype=torch.bool), 1.0, mine.abs())
+    row = mine.t() @ X  # dw's rows of the targets
+    tol = ((dG.t() * cross.abs()).sum(1)
+           + u * (row.abs() * along.abs()).sum(1) + 1e-5 * left)
+    bad = ~((got - ref_g).abs() <= tol)
+    assert not bool(bad.any()), (
+        int(bad.sum()), (got - ref_g)[bad][:5], tol[bad][:5], left[bad][:5])
+    assert G.device_status() == 0
