@@ -38,6 +38,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -77,7 +78,14 @@ __device__ __forceinline__ int sum_steps(const VocabCall& p, int learnt) {
   return p.T <= 8 ? 4 : learnt <= kVocabTile ? 8 : 16;
 }
 
+// Steps that an accumulator sums for dW and dX, whose results are rounded to
+// 16 bits: what it drops over 256 steps is 1e-4 of a sum whose terms have one
+// sign, half of binary16's rounding.  It grows with the depth (65536 tokens
+// 4e-4, 262144 tokens 1.5e-3).
+constexpr int kDeepSteps = 256;
+
 enum Kind { kStats, kGrad, kDw, kDx };
+enum Loop { kShallow, kDeep, kLogits };  // of the gradients' epilogue
 
 template <bool FORWARD>
 struct Shape {
@@ -336,6 +344,13 @@ struct Walk {
     }
   }
 
+  // Whether some sum of dW or dX may be deeper than `most` (asked before the
+  // first of them).
+  __device__ __forceinline__ bool deep(int most) const {
+    return (dw_steps + splits - 1) / splits > most ||
+           (dx_steps > most && (whole > 0 || x1 - x > most));
+  }
+
   // dX's whole tiles, then its share of the line
   __device__ __forceinline__ bool next_dx(Unit& u) {
     u.kind = kDx;
@@ -498,7 +513,8 @@ __device__ __forceinline__ float pick(const float* f, int i) {
 }
 
 
-template <int AB_TYPE, bool FORWARD>
+// DEEP: sums of dW or dX may be more than kDeepSteps deep.
+template <int AB_TYPE, bool FORWARD, bool DEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Maps maps,
                       const __grid_constant__ VocabCall p, const int phase,
@@ -634,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kb = u.kb0;
         const int most = u.kind == kStats || u.kind == kGrad
                              ? sum_steps(p, learnt)
-                             : INT_MAX;
-        do {  // one sum; logits: several to a tile
+                             : kDeepSteps;
+        do {  // one sum; several to a deep tile
           const int end = u.kb1 - kb > most ? kb + most : u.kb1;
           const int b = i & 1;
           if (i >= 2 && !bounded_wait(acc_empty(b), ((i >> 1) - 1) & 1, wc.limit,
@@ -761,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
+    const bool deep = DEEP && phase > 0 && walk.deep(kDeepSteps);
     bool more = look_ahead(std::false_type());
     if constexpr (FORWARD) {
       const int most = sum_steps(p, learnt);
@@ -854,9 +871,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot_rows = vocab_tiles(learnt) * kVocabTile;
       const int most = sum_steps(p, learnt);
       // dW's and dX's tiles, then the logits': a loop each, so that the sums
-      // of the logits share their registers with little else.
-      auto epilogues = [&](auto in_logits) {
-        constexpr bool LOGITS = decltype(in_logits)::value;
+      // of the logits share their registers with little else; and one for
+      // tiles of dW and dX that are several sums, which holds too much beside
+      // these not to spill.  (It is in a kernel of its own: 8192 × 1000 × 512
+      // distillation steps took 4 us more with it in the code.)
+      auto epilogues = [&](auto loop) {
+        constexpr bool LOGITS = decltype(loop)::value == kLogits;
+        constexpr bool DEEP_LOOP = decltype(loop)::value == kDeep;
         for (;; first_pass = false) {
           int token = 0, seen = 0;
           float shift = 0.f, g = 0.f;
@@ -875,9 +896,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t acc = my_tmem;
           const int wide_here = LOGITS && !first_pass ? walk.wide : u.wide;
           const int half = wide_here >> 1;  // this warp's columns
-          const bool several = LOGITS && !first_pass && walk.steps > most;
-          if (several && !join_sums(half, walk.steps, most, acc)) break;
-          if (!first_pass) more = look_ahead(in_logits);
+          const int steps = LOGITS ? walk.steps : u.kb1 - u.kb0;
+          const bool several = (LOGITS || DEEP_LOOP) && !first_pass &&
+                               steps > (LOGITS ? most : kDeepSteps);
+          if (several &&
+              !join_sums(half, steps, LOGITS ? most : kDeepSteps, acc))
+            break;
+          if (!first_pass) more = look_ahead(std::bool_constant<LOGITS>());
           const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
           const int r = m0 + lane;
           const int n0 = u.tn * wide_here + h * half;
@@ -1092,8 +1117,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      if (phase > 0) epilogues(std::false_type());
-      if (phase < p.pieces) epilogues(std::true_type());
+      if (phase > 0) {
+        if (deep) {
+          if constexpr (DEEP) epilogues(std::integral_constant<Loop, kDeep>());
+        } else {
+          epilogues(std::integral_constant<Loop, kShallow>());
+        }
+      }
+      if (phase < p.pieces)
+        epilogues(std::integral_constant<Loop, kLogits>());
       if (lane == 0) bulk_wait_group<0>();
     }
   }
@@ -1177,13 +1209,13 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   return ok;
 }
 
-template <int AB_TYPE, bool FORWARD>
+template <int AB_TYPE, bool FORWARD, bool DEEP = false>
 cudaError_t launch(const VocabCall& p, const WaitCfg& wc,
                    cudaStream_t stream) {
   using Sh = Shape<FORWARD>;
   Maps maps;
   if (!make_maps<AB_TYPE>(p, !FORWARD, &maps)) return cudaErrorInvalidValue;
-  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD>;
+  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD, DEEP>;
   cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(fn), Sh::kSmemBytes);
   const int phases = FORWARD ? 1 : p.pieces + 1;
@@ -1203,9 +1235,14 @@ cudaError_t vocab_forward(const VocabCall& c, const WaitCfg& wc,
 
 cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
                             cudaStream_t stream) {
-  return c.type == GEMM_F32_MIXED_BF16
-             ? vocab::launch<1, false>(c, wc, stream)
-             : vocab::launch<0, false>(c, wc, stream);
+  // dW sums over the tokens, dX over a piece's words
+  const bool deep =
+      std::max(vocab_steps(c.T), vocab_steps(c.piece)) > vocab::kDeepSteps;
+  if (c.type == GEMM_F32_MIXED_BF16)
+    return deep ? vocab::launch<1, false, true>(c, wc, stream)
+                : vocab::launch<1, false>(c, wc, stream);
+  return deep ? vocab::launch<0, false, true>(c, wc, stream)
+              : vocab::launch<0, false>(c, wc, stream);
 }
 
 }  // namespace gemm_f32_impl

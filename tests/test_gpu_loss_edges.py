@@ -185,3 +185,59 @@ def test_gradients_of_tokens_learnt_by_heart(T, D, dtype):
     assert not bool(bad.any()), (
         int(bad.sum()), (got - ref_g)[bad][:5], tol[bad][:5], left[bad][:5])
     assert G.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T,V,D", [(65536, 2048, 64), (262144, 512, 64),
+                                   (100_000, 1300, 600), (64, 262144, 4096)])
+def test_deep_sums_of_the_gradients(T, V, D, dtype):
+    """Many tokens (dW) and many words beside few tokens (dX): the depth of a
+    sum does not show in the result, though the tensor cores drop bits at
+    every step.  x has one sign, so that the roundings of a row of dw that is
+    no target's all go one way.
+
+    What they may add up to: a step of 64 terms is four additions, each short
+    of less than two of the sum's last places (2^-23 of it and less; on
+    average half of that, while the sum grows to its value from 0): over the
+    256 steps of one sum 4·256·2^-23/2 = 6e-5 of it, twice that at most, as a
+    mean over many sums.  Beside it stands the mean of the roundings to 16
+    bits, which have no sign: none over more than 10^4 results, 1e-5 for
+    bfloat16's 2^-9, and lse's own error, 1e-5."""
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn(T, D, generator=gen, device=DEV)
+    x = (x * 0.5 + 1.0).to(dtype)
+    w = (torch.randn(V, D, generator=gen, device=DEV) * 2 / math.sqrt(D)).to(
+        dtype)
+    y = torch.randint(0, V // 8, (T,), generator=gen, device=DEV)
+    g = torch.full((T,), 1024.0 / T, device=DEV)
+    _, lse = L.cross_entropy(x, w, y)
+    dx, dw = L.cross_entropy_grad(x, w, y, lse, g)
+    assert G.device_status() == 0
+
+    X = x.double()
+    n = max(64, 2**28 // T)  # words at a time
+    want = None
+    for v in range(0, V, n):
+        z = X @ w[v:v + n].double().t()
+        part = torch.logsumexp(z, 1)
+        want = part if want is None else torch.logaddexp(want, part)
+    DX, DW = torch.zeros_like(X), torch.empty(V, D, dtype=torch.float64,
+                                              device=DEV)
+    for v in range(0, V, n):
+        W = w[v:v + n].double()
+        P = (X @ W.t() - want[:, None]).exp()
+        t = ((y >= v) & (y < v + n)).nonzero()[:, 0]
+        P[t, y[t] - v] -= 1.0
+        P *= g[:, None].double()
+        DX += P @ W
+        DW[v:v + n] = P.t() @ X
+    cold = DW[V // 8:]
+    bias = float(((dw[V // 8:].double() - cold) * cold.sign()).sum()
+                 / cold.abs().sum())
+    assert abs(bias) <= 1.4e-4, bias
+    # and in the norm: G's rounding and the result's (u/√3 each at worst,
+    # their mean square), and that bias
+    u = 2.0**-8 if dtype == BF16 else 2.0**-11
+    for name, got, ref_ in (("dx", dx, DX), ("dw", dw, DW)):
+        err = float((got.double() - ref_).norm() / ref_.norm())
+        assert err <= 2 * u / math.sqrt(3.0) + 1.4e-4, (name, err)
