@@ -15,6 +15,10 @@ constexpr uint32_t kVocabNone = 0xffff;
 constexpr int kVocabTile = 256;      // rows and columns of an output tile
 constexpr int kVocabMaxPairs = 128;  // CTA pairs of a launch
 constexpr int kVocabMaxDwSplits = 16;
+// A tile of dX is cut, and dW's depth split, into shares of at least so many
+// steps (where there are as many).
+constexpr int kVocabLeastDxShare = 8;
+constexpr int kVocabLeastDwShare = 4;
 constexpr int kVocabGroup = 16;  // tile rows walked together (L2 reuse)
 // The most tokens, words and columns a call may have: rows and columns are
 // 32-bit numbers, and so is what lies past the last of them, up to one piece
@@ -131,7 +135,8 @@ struct VocabCall {
   float* picked;  // [T][top]: logits / τ of the entries
   // gradients
   int piece, pieces;  // columns of G; the pieces of the vocabulary
-  void* G;            // [2 · g_rows][piece]: two pieces' G in turn
+  void* G;            // [2 · g_rows][piece]: two pieces' G in turn (one
+                      // piece: [g_rows][piece])
   int g_rows;
   int* tile_slots;    // slots of each tile of dX, in the order of the walk
   float* slots;       // dX: [slot_rows][ld_slot]

@@ -1194,11 +1194,9 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   if (fits_tensor_map(p.X, p.ldx))
     ok = ok && encode(&maps->x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
   if (!grad) return ok;
-  ok = ok &&
-       encode(&maps->g_in, t16, 2, p.G, p.piece, 2ll * p.g_rows, p.piece,
-              64) &&
-       encode(&maps->g_out, t16, 2, p.G, p.piece, 2ll * p.g_rows, p.piece,
-              32) &&
+  const long long g_rows = (p.pieces > 1 ? 2ll : 1ll) * p.g_rows;
+  ok = ok && encode(&maps->g_in, t16, 2, p.G, p.piece, g_rows, p.piece, 64) &&
+       encode(&maps->g_out, t16, 2, p.G, p.piece, g_rows, p.piece, 32) &&
        encode(&maps->slots, t32, 4, p.slots, p.D, p.slot_rows, p.ld_slot, 32);
   if (p.dw_slots)
     ok = ok && encode(&maps->dw_slots, t32, 4, p.dw_slots, p.D,

@@ -191,7 +191,7 @@ __device__ __forceinline__ int dw_splits(const VocabCall& p, int learnt,
                     vocab_tiles(learnt) * wide * vocab_steps(p.piece)) /
                        pairs + 1;
   if (4 * depth <= 5 * even) return 1;
-  return max(1, min(min((depth + even - 1) / even, depth / 4),
+  return max(1, min(min((depth + even - 1) / even, depth / kVocabLeastDwShare),
                     p.dw_max_splits));
 }
 
@@ -256,7 +256,8 @@ __device__ void share_out(const VocabCall& p, int learnt, int* s_end) {
   const int left = (tiles - rounds * pairs) * line;
   const long long slot = (long long)vocab_tiles(learnt) * kVocabTile;
   const int most = (int)max(1ll, min(1ll << 30, p.slot_rows / max(1ll, slot)));
-  const int cut = max((line + most - 1) / most, min(line, 8));
+  const int cut =
+      max((line + most - 1) / most, min(line, kVocabLeastDxShare));
   room0 -= rounds * line;
   room1 -= rounds * line;
   room2 -= rounds * line;
@@ -631,9 +632,9 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
     c->pieces = 1;
     // one for each row of a half tile: 128 columns, or down to 32 where two
     // rounds of 256 × 256 tiles hold all logits
-    take(&c->stats, std::max<int64_t>((V + 127) / 128 * rows,
-                                      2 * kVocabMaxPairs * 8 * kVocabTile) *
-                        8);
+    const int64_t narrow = std::min<int64_t>(
+        (V + 31) / 32 * rows, 2 * kVocabMaxPairs * 8 * kVocabTile);
+    take(&c->stats, std::max((V + 127) / 128 * rows, narrow) * 8);
     take(&c->picked, rows * top * 4);
     return at;
   }
@@ -646,14 +647,18 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   pieces = (V + piece - 1) / piece;
   c->piece = (int)piece, c->pieces = (int)pieces;
   c->g_rows = (int)g_rows;
-  take(&bytes, 2 * g_rows * piece * 2);
+  take(&bytes, (pieces > 1 ? 2 : 1) * g_rows * piece * 2);
   c->G = bytes;
   take(&c->tile_slots, (int64_t)vocab_tiles(rows) * vocab_tiles(D) * 4);
   c->ld_slot = up(D, 4);
   const int64_t slot = g_rows * c->ld_slot * 4;
-  c->slot_rows = g_rows * std::min<int64_t>(
-                              kVocabMaxPairs,
-                              std::max<int64_t>(1, kMostSlots / slot));
+  // (as many as pairs, or as a tile's steps give shares)
+  const int64_t line = vocab_steps(piece);
+  const int64_t least = std::min<int64_t>(line, kVocabLeastDxShare);
+  const int64_t shares =
+      std::min<int64_t>(kVocabMaxPairs, (line + least - 1) / least);
+  c->slot_rows =
+      g_rows * std::min(shares, std::max<int64_t>(1, kMostSlots / slot));
   take(&c->slots, c->slot_rows * c->ld_slot * 4);
   // dW's slots: only where the whole vocabulary is one piece of few tiles
   c->dw_slot_rows = (int)up(V, 32);
@@ -661,10 +666,10 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   c->dw_slots = nullptr;
   if (pieces == 1 &&
       (int64_t)vocab_tiles(V) * vocab_tiles(D) < kVocabMaxPairs)
-    c->dw_max_splits = (int)std::min<int64_t>(
-        kVocabMaxDwSplits,
-        std::max<int64_t>(1,
-                          kMostDwSlots / (c->dw_slot_rows * c->ld_slot * 4)));
+    c->dw_max_splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>(
+               {kVocabMaxDwSplits, vocab_steps(T) / kVocabLeastDwShare,
+                kMostDwSlots / (c->dw_slot_rows * c->ld_slot * 4)}));
   if (c->dw_max_splits > 1)
     take(&c->dw_slots, c->dw_max_splits * c->dw_slot_rows * c->ld_slot * 4);
   return at;
@@ -925,7 +930,10 @@ int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V, int64_t D,
     return -GEMM_F32_ERR_INVALID_ARG;
   if (!countable(T, V, D)) return -GEMM_F32_ERR_UNSUPPORTED;
   VocabCall c = {};
-  return lay_out(&c, nullptr, T, V, D, top, grad != 0, aligned == 0);
+  int64_t n = lay_out(&c, nullptr, T, V, D, top, false, aligned == 0);
+  if (grad)  // (room for either call)
+    n = std::max(n, lay_out(&c, nullptr, T, V, D, top, true, aligned == 0));
+  return n;
 }
 
 }  // extern "C"

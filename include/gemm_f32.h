@@ -510,7 +510,8 @@ GEMM_F32_API int gemm_f32_vocab_distill_grad(
  * forward calls (grad = 0) or the gradients (grad = 1), with `top` entries a
  * token (1 for cross entropy).  aligned = 1: X and W are 16-byte aligned
  * with leading dimensions that are multiples of 8; 0: any layout (room for
- * an aligned copy of W is included).  Minus a status on error. */
+ * an aligned copy of W is included).  The gradients' bytes are enough for the
+ * forward call of the same sizes too.  Minus a status on error. */
 GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
                                                    int64_t D, int64_t top,
                                                    int grad, int aligned);

@@ -51,3 +51,27 @@ def test_workspace_bytes_do_not_overflow(built_lib):  # noqa: F811
         for grad in (0, 1):
             got = size(T, V, D, 256, grad, 0)
             assert 2 * (T + V) * D + 8 * T * 256 < got < 2**60, (T, V, D)
+
+
+@pytest.mark.parametrize("T,V,D,top,most", [
+    (8192, 1000, 512, 16, 100), (777, 9973, 521, 5, 130), (2, 5, 7, 1, 1),
+    (300, 700, 96, 64, 2), (8192, 32000, 768, 1, 700)])
+def test_workspace_holds_what_is_written(built_lib, T, V, D, top,  # noqa: F811
+                                         most):
+    """The gradients' workspace in MB: one buffer of G where the vocabulary
+    is one piece, and no more fp32 slots than the steps of a tile of dX and
+    the depth of dW can be cut into (it was 31 to 882 MB for these)."""
+    from dense_fp32_matrix_02_gb300 import gemm
+    assert gemm.lib().gemm_f32_vocab_workspace_size(
+        T, V, D, top, 1, 1) <= most * 1_000_000
+
+
+@pytest.mark.parametrize("T,V,D,top", [
+    (1, 1, 1, 1), (300, 900, 72, 1), (2, 5, 7, 256), (2**20, 128000, 64, 1),
+    (8192, 1000, 512, 16), (0, 100, 8, 1)])
+def test_gradients_workspace_serves_the_forward_call(built_lib,  # noqa: F811
+                                                     T, V, D, top):
+    from dense_fp32_matrix_02_gb300 import gemm
+    size = gemm.lib().gemm_f32_vocab_workspace_size
+    for aligned in (0, 1):
+        assert size(T, V, D, top, 1, aligned) >= size(T, V, D, top, 0, aligned)
