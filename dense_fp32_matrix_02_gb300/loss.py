@@ -140,8 +140,12 @@ def _scratch(workspace, head, top, grad, aligned, device, stream):
         n = _size(head[1], head[2], head[3], top, grad, aligned)
         workspace = _new(n, torch.uint8, device, stream)
     else:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch tensor")
         if workspace.device != device:
             raise ValueError("workspace must live on x's device")
+        if not workspace.is_contiguous():  # (an expanded one has fewer bytes)
+            raise ValueError("workspace must be contiguous")
         n = workspace.numel() * workspace.element_size()
     return workspace, workspace.data_ptr() or None, n
 

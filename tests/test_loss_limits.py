@@ -75,3 +75,21 @@ def test_gradients_workspace_serves_the_forward_call(built_lib,  # noqa: F811
     size = gemm.lib().gemm_f32_vocab_workspace_size
     for aligned in (0, 1):
         assert size(T, V, D, top, 1, aligned) >= size(T, V, D, top, 0, aligned)
+
+
+def test_workspaces_that_hold_less_than_they_count(built_lib):  # noqa: F811
+    """An expanded tensor counts elements that it has no memory for."""
+    torch = pytest.importorskip("torch")
+    from dense_fp32_matrix_02_gb300 import loss as L
+    host, head = torch.device("cpu"), (0, 4, 8, 8)
+    with pytest.raises(ValueError, match="contiguous"):
+        L._scratch(torch.empty(1, dtype=torch.uint8).expand(1 << 20), head, 1,
+                   0, 1, host, None)
+    with pytest.raises(ValueError, match="contiguous"):
+        L._scratch(torch.empty(1 << 10, 2, dtype=torch.uint8)[:, 0], head, 1,
+                   0, 1, host, None)
+    with pytest.raises(TypeError, match="tensor"):
+        L._scratch(bytearray(1 << 20), head, 1, 0, 1, host, None)
+    ws = torch.empty(64, 4, dtype=torch.float32)
+    assert L._scratch(ws, head, 1, 0, 1, host, None) == (ws, ws.data_ptr(),
+                                                         1024)
