@@ -152,7 +152,9 @@ cudaError_t vocab_forward(const VocabCall& c, const WaitCfg& wc,
 cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
                             cudaStream_t stream);
 
-__device__ __forceinline__ bool vocab_maps(const void* p, long long ld) {
+// Whether a tensor map can describe a 16-bit matrix.
+__host__ __device__ __forceinline__ bool vocab_maps(const void* p,
+                                                    long long ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
 }
 __device__ __forceinline__ bool vocab_is_learnt(const VocabCall& c,

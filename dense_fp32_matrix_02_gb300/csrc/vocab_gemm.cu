@@ -259,7 +259,7 @@ struct Divisor {
     d = by > 1 ? by : 1;
     m = 0xffffffffu / d;
   }
-  // (m is less than one below 2^32 / d, so the first quotient is right or one
+  // (m is at most one below 2^32 / d, so the first quotient is right or one
   // too small)
   __device__ __forceinline__ int quotient(int n, int& rest) const {
     unsigned q = __umulhi((unsigned)n, m), r = (unsigned)n - q * d;
@@ -1173,10 +1173,6 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int size,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool fits_tensor_map(const void* p, long long ld) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
-}
-
 template <int AB_TYPE>
 bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   const CUtensorMapDataType t16 = AB_TYPE == 1
@@ -1191,7 +1187,7 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
     ok = ok && encode(&maps->xp, t16, 2, p.Xp, p.D, (p.T + 63) / 64 * 64,
                       p.ldxp, 64);
   // X as given may have no tensor map: then only the packed copy is read
-  if (fits_tensor_map(p.X, p.ldx))
+  if (vocab_maps(p.X, p.ldx))
     ok = ok && encode(&maps->x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
   if (!grad) return ok;
   const long long g_rows = (p.pieces > 1 ? 2ll : 1ll) * p.g_rows;
@@ -1202,7 +1198,7 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
     ok = ok && encode(&maps->dw_slots, t32, 4, p.dw_slots, p.D,
                       (long long)p.dw_slot_rows * p.dw_max_splits, p.ld_slot,
                       32);
-  if (fits_tensor_map(p.dW, p.lddw))
+  if (vocab_maps(p.dW, p.lddw))
     ok = ok && encode(&maps->dw, t16, 2, p.dW, p.D, p.V, p.lddw, 32);
   return ok;
 }

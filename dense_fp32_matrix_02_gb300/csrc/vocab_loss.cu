@@ -587,10 +587,6 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------- host side
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-bool fits_tensor_map(const void* p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
-}
-
 // Places a call's state in its workspace (c.token .. c.dw_max_splits), from
 // T, V, D and top alone; returns its bytes.  The pointers are offsets from
 // `ws` and only numbers where it is null.
@@ -600,7 +596,8 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   // they are read from again (1800 learnt tokens of 6000, 65537 × 2048: 32,
   // 64, 128, 256 MB 1560, 1400, 1350, 1500 us a step), large enough that a
   // launch's ends do not count (4096 × 128000 × 4096: within 2 % from 64 MB
-  // on).  dX's slots: five of the largest dX (8192 × 4096) in question.
+  // on).  Two are held where there are more.  dX's slots: six of an
+  // 8192 × 4096 dX, or more of a smaller one.
   constexpr int64_t kMostG = 128ll << 20;
   constexpr int64_t kMostSlots = 768ll << 20;
   constexpr int64_t kMostDwSlots = 128ll << 20;
@@ -767,7 +764,7 @@ cudaError_t run_forward(VocabCall& c, int sms, const WaitCfg& wc,
   // One row of tiles takes its time whichever of its tokens are learnt from
   // (a row's statistics are its own): nothing is numbered, the results skip
   // the others.
-  if (c.T <= kVocabTile && !c.Wp && fits_tensor_map(c.X, c.ldx))
+  if (c.T <= kVocabTile && !c.Wp && vocab_maps(c.X, c.ldx))
     c.header = nullptr;
   cudaError_t e = launch_targets(c, true, sms, stream);
   if (e == cudaSuccess) e = vocab_forward(c, wc, stream);
@@ -806,7 +803,7 @@ int run(const Request& r) {
   VocabCall c = {};
   const int64_t need =
       lay_out(&c, static_cast<char*>(r.ws), r.T, r.V, r.D, r.top, r.grad,
-              !fits_tensor_map(r.W, r.ldw));
+              !vocab_maps(r.W, r.ldw));
   if (!r.ws || (reinterpret_cast<uintptr_t>(r.ws) & 15u) != 0 ||
       r.ws_bytes < need)
     return GEMM_F32_ERR_INVALID_ARG;

@@ -11,6 +11,10 @@ than 0, and take an optional ``workspace`` (a CUDA tensor of at least
 
     loss, lse = cross_entropy(x, w, targets)             # per token, fp32
     dx, dw = cross_entropy_grad(x, w, targets, lse, grad_loss)
+
+Autograd records none of this: results of inputs that require gradients have
+no graph, and the gradients come from the _grad calls, which overwrite dx and
+dw (in memory of their own).
 """
 
 from __future__ import annotations
