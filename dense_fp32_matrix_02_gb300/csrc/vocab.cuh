@@ -55,7 +55,7 @@ struct VocabShare {
 struct VocabHeader {
   int learnt;       // tokens that are learnt from
   int packed;       // X is read from its packed copy
-  float scale;      // gradients: G is stored times this power of two
+  float scale;      // gradients: G is stored times this
   float inv_scale;  // 1 / scale
   int wide;         // columns of a tile of the logits
   int dw_wide;      // columns of a tile of dW

@@ -202,6 +202,29 @@ __device__ __forceinline__ void scale_add_32(float* f, float m, float a) {
   }
 }
 
+template <int AB_TYPE>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (AB_TYPE == 1) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// Two values times m, rounded to 16 bits.
+template <int AB_TYPE>
+__device__ __forceinline__ uint32_t pack16_scaled(float lo, float hi,
+                                                  float m) {
+  uint64_t x, mm;
+  asm("mov.b64 %0, {%1, %1};\n" : "=l"(mm) : "f"(m));
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(lo), "f"(hi));
+  asm("mul.rn.f32x2 %0, %0, %1;\n" : "+l"(x) : "l"(mm));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(x));
+  return pack16<AB_TYPE>(lo, hi);
+}
+
 // The sum of 32 values, two additions to an instruction, in four runs.
 __device__ __forceinline__ float sum_32(const float* f) {
   uint64_t s[2];
@@ -219,18 +242,6 @@ __device__ __forceinline__ float sum_32(const float* f) {
   asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(s[0]));
   return a + b;
 }
-
-template <int AB_TYPE>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (AB_TYPE == 1) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
 
 struct Maps {
   CUtensorMap x, xp, w;     // operands, 64 × 64 boxes
@@ -945,10 +956,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  float lo = __uint_as_float(v[8 * j + 2 * k]);
-                  float hi = __uint_as_float(v[8 * j + 2 * k + 1]);
-                  if (AB_TYPE == 0) lo *= inv_scale, hi *= inv_scale;
-                  w[k] = empty ? 0u : pack16<AB_TYPE>(lo, hi);
+                  const float lo = __uint_as_float(v[8 * j + 2 * k]);
+                  const float hi = __uint_as_float(v[8 * j + 2 * k + 1]);
+                  w[k] =
+                      empty ? 0u : pack16_scaled<AB_TYPE>(lo, hi, inv_scale);
                 }
                 *reinterpret_cast<uint4*>(stg + lane * 128 +
                                           ((j ^ (lane & 7)) << 4)) =
@@ -1024,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             // 16-bit, 64 columns: half a staged block at a time
-            if (AB_TYPE == 0 && !LOGITS) {  // (bfloat16: 1)
+            if (!LOGITS) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) f[j] *= inv_scale;
             }

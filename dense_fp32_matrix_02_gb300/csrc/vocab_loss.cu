@@ -300,9 +300,12 @@ __device__ void share_out(const VocabCall& p, int learnt, int* s_end) {
 // has no tensor map); packs W's rows where they have no tensor map.  Every
 // block counts all learnt tokens and those before its own share (the targets
 // come from L2), and numbers that share.  Forward: loss and lse of the other
-// tokens are 0.  Gradients: the power of two that brings the largest |g·τ|
-// near 2^14 (binary16 G; 1 for bfloat16, whose exponents need no help), and
-// how dW and dX are cut.
+// tokens are 0.  Gradients: what brings the largest |g·τ| to 1, or 2^14 for
+// binary16, and how dW and dX are cut.  Most losses are means, with one g for
+// all tokens: rounded as it is, g's own error (up to 2^-8 of it in bfloat16)
+// would be the same in every token's target, and stay in all sums; scaled to
+// 1, the target's G is p - 1, just below a power of two, where roundings are
+// least.
 __global__ void __launch_bounds__(1024)
     number_tokens_kernel(const __grid_constant__ VocabCall p, int forward) {
   __shared__ int s_all[32], s_before[32], s_end[kVocabMaxPairs + 1];
@@ -313,8 +316,7 @@ __global__ void __launch_bounds__(1024)
   const long long share = (p.T + gridDim.x - 1) / gridDim.x;
   const long long own0 = min((long long)p.T, blockIdx.x * share);
   const long long own1 = min((long long)p.T, own0 + share);
-  const bool scaled =
-      !forward && blockIdx.x == 0 && p.type == GEMM_F32_MIXED_F16;
+  const bool scaled = !forward && blockIdx.x == 0;
   int all = 0, before = 0;
   float most = 0.f;
 #pragma unroll 8
@@ -322,8 +324,9 @@ __global__ void __launch_bounds__(1024)
     const bool learnt = vocab_is_learnt(p, t);
     all += learnt;
     before += learnt && t < own0;
-    if (scaled && learnt)
-      most = fmaxf(most, fabsf(p.grad_loss[t * p.grad_stride]));
+    // (read whether learnt or not, so that no load waits for another)
+    const float g = scaled ? fabsf(p.grad_loss[t * p.grad_stride]) : 0.f;
+    most = fmaxf(most, learnt ? g : 0.f);
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
@@ -374,15 +377,21 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 1023) {  // (a warp that does not share out)
       for (int w = 0; w < 31; ++w) most = fmaxf(most, s_most[w]);
       most *= p.tau;
-      int e = 0;
-      // 0, Inf and NaN: no scale
-      if (scaled && most > 0.f && most < INFINITY)
-        e = min(max(14 - ilogbf(most), -100), 100);
+      // 0, Inf and NaN: no scale; outside 2^±100 only its power of two
+      const float top = p.type == GEMM_F32_MIXED_F16 ? 16384.f : 1.f;
+      float scale = 1.f, inv_scale = 1.f;
+      if (scaled && most >= 0x1p-100f && most <= 0x1p100f) {
+        scale = top / most;
+        inv_scale = most / top;
+      } else if (scaled && most > 0.f && most < INFINITY) {
+        scale = most < 1.f ? 0x1p100f : 0x1p-100f;
+        inv_scale = 1.f / scale;
+      }
       VocabHeader* h = p.header;
       h->learnt = all;
       h->packed = packed;
-      h->scale = ldexpf(1.f, e);
-      h->inv_scale = ldexpf(1.f, -e);
+      h->scale = scale;
+      h->inv_scale = inv_scale;
       // (G is stored in blocks of 64 columns, half a tile's least)
       h->wide = all == p.T || p.pieces > 1
                     ? p.wide

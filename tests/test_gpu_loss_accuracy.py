@@ -181,3 +181,34 @@ def test_not_finite_inputs_spread_as_the_formulas_say(T, D):
     odd = odd[odd != 9]
     assert bool(loss[odd].isfinite().all())
     assert G.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("op", ["ce", "kd"])
+def test_one_gradient_that_rounds_badly(op, dtype):
+    """A mean's gradient, the same for every token, just short of half-way
+    between two 16-bit numbers: its rounding would be the same in all targets
+    (2^-8 in bfloat16, all of dx and dw).  Scaled to a power of two, a target's
+    G = p - 1 is within u/2 of it, u = 2^-8 or 2^-11; the result's own rounding
+    adds a mean square of u/√3 at most."""
+    u = 2.0**-8 if dtype == BF16 else 2.0**-11
+    T, V, D, tau = 400, 5000, 128, 1.0 if op == "ce" else 2.0
+    x, w, y, _, _ = operands(T, V, D, dtype, 11)
+    w.mul_(0.25)  # probabilities of a model at its start
+    for size in (1.0, 2.0**-9, 2.0**9):
+        g = torch.full((T,), (1 + u - 2.0**-20) * size / tau, device=DEV)
+        if op == "ce":
+            got = ce(x, w, y, g)
+            targets = ref.cross_entropy_targets(y, V)
+        else:
+            ids = y[:, None]
+            logits = torch.ones(T, 1, device=DEV)
+            loss, lse = L.distill(x, w, logits, ids, tau)
+            dx, dw = L.distill_grad(x, w, logits, ids, lse, g, tau)
+            got = {"dx": dx, "dw": dw}
+            targets = ref.distill_targets(logits, ids, tau, V)
+        want = ref.loss_and_grads(x, w, *targets, tau, g)
+        for name in ("dx", "dw"):
+            b = want[name]
+            err = float((got[name].double() - b).norm() / b.norm())
+            assert err <= u * math.sqrt(1 / 3 + 1 / 4), (name, size, err)
