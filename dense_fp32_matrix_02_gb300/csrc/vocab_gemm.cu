@@ -934,8 +934,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!LOGITS && u.kind == kDw && !wide && !dw_direct) {
             // Nothing to work out: 64 columns at a time, packed and stored.  With
             // few tokens a tile is its epilogue alone, which waits for itself
-            // more than for anything else (16 tokens, 100000 × 2048: a step in
-            // 330 us, 352 with 32 columns at a time as below).
+            // more than for anything else (16 tokens, 100000 × 2048: a step took
+            // 22 us more, of 330, with 32 columns at a time as below).
 #pragma unroll 1
             for (int c0 = 0; c0 < half; c0 += 64) {
               uint32_t v[64];
