@@ -212,3 +212,24 @@ def test_one_gradient_that_rounds_badly(op, dtype):
             b = want[name]
             err = float((got[name].double() - b).norm() / b.norm())
             assert err <= u * math.sqrt(1 / 3 + 1 / 4), (name, size, err)
+
+
+def test_checked_build_runs_clean():
+    """Sums of several parts, and deep ones, under the checked build, in a
+    process of its own: no index leaves its buffer."""
+    import os
+    import subprocess
+    import sys
+
+    from dense_fp32_matrix_02_gb300 import build
+    path = build.build(checked=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k",
+         "cross_entropy or distillation or last_words or deep or heart or"
+         " lowest",
+         os.path.join(here, "test_gpu_loss_accuracy.py"),
+         os.path.join(here, "test_gpu_loss_edges.py")],
+        env=dict(os.environ, GEMM_F32_LIBRARY=path), cwd=here,
+        capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
