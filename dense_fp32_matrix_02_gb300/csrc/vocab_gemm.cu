@@ -62,8 +62,8 @@ constexpr uint32_t kSleepNs = 100000;
 constexpr float kLog2e = 1.4426950408889634f;
 // Steps of a logit that an accumulator in tensor memory sums before the
 // epilogue adds them to its own fp32 sums.  It drops bits below its last at
-// every step, towards zero: 2048 to 4096 deep, the losses' error against 64 bits
-// was 1-3e-6 with one sum.  At 2048 × 50021 × 768 (12 steps) it is 2.1e-7,
+// every step, towards zero: 2048 to 4096 deep, the losses' error against 64
+// bits was 1-3e-6 with one sum.  At 2048 × 50021 × 768 (12 steps) it is 2.1e-7,
 // with 8, 4 and 2 steps a sum 1.5e-7, 1.3e-7 and 1.2e-7 at 6, 26 and 60 % more
 // time.  The fewer the tokens, the less their errors average out, and one row
 // of tiles waits for W anyway: it sums 8 steps, or 4 for a few tokens (one
@@ -932,10 +932,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc += h * half;
           }
           if (!LOGITS && u.kind == kDw && !wide && !dw_direct) {
-            // Nothing to work out: 64 columns at a time, packed and stored.  With
-            // few tokens a tile is its epilogue alone, which waits for itself
-            // more than for anything else (16 tokens, 100000 × 2048: a step took
-            // 22 us more, of 330, with 32 columns at a time as below).
+            // Nothing to work out: 64 columns at a time, packed and stored.
+            // With few tokens a tile is its epilogue alone, which waits for
+            // itself more than for anything else (16 tokens, 100000 × 2048: a
+            // step took 22 us more, of 330, with 32 columns at a time as
+            // below).
 #pragma unroll 1
             for (int c0 = 0; c0 < half; c0 += 64) {
               uint32_t v[64];
