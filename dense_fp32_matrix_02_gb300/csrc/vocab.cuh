@@ -19,6 +19,15 @@ constexpr int kVocabMaxDwSplits = 16;
 // steps (where there are as many).
 constexpr int kVocabLeastDxShare = 8;
 constexpr int kVocabLeastDwShare = 4;
+// Up to so many tokens, G is kept in two 16-bit parts, its value's rounding
+// and what that leaves: rows r and lo + r of one row of tiles, with X's row
+// packed in both places, so that dW adds them up and dX's are added at the
+// end.  The errors of many tokens' G average out beside the rounding of the
+// results; those of a few do not (a token's dX hangs on the one or few entries
+// at its targets).  The rows would be empty; a step of 16 tokens, 100000 ×
+// 2048 takes 346 us with it, 340 without.  (Loading X's rows twice instead, in
+// boxes of 32 rows, held up the logits by 6 us.)
+constexpr int kVocabFewTokens = kVocabTile / 2;
 constexpr int kVocabGroup = 16;  // tile rows walked together (L2 reuse)
 // The most tokens, words and columns a call may have: rows and columns are
 // 32-bit numbers, and so is what lies past the last of them, up to one piece
@@ -55,6 +64,7 @@ struct VocabShare {
 struct VocabHeader {
   int learnt;       // tokens that are learnt from
   int packed;       // X is read from its packed copy
+  int lo;           // gradients: where G's second parts start, or 0
   float scale;      // gradients: G is stored times this
   float inv_scale;  // 1 / scale
   int wide;         // columns of a tile of the logits
@@ -128,7 +138,8 @@ struct VocabCall {
                          // the block or after it, in the high half its column
                          // in the block (kVocabNone: it is after it)
   void* Xp;              // X's packed copy: the learnt tokens' rows, then
-  long long ldxp;        // zero rows up to a multiple of 64
+  long long ldxp;        // zero rows up to a multiple of 64; or, few tokens,
+  long long xp_rows;     // both twice (VocabHeader::lo)
   void* Wp;              // W's packed copy, or null (W has a tensor map)
   // forward
   float2* stats;  // [half tiles' columns][learnt]: (max, sum), powers of 2
@@ -156,6 +167,10 @@ cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
 __host__ __device__ __forceinline__ bool vocab_maps(const void* p,
                                                     long long ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
+}
+// Rows of the gradients' products.
+__device__ __forceinline__ int vocab_rows(int learnt, int lo) {
+  return lo ? 2 * lo : learnt;
 }
 __device__ __forceinline__ bool vocab_is_learnt(const VocabCall& c,
                                                 long long t) {

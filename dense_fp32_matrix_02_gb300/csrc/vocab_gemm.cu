@@ -213,6 +213,20 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+// What the rounding of two values leaves, rounded to 16 bits.
+template <int AB_TYPE>
+__device__ __forceinline__ uint32_t pack16_rest(float lo, float hi,
+                                                uint32_t rounded) {
+  if constexpr (AB_TYPE == 1) {
+    return pack16<AB_TYPE>(lo - __uint_as_float(rounded << 16),
+                           hi - __uint_as_float(rounded & 0xffff0000u));
+  } else {
+    const float2 r =
+        __half22float2(*reinterpret_cast<const __half2*>(&rounded));
+    return pack16<AB_TYPE>(lo - r.x, hi - r.y);
+  }
+}
+
 // Two values times m, rounded to 16 bits.
 template <int AB_TYPE>
 __device__ __forceinline__ uint32_t pack16_scaled(float lo, float hi,
@@ -317,7 +331,7 @@ struct Walk {
   bool dx_first;
   Tiles tiles, dw_tiles, dx_tiles;
 
-  __device__ __forceinline__ Walk(const VocabCall& p, int learnt, int phase,
+  __device__ __forceinline__ Walk(const VocabCall& p, int rows, int phase,
                                   int pair_, int pairs_)
       : stage(FORWARD ? 3 : 0), j(pair_), pair(pair_), pairs(pairs_) {
     const VocabHeader* h = p.header;
@@ -325,7 +339,7 @@ struct Walk {
     grad_n = phase < p.pieces ? min(p.piece, p.V - grad_v0) : 0;
     back_v0 = grad_v0 - p.piece;
     back_n = phase > 0 ? min(p.piece, p.V - back_v0) : 0;
-    tiles_m = vocab_tiles(learnt);
+    tiles_m = vocab_tiles(rows);
     wide = h ? h->wide : p.wide;
     tiles_n = ((FORWARD ? p.V : grad_n) + wide - 1) / wide;
     steps = vocab_steps(p.D);
@@ -339,7 +353,7 @@ struct Walk {
       dw_wide = h->dw_wide;
       dw_n = (p.D + dw_wide - 1) / dw_wide;
       dw_m = vocab_tiles(back_n);
-      dw_steps = vocab_steps(learnt);
+      dw_steps = vocab_steps(rows);
       splits = h->dw_splits;
       dw_tiles.set(dw_m, dw_n);
       dx_m = tiles_m;
@@ -524,8 +538,9 @@ __device__ __forceinline__ float pick(const float* f, int i) {
 }
 
 
-// DEEP: sums of dW or dX may be more than kDeepSteps deep.
-template <int AB_TYPE, bool FORWARD, bool DEEP>
+// DEEP: sums of dW or dX may be more than kDeepSteps deep.  FEW: G is in two
+// parts (kVocabFewTokens).
+template <int AB_TYPE, bool FORWARD, bool DEEP, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Maps maps,
                       const __grid_constant__ VocabCall p, const int phase,
@@ -581,7 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const VocabHeader* header = p.header;
   const int learnt = header ? header->learnt : p.T;
-  Walk<FORWARD> walk(p, learnt, phase, pair, pairs);
+  const int lo = FEW ? header->lo : 0;
+  const int all_rows = vocab_rows(learnt, lo);
+  Walk<FORWARD> walk(p, all_rows, phase, pair, pairs);
   Unit u;
   int it = 0, i = 0;  // steps and sums so far
   bool ok = true;
@@ -601,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 100000 × 2048: 98 us with the empty ones, 83 without)
         const bool two = u.wide == kVocabTile;
         const int rows = u.kind == kDw ? kVocabTile
-                                       : min(learnt - u.tm * kVocabTile,
+                                       : min(all_rows - u.tm * kVocabTile,
                                              kVocabTile);
         const int boxes0 = min((rows + 63) / 64, 2);
         const int boxes1 = max((rows + 63) / 64 - 2, 0);
@@ -776,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto look_ahead = [&](auto in_logits) -> bool {
       if (!(decltype(in_logits)::value ? walk.next_logits(nu) : walk.next(nu)))
         return false;
-      const int r = nu.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
+      int r = nu.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
+      if (FEW && r >= lo) r -= lo;  // (both parts are one token's)
       if ((nu.kind == kStats || nu.kind == kGrad) && r < learnt) {
         n_token = learnt == p.T ? r : p.token[r];
         const int n0 = nu.tn * nu.wide + h * (nu.wide >> 1);
@@ -915,7 +933,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           if (!first_pass) more = look_ahead(std::bool_constant<LOGITS>());
           const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
-          const int r = m0 + lane;
+          // this warp's rows are the second parts of G's
+          const bool second = FEW && LOGITS && m0 >= lo;
+          const int r = m0 + lane - (second ? lo : 0);
           const int n0 = u.tn * wide_here + h * half;
           // G is written to the end of its tiles
           const int cols = LOGITS ? INT_MAX : p.D;
@@ -1019,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (lane == 0) {
                 if (u.kind == kDx) {
-                  if (!first_pass && m0 < learnt) {
+                  if (!first_pass && m0 < all_rows) {
                     if (phase == 1)  // the first piece
                       tma_store_2d(&maps.slots, stg_s, n,
                                    u.slot * slot_rows + m0);
@@ -1054,9 +1074,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int chunk = (c0 & 32) / 8 + j;
               uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = (pack16<AB_TYPE>(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]) ^
-                        flip) & keep;
+              for (int k = 0; k < 4; ++k) {
+                const float a = f[8 * j + 2 * k], b = f[8 * j + 2 * k + 1];
+                w[k] = pack16<AB_TYPE>(a, b);
+                if (second) w[k] = pack16_rest<AB_TYPE>(a, b, w[k]);
+                w[k] = (w[k] ^ flip) & keep;
+              }
               *reinterpret_cast<uint4*>(stg + lane * 128 +
                                         ((chunk ^ (lane & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
@@ -1075,10 +1098,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unsigned char* to = stg + lane * 128 +
                                         ((chunk ^ (lane & 7)) << 4) +
                                         (c & 7) * 2;
-                    if (span_ok(to, 2, stg, kStagingBytes, wc.status))
-                      *reinterpret_cast<uint16_t*>(to) =
-                          (uint16_t)pack16<AB_TYPE>(
-                              copysignf(pick(f, c), g) - g * part, 0.f);
+                    if (span_ok(to, 2, stg, kStagingBytes, wc.status)) {
+                      const float v = copysignf(pick(f, c), g) - g * part;
+                      uint32_t w = pack16<AB_TYPE>(v, 0.f);
+                      if (second) w = pack16_rest<AB_TYPE>(v, 0.f, w);
+                      *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+                    }
                     part = 0.f;
                   }
                 }
@@ -1196,8 +1221,7 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   bool ok = p.Wp ? encode(&maps->w, t16, 2, p.Wp, p.D, p.V, p.ldxp, 64)
                  : encode(&maps->w, t16, 2, p.W, p.D, p.V, p.ldw, 64);
   if (p.header)
-    ok = ok && encode(&maps->xp, t16, 2, p.Xp, p.D, (p.T + 63) / 64 * 64,
-                      p.ldxp, 64);
+    ok = ok && encode(&maps->xp, t16, 2, p.Xp, p.D, p.xp_rows, p.ldxp, 64);
   // X as given may have no tensor map: then only the packed copy is read
   if (vocab_maps(p.X, p.ldx))
     ok = ok && encode(&maps->x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
@@ -1215,13 +1239,13 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   return ok;
 }
 
-template <int AB_TYPE, bool FORWARD, bool DEEP = false>
+template <int AB_TYPE, bool FORWARD, bool DEEP = false, bool FEW = false>
 cudaError_t launch(const VocabCall& p, const WaitCfg& wc,
                    cudaStream_t stream) {
   using Sh = Shape<FORWARD>;
   Maps maps;
   if (!make_maps<AB_TYPE>(p, !FORWARD, &maps)) return cudaErrorInvalidValue;
-  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD, DEEP>;
+  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD, DEEP, FEW>;
   cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(fn), Sh::kSmemBytes);
   const int phases = FORWARD ? 1 : p.pieces + 1;
@@ -1244,11 +1268,14 @@ cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
   // dW sums over the tokens, dX over a piece's words
   const bool deep =
       std::max(vocab_steps(c.T), vocab_steps(c.piece)) > vocab::kDeepSteps;
+  const bool few = c.T <= kVocabFewTokens;
   if (c.type == GEMM_F32_MIXED_BF16)
-    return deep ? vocab::launch<1, false, true>(c, wc, stream)
-                : vocab::launch<1, false>(c, wc, stream);
-  return deep ? vocab::launch<0, false, true>(c, wc, stream)
-              : vocab::launch<0, false>(c, wc, stream);
+    return few    ? vocab::launch<1, false, true, true>(c, wc, stream)
+           : deep ? vocab::launch<1, false, true>(c, wc, stream)
+                  : vocab::launch<1, false>(c, wc, stream);
+  return few    ? vocab::launch<0, false, true, true>(c, wc, stream)
+         : deep ? vocab::launch<0, false, true>(c, wc, stream)
+                : vocab::launch<0, false>(c, wc, stream);
 }
 
 }  // namespace gemm_f32_impl

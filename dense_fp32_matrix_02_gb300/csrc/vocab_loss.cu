@@ -182,49 +182,49 @@ __device__ __forceinline__ int tile_cost(int steps) {
 
 // Slots that dW's tiles are summed in: 1 unless so few tiles are left to
 // the pairs that one tile's depth outlasts an even share by a quarter.
-__device__ __forceinline__ int dw_splits(const VocabCall& p, int learnt,
+__device__ __forceinline__ int dw_splits(const VocabCall& p, int rows,
                                          int pairs) {
-  const int wide = vocab_tiles(p.D), depth = vocab_steps(learnt);
+  const int wide = vocab_tiles(p.D), depth = vocab_steps(rows);
   const int tiles = vocab_tiles(p.piece) * wide;
   if (p.dw_max_splits < 2 || tiles >= pairs) return 1;
   const int even = (tiles * depth +
-                    vocab_tiles(learnt) * wide * vocab_steps(p.piece)) /
+                    vocab_tiles(rows) * wide * vocab_steps(p.piece)) /
                        pairs + 1;
   if (4 * depth <= 5 * even) return 1;
   return max(1, min(min((depth + even - 1) / even, depth / kVocabLeastDwShare),
                     p.dw_max_splits));
 }
 
-// How dW and dX are cut, by 128 threads, a pair a thread.  Each pair's share
-// of dX's line (VocabShare) is what its tiles of G and dW leave of an even
-// total, in stretches that keep a tile's slots within the room for them and
-// no share under eight steps.  The first pairs have one tile of dW more than
-// the others, the last one of G; so the pairs fall into three runs with one
-// room each, and everything has a closed form.  (All step counts are below
-// 2^30: the host checks.)
-__device__ void share_out(const VocabCall& p, int learnt, int* s_end) {
+// How dW and dX (of `rows` rows) are cut, by 128 threads, a pair a thread.
+// Each pair's share of dX's line (VocabShare) is what its tiles of G and dW
+// leave of an even total, in stretches that keep a tile's slots within the
+// room for them and no share under eight steps.  The first pairs have one tile
+// of dW more than the others, the last one of G; so the pairs fall into three
+// runs with one room each, and everything has a closed form.  (All step counts
+// are below 2^30: the host checks.)
+__device__ void share_out(const VocabCall& p, int rows, int* s_end) {
   VocabHeader* h = p.header;
   const int pair = threadIdx.x, pairs = p.pairs;
-  const int splits = dw_splits(p, learnt, pairs);
+  const int splits = dw_splits(p, rows, pairs);
   const int dw_wide =
       p.pieces > 1 || splits > 1
           ? kVocabTile
-          : vocab_tile_width(p.V, p.D, vocab_steps(learnt), 128, pairs);
+          : vocab_tile_width(p.V, p.D, vocab_steps(rows), 128, pairs);
   if (pair == 0) {
     h->dw_splits = splits;
     h->dw_wide = dw_wide;
     h->dx_rounds = 0;
   }
-  if (learnt == 0) {
+  if (rows == 0) {
     if (pair < pairs) h->share[pair] = VocabShare{0, 0, 0};
     return;
   }
-  const int tiles = vocab_tiles(learnt) * vocab_tiles(p.D);
+  const int tiles = vocab_tiles(rows) * vocab_tiles(p.D);
   const int tall = vocab_tiles(p.piece), line = vocab_steps(p.piece);
   const int tiles_w = tall * ((p.D + dw_wide - 1) / dw_wide) * splits;
-  const int tiles_g = p.pieces > 1 ? vocab_tiles(learnt) * tall : 0;
+  const int tiles_g = p.pieces > 1 ? vocab_tiles(rows) * tall : 0;
   const int cost_w = max(
-      1, tile_cost(vocab_steps(learnt) / splits) * dw_wide / kVocabTile);
+      1, tile_cost(vocab_steps(rows) / splits) * dw_wide / kVocabTile);
   const int cost_g = tile_cost(vocab_steps(p.D));
   const int more_w = tiles_w % pairs, more_g = tiles_g % pairs;
   const int end0 = min(more_w, pairs - more_g);
@@ -254,7 +254,7 @@ __device__ void share_out(const VocabCall& p, int learnt, int* s_end) {
   if (n2) least = min(least, room2);
   const int rounds = min(least / line, tiles / pairs);
   const int left = (tiles - rounds * pairs) * line;
-  const long long slot = (long long)vocab_tiles(learnt) * kVocabTile;
+  const long long slot = (long long)vocab_tiles(rows) * kVocabTile;
   const int most = (int)max(1ll, min(1ll << 30, p.slot_rows / max(1ll, slot)));
   const int cut =
       max((line + most - 1) / most, min(line, kVocabLeastDxShare));
@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(1024)
   all = __reduce_add_sync(0xffffffffu, s_all[lane]);
   before = __reduce_add_sync(0xffffffffu, s_before[lane]);
   const bool x_fits = vocab_maps(p.X, p.ldx);
-  const bool packed = !x_fits || all != p.T;
+  const int lo =
+      forward || p.T > kVocabFewTokens ? 0 : (all + 31) / 32 * 32;
+  const bool packed = !x_fits || all != p.T || lo;
   if (all != p.T) {
     if (warp == 0)
       for (long long t0 = own0; t0 < own1; t0 += 32) {
@@ -361,7 +363,25 @@ __global__ void __launch_bounds__(1024)
       }
     __syncthreads();
   }
-  if (packed) {
+  if (lo) {  // a few rows, all threads on each, written twice
+    const uint16_t* from = static_cast<const uint16_t*>(p.X);
+    uint16_t* to = static_cast<uint16_t*>(p.Xp);
+    const int chunks = (p.D + 7) / 8, rows = (int)(own1 - own0);
+    for (int k = threadIdx.x; k < rows * chunks; k += 1024) {
+      const long long t = own0 + k / chunks;
+      const int c = 8 * (k % chunks), r = all != p.T ? p.row[t] : (int)t;
+      if (r < 0) continue;
+      const uint4 v = read_8(from + t * p.ldx, c, p.D, x_fits);
+      *reinterpret_cast<uint4*>(to + r * p.ldxp + c) = v;
+      *reinterpret_cast<uint4*>(to + (r + lo) * p.ldxp + c) = v;
+    }
+    for (int r = all + blockIdx.x; r < lo; r += gridDim.x)
+      for (int c = 8 * threadIdx.x; c < p.D; c += 8192) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(to + r * p.ldxp + c) = zero;
+        *reinterpret_cast<uint4*>(to + (r + lo) * p.ldxp + c) = zero;
+      }
+  } else if (packed) {
     uint16_t* to = static_cast<uint16_t*>(p.Xp);
     pack_rows(static_cast<const uint16_t*>(p.X), p.ldx, p.D, to, p.ldxp,
               all != p.T ? p.row : nullptr, x_fits, own0 + warp, own1, 32,
@@ -373,7 +393,8 @@ __global__ void __launch_bounds__(1024)
               make_uint4(0, 0, 0, 0);
   }
   if (blockIdx.x == 0) {
-    if (!forward && threadIdx.x < 128) share_out(p, all, s_end);
+    if (!forward && threadIdx.x < 128)
+      share_out(p, vocab_rows(all, lo), s_end);
     if (threadIdx.x == 1023) {  // (a warp that does not share out)
       for (int w = 0; w < 31; ++w) most = fmaxf(most, s_most[w]);
       most *= p.tau;
@@ -390,6 +411,7 @@ __global__ void __launch_bounds__(1024)
       VocabHeader* h = p.header;
       h->learnt = all;
       h->packed = packed;
+      h->lo = lo;
       h->scale = scale;
       h->inv_scale = inv_scale;
       // (G is stored in blocks of 64 columns, half a tile's least)
@@ -498,21 +520,26 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// The sum of n slots, `next` apart, in order.
-template <int AHEAD>
+// The sum of n slots, `next` apart, in order; in two parts, with those `second`
+// behind them.
+template <int AHEAD, int PARTS>
 __device__ __forceinline__ float4 sum_slots(const float* from, long long next,
-                                            int n) {
+                                            int n, long long second = 0) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int s0 = 0; s0 < n; s0 += AHEAD) {
-    float4 a[AHEAD];
+    float4 a[AHEAD][PARTS];
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s)  // (past the end, the last again)
-      a[s] = *reinterpret_cast<const float4*>(from +
-                                              min(s0 + s, n - 1) * next);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+        a[s][part] = *reinterpret_cast<const float4*>(
+            from + min(s0 + s, n - 1) * next + part * second);
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s)
-      if (s0 + s < n) v = add4(v, a[s]);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+        if (s0 + s < n) v = add4(v, a[s][part]);
   }
   return v;
 }
@@ -551,7 +578,8 @@ __device__ __forceinline__ void store_4(T16* to, float4 v, float scale, int i,
 // tiles were summed in slots.  AHEAD slots are read side by side: many where
 // there are few elements, whose tiles are cut finely (they were one row of
 // tiles), few otherwise.
-template <typename T16, int AHEAD>
+// PARTS: of G, and so of dX.
+template <typename T16, int AHEAD, int PARTS>
 __global__ void __launch_bounds__(256)
     finish_grad_kernel(const __grid_constant__ VocabCall p) {
   griddep_wait();
@@ -575,7 +603,9 @@ __global__ void __launch_bounds__(256)
       const int high = min(vocab_tiles(learnt) - group, kVocabGroup);
       const int n =
           p.tile_slots[group * wide + i / kVocabTile * high + (tm - group)];
-      v = sum_slots<AHEAD>(p.slots + (long long)r * p.ld_slot + i, next, n);
+      // (both parts lie in one row of tiles)
+      v = sum_slots<AHEAD, PARTS>(p.slots + (long long)r * p.ld_slot + i, next,
+                                  n, PARTS > 1 ? h->lo * p.ld_slot : 0);
     }
     store_4(static_cast<T16*>(p.dX) + t * p.lddx + i, v, inv_scale, i, p.D,
             p.dX, p.T, p.lddx, p.status);
@@ -586,7 +616,7 @@ __global__ void __launch_bounds__(256)
   for (long long k = first; k < (long long)p.V * chunks; k += stride) {
     const long long r = k / chunks;
     const int i = (int)(k - r * chunks) * 4;
-    const float4 v = sum_slots<AHEAD>(
+    const float4 v = sum_slots<AHEAD, 1>(
         p.dw_slots + 4 * k, (long long)p.dw_slot_rows * p.ld_slot, splits);
     store_4(static_cast<T16*>(p.dW) + r * p.lddw + i, v, inv_scale, i, p.D,
             p.dW, p.V, p.lddw, p.status);
@@ -627,7 +657,8 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   take(&c->starts, rows * c->blocks * 4);
   c->ldxp = up(D, 8);
   char* bytes = nullptr;
-  take(&bytes, up(rows, 64) * c->ldxp * 2);
+  c->xp_rows = grad && T <= kVocabFewTokens ? 2 * up(rows, 32) : up(rows, 64);
+  take(&bytes, c->xp_rows * c->ldxp * 2);
   c->Xp = bytes;
   c->Wp = nullptr;
   if (pack_w) {
@@ -763,7 +794,10 @@ cudaError_t launch_targets(const VocabCall& c, bool forward, int sms,
                    dim3(32 * kTeacherWarps), 0, stream, c, forward ? 1 : 0);
   }
   if (e != cudaSuccess || !c.header) return e;
-  const int blocks = c.Wp ? sms : std::min(sms, (c.T + 31) / 32);
+  // (a block packs the rows of 32 tokens, or of 2 where there are few)
+  const bool few = !forward && c.T <= kVocabFewTokens;
+  const int blocks =
+      c.Wp ? sms : std::min(sms, few ? (c.T + 1) / 2 : (c.T + 31) / 32);
   return launch_pdl(number_tokens_kernel, dim3(blocks), dim3(1024), 0, stream,
                     c, forward ? 1 : 0);
 }
@@ -794,15 +828,19 @@ cudaError_t run_gradients(const VocabCall& c, int sms, const WaitCfg& wc,
       c.ld_slot / 4 * std::max<int64_t>(c.T, c.dw_slots ? c.V : 0);
   const unsigned blocks =
       (unsigned)std::min<int64_t>((chunks + 255) / 256, 8ll * sms);
-  const bool few = c.T <= kVocabTile;
   auto launch = [&](auto* fn) {
     return launch_pdl(fn, dim3(blocks), dim3(256), 0, stream, c);
   };
-  if (c.type == GEMM_F32_MIXED_BF16)
-    return few ? launch(finish_grad_kernel<__nv_bfloat16, 16>)
-               : launch(finish_grad_kernel<__nv_bfloat16, 4>);
-  return few ? launch(finish_grad_kernel<__half, 16>)
-             : launch(finish_grad_kernel<__half, 4>);
+  using Bf16 = __nv_bfloat16;
+  const bool bf16 = c.type == GEMM_F32_MIXED_BF16;
+  if (c.T <= kVocabFewTokens)
+    return bf16 ? launch(finish_grad_kernel<Bf16, 12, 2>)
+                : launch(finish_grad_kernel<__half, 12, 2>);
+  if (c.T <= kVocabTile)
+    return bf16 ? launch(finish_grad_kernel<Bf16, 16, 1>)
+                : launch(finish_grad_kernel<__half, 16, 1>);
+  return bf16 ? launch(finish_grad_kernel<Bf16, 4, 1>)
+              : launch(finish_grad_kernel<__half, 4, 1>);
 }
 
 int run(const Request& r) {

@@ -460,8 +460,8 @@ GEMM_F32_API int gemm_f32_host_chunks(int64_t M, int64_t N, int sm_count,
  *   dX = G·W (T×D, lddx),   dW = Gᵀ·X (V×D, lddw),
  * both 16-bit of `type`, written whole (not added to what was there), neither
  * in memory that an input lies in.  G is rounded to `type` once before the two
- * products (scaled so that the largest |g_t·τ| is 1, in binary16 2^14), whose
- * sums are fp32 (in the tensor cores over at most 256 steps of 64 terms, which
+ * products (scaled so that the largest |g_t·τ| is 1, in binary16 2^14; for
+ * T <= 128 what the rounding leaves is multiplied too), whose sums are fp32 (in the tensor cores over at most 256 steps of 64 terms, which
  * drop up to 1e-4 of a sum of one sign), and each result is rounded once.
  * Sums run in a fixed order: the same call gives the same bits.
  *
