@@ -134,6 +134,12 @@ def lib() -> ctypes.CDLL:
         L.gemm_f32_vocab_workspace_size.restype = i64
         L.gemm_f32_vocab_workspace_size.argtypes = [i64, i64, i64, i64, ci,
                                                     ci]
+        L.gemm_f32_grad_norm.restype = ci
+        L.gemm_f32_grad_norm.argtypes = [i64, vp, vp, vp, i64, vp]
+        L.gemm_f32_grad_clip.restype = ci
+        L.gemm_f32_grad_clip.argtypes = [i64, vp, cf, vp, vp, i64, vp]
+        L.gemm_f32_grad_workspace_size.restype = i64
+        L.gemm_f32_grad_workspace_size.argtypes = [i64]
         _lib = L
         return L
 

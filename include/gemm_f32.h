@@ -517,6 +517,61 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
                                                    int64_t D, int64_t top,
                                                    int grad, int aligned);
 
+/* Element types of a gradient (the first two: gemm_f32_mixed_type's). */
+typedef enum {
+    GEMM_F32_GRAD_BF16 = 0,
+    GEMM_F32_GRAD_F16 = 1,
+    GEMM_F32_GRAD_F32 = 2
+} gemm_f32_grad_type;
+
+/* One gradient: rows × cols elements at `data`, rows ld elements apart, and
+ * where it goes when it is clipped (rows ld_out apart; `data` itself with
+ * ld_out = ld, or memory that no gradient of the call lies in).  Any element
+ * boundary.  A gradient of one row has no need of ld and ld_out, one without
+ * rows or columns of nothing.  The norm alone reads no out and ld_out. */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t rows, cols, ld, ld_out;
+    int64_t type; /* gemm_f32_grad_type */
+} gemm_f32_grad;
+
+/*
+ * The global norm of n gradients, and clipping by it.
+ *   norm = sqrt(Σ over every element of every gradient of g²),
+ *   out  = g·min(1, max_norm / norm), rounded once to the gradient's type.
+ * `grads` is an array in host memory, read before the call returns; `norm`
+ * is one float on the device.  A norm that is not finite (a NaN or an
+ * infinity in a gradient) clips nothing: out is a copy, to the bit, as it is
+ * where norm <= max_norm; a gradient clipped in place is then not written.
+ * max_norm is >= 0 (infinity: never clipped).  Squares are summed in fp32
+ * over at most 128 elements, the sums in fp64, in a fixed order: the same
+ * call gives the same bits.  Neither overflow nor underflow of a square of
+ * fp32 changes the norm.
+ *
+ * `workspace` is 16-byte aligned device memory of at least
+ * gemm_f32_grad_workspace_size(n) bytes (else GEMM_F32_ERR_INVALID_ARG), in
+ * use until the stream passes the call.  n = 0: norm = 0.
+ * GEMM_F32_ERR_INVALID_ARG also for an unknown type, negative sizes, leading
+ * dimensions below the row width, a NULL or misaligned pointer and a max_norm
+ * that is negative or NaN; GEMM_F32_ERR_UNSUPPORTED for more than 2^48 elements of a gradient or
+ * its rows' span, or 2^31 rows, or columns of several rows that are not one behind the other,
+ * or more gradients.
+ */
+GEMM_F32_API int gemm_f32_grad_norm(int64_t n, const gemm_f32_grad *grads,
+                                    float *norm, void *workspace,
+                                    int64_t workspace_bytes,
+                                    gemm_f32_stream_t stream);
+
+GEMM_F32_API int gemm_f32_grad_clip(int64_t n, const gemm_f32_grad *grads,
+                                    float max_norm, float *norm,
+                                    void *workspace, int64_t workspace_bytes,
+                                    gemm_f32_stream_t stream);
+
+/* Workspace bytes for n gradients (no device call).  Minus a status on
+ * error. */
+GEMM_F32_API int64_t gemm_f32_grad_workspace_size(int64_t n);
+
 /* Static description of a status code. */
 GEMM_F32_API const char *gemm_f32_status_string(int status);
 
