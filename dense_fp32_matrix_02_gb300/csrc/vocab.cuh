@@ -1,5 +1,6 @@
-// What the vocabulary losses' kernels and their caller share: the call as
-// the kernels see it, where its state lies, and the counts they all make.
+// What the kernels of the vocabulary losses and log probabilities and their
+// caller share: the call as the kernels see it, where its state lies, and the
+// counts they all make.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -123,6 +124,15 @@ struct VocabCall {
   void* dW;
   long long lddw;
 
+  // log probabilities (one target a token); else null
+  float* entropy_out;         // forward (loss is the log probability)
+  float* top_logp;            // [T][alternatives]
+  int64_t* top_out;           // their ids
+  int alternatives;
+  const float* entropy;       // gradients (grad_loss: of the log probability)
+  const float* grad_entropy;  // or null
+  long long entropy_stride;
+
   int pairs;  // CTA pairs of the products
   int wide;   // columns of the logits' tiles if all tokens are learnt from
   unsigned int* status;  // where a bounds check reports
@@ -144,6 +154,11 @@ struct VocabCall {
   // forward
   float2* stats;  // [half tiles' columns][learnt]: (max, sum), powers of 2
   float* picked;  // [T][top]: logits / τ of the entries
+  // log probabilities
+  float2* slants;  // beside stats: Σ e·log2 e of its terms e, the largest logit
+  float* logits;   // [chunk][ld_logits]: the logits of the learnt tokens, of
+  long long ld_logits;  // all (kept for the gradients) or, for their largest,
+  int chunk, keep;      // of `chunk` in turn; or null
   // gradients
   int piece, pieces;  // columns of G; the pieces of the vocabulary
   void* G;            // [2 · g_rows][piece]: two pieces' G in turn (one
@@ -162,11 +177,83 @@ cudaError_t vocab_forward(const VocabCall& c, const WaitCfg& wc,
                           cudaStream_t stream);
 cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
                             cudaStream_t stream);
+// Log probabilities: chunk `phase` of the tokens.
+cudaError_t vocab_score(const VocabCall& c, const WaitCfg& wc, int phase,
+                        cudaStream_t stream);
+
+// What surrounds them for log probabilities (vocab_score.cu).
+// The results of chunk `phase`.
+cudaError_t vocab_score_results(const VocabCall& c, int phase, int sms,
+                                cudaStream_t stream);
+// G of a piece of the vocabulary from the kept logits.
+cudaError_t vocab_score_g(const VocabCall& c, int piece, int sms,
+                          cudaStream_t stream);
 
 // Whether a tensor map can describe a 16-bit matrix.
 __host__ __device__ __forceinline__ bool vocab_maps(const void* p,
                                                     long long ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
+}
+// Eight 16-bit elements from column c of n of a row, zeros past the end.
+// vec: the row is 16-byte aligned; else it is read in the aligned 4-byte
+// words that hold it (a word that lies partly outside the row is read as
+// single elements).
+__device__ __forceinline__ uint4 read_8(const uint16_t* __restrict__ src,
+                                        int c, int n, bool vec) {
+  if (vec && c + 8 <= n) return *reinterpret_cast<const uint4*>(src + c);
+  const int odd = (reinterpret_cast<uintptr_t>(src) >> 1) & 1;
+  if (c >= odd && c + 8 + odd <= n) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(src + c - odd);
+    const uint32_t a = w[0], b = w[1], d = w[2], e = w[3];
+    if (!odd) return make_uint4(a, b, d, e);
+    return make_uint4(__funnelshift_r(a, b, 16), __funnelshift_r(b, d, 16),
+                      __funnelshift_r(d, e, 16), __funnelshift_r(e, w[4], 16));
+  }
+  uint32_t e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) e[j] = c + j < n ? src[c + j] : 0;
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
+                    e[6] | e[7] << 16);
+}
+// Two values rounded to 16 bits, and what the rounding leaves of them,
+// rounded too (AB_TYPE 1: bfloat16).
+template <int AB_TYPE>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (AB_TYPE == 1) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <int AB_TYPE>
+__device__ __forceinline__ uint32_t pack16_rest(float lo, float hi,
+                                                uint32_t rounded) {
+  if constexpr (AB_TYPE == 1) {
+    return pack16<AB_TYPE>(lo - __uint_as_float(rounded << 16),
+                           hi - __uint_as_float(rounded & 0xffff0000u));
+  } else {
+    const float2 r =
+        __half22float2(*reinterpret_cast<const __half2*>(&rounded));
+    return pack16<AB_TYPE>(lo - r.x, hi - r.y);
+  }
+}
+// 2^x by the hardware's approximation (relative error about 2^-22; x = -Inf
+// gives 0), the exponential of all statistics and gradients.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// What a token that is not scored is given besides.
+__device__ __forceinline__ void vocab_unscored(const VocabCall& c,
+                                               long long t) {
+  c.entropy_out[t] = 0.f;
+  for (int j = 0; j < c.alternatives; ++j) {
+    c.top_logp[t * c.alternatives + j] = 0.f;
+    c.top_out[t * c.alternatives + j] = -1;
+  }
 }
 // Rows of the gradients' products.
 __device__ __forceinline__ int vocab_rows(int learnt, int lo) {

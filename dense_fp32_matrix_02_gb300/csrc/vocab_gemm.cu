@@ -6,6 +6,9 @@
 //   Grad   z = X·W_pᵀ: G = g·τ·(exp(z/τ − lse) − q), rounded to 16 bits;
 //   Dw     Gᵀ·X, rounded to 16 bits (or, few tiles, into fp32 slots);
 //   Dx     G·W_p, added into fp32 slots.
+// Log probabilities (vocab_score.cu) take Stats with a third number, for the
+// entropy, and with the logits stored where they are kept or searched; their
+// gradients Dw and Dx, of a G that is made from the kept logits.
 // Stats is the forward launch.  The gradients take one launch per piece of
 // the vocabulary and one more, each of which makes Grad of one piece beside
 // Dw and Dx of the one before: they do not depend on each other, and the
@@ -87,12 +90,12 @@ constexpr int kDeepSteps = 256;
 enum Kind { kStats, kGrad, kDw, kDx };
 enum Loop { kShallow, kDeep, kLogits };  // of the gradients' epilogue
 
-template <bool FORWARD>
+template <bool STAGED>
 struct Shape {
-  static constexpr int kStages = FORWARD ? 7 : 6;
+  static constexpr int kStages = STAGED ? 6 : 7;
   static constexpr int kOffStaging = kStages * kStageBytes;
   static constexpr int kOffCtl =
-      kOffStaging + (FORWARD ? 0 : kEpiWarps * kStagingBytes);
+      kOffStaging + (STAGED ? kEpiWarps * kStagingBytes : 0);
   struct __align__(8) Control {
     uint64_t full[kStages];   // TMA of both CTAs -> MMA (first CTA's is used)
     uint64_t empty[kStages];  // MMA completion -> producers
@@ -180,14 +183,6 @@ __device__ __forceinline__ void tma_add_2d(const void* tmap, uint32_t src,
       : "memory");
 }
 
-// 2^x by the hardware's approximation (relative error about 2^-22; x = -Inf
-// gives 0), the exponential of all statistics and gradients here.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // f[i] = f[i]·m + a for 32 values, two to an instruction.
 __device__ __forceinline__ void scale_add_32(float* f, float m, float a) {
   uint64_t mm, aa;
@@ -199,31 +194,6 @@ __device__ __forceinline__ void scale_add_32(float* f, float m, float a) {
     asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(f[j]), "f"(f[j + 1]));
     asm("fma.rn.f32x2 %0, %0, %1, %2;\n" : "+l"(x) : "l"(mm), "l"(aa));
     asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f[j]), "=f"(f[j + 1]) : "l"(x));
-  }
-}
-
-template <int AB_TYPE>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (AB_TYPE == 1) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
-// What the rounding of two values leaves, rounded to 16 bits.
-template <int AB_TYPE>
-__device__ __forceinline__ uint32_t pack16_rest(float lo, float hi,
-                                                uint32_t rounded) {
-  if constexpr (AB_TYPE == 1) {
-    return pack16<AB_TYPE>(lo - __uint_as_float(rounded << 16),
-                           hi - __uint_as_float(rounded & 0xffff0000u));
-  } else {
-    const float2 r =
-        __half22float2(*reinterpret_cast<const __half2*>(&rounded));
-    return pack16<AB_TYPE>(lo - r.x, hi - r.y);
   }
 }
 
@@ -257,8 +227,30 @@ __device__ __forceinline__ float sum_32(const float* f) {
   return a + b;
 }
 
+// Σ f[i]·g[i] of 32 values, two to an instruction, in four runs.
+__device__ __forceinline__ float dot_32(const float* f, const float* g) {
+  uint64_t s[2];
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    uint64_t x, y;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(x) : "f"(f[j]), "f"(f[j + 1]));
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(y) : "f"(g[j]), "f"(g[j + 1]));
+    if (j < 4)
+      asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(s[j >> 1]) : "l"(x), "l"(y));
+    else
+      asm("fma.rn.f32x2 %0, %1, %2, %0;\n"
+          : "+l"(s[(j >> 1) & 1])
+          : "l"(x), "l"(y));
+  }
+  asm("add.rn.f32x2 %0, %0, %1;\n" : "+l"(s[0]) : "l"(s[1]));
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(s[0]));
+  return a + b;
+}
+
 struct Maps {
   CUtensorMap x, xp, w;     // operands, 64 × 64 boxes
+  CUtensorMap logits;       // fp32, 32 × 32
   CUtensorMap g_in, g_out;  // G: 64 × 64, 64 × 32
   CUtensorMap dw;           // 64 × 32
   CUtensorMap slots, dw_slots;  // fp32, 32 × 32
@@ -336,7 +328,8 @@ struct Walk {
       : stage(FORWARD ? 3 : 0), j(pair_), pair(pair_), pairs(pairs_) {
     const VocabHeader* h = p.header;
     grad_v0 = phase * p.piece;
-    grad_n = phase < p.pieces ? min(p.piece, p.V - grad_v0) : 0;
+    // (kept logits: G is made outside)
+    grad_n = phase < p.pieces && !p.logits ? min(p.piece, p.V - grad_v0) : 0;
     back_v0 = grad_v0 - p.piece;
     back_n = phase > 0 ? min(p.piece, p.V - back_v0) : 0;
     tiles_m = vocab_tiles(rows);
@@ -539,13 +532,13 @@ __device__ __forceinline__ float pick(const float* f, int i) {
 
 
 // DEEP: sums of dW or dX may be more than kDeepSteps deep.  FEW: G is in two
-// parts (kVocabFewTokens).
-template <int AB_TYPE, bool FORWARD, bool DEEP, bool FEW>
+// parts (kVocabFewTokens).  SCORE: log probabilities, chunk `phase` of the rows.
+template <int AB_TYPE, bool FORWARD, bool DEEP, bool FEW, bool SCORE>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Maps maps,
                       const __grid_constant__ VocabCall p, const int phase,
                       const __grid_constant__ WaitCfg wc) {
-  using Sh = Shape<FORWARD>;
+  using Sh = Shape<!FORWARD || SCORE>;
   using Control = typename Sh::Control;
   constexpr int kStages = Sh::kStages;
   extern __shared__ unsigned char smem_raw[];
@@ -597,7 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const VocabHeader* header = p.header;
   const int learnt = header ? header->learnt : p.T;
   const int lo = FEW ? header->lo : 0;
-  const int all_rows = vocab_rows(learnt, lo);
+  const int row0 = SCORE ? (int)min((long long)phase * p.chunk, (long long)learnt)
+                         : 0;
+  const int all_rows =
+      SCORE ? min(learnt - row0, p.chunk) : vocab_rows(learnt, lo);
   Walk<FORWARD> walk(p, all_rows, phase, pair, pairs);
   Unit u;
   int it = 0, i = 0;  // steps and sums so far
@@ -633,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              : (const void*)&maps.g_in;
         const void* mb = u.kind == kDw ? mx : (const void*)&maps.w;
         // rows of G start at g_in, W's at the piece's first column
-        const int am = u.kind == kDx ? g_in + m0 : m0;
+        const int am = u.kind == kDx ? g_in + m0 : row0 + m0;
         const int ak = u.kind == kDw ? g_in : 0;
         const int bn = u.kind == kGrad ? walk.grad_v0 + n0 : n0;
         const int bk = u.kind == kDx ? walk.back_v0 : 0;
@@ -793,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto look_ahead = [&](auto in_logits) -> bool {
       if (!(decltype(in_logits)::value ? walk.next_logits(nu) : walk.next(nu)))
         return false;
-      int r = nu.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
+      int r = row0 + nu.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
       if (FEW && r >= lo) r -= lo;  // (both parts are one token's)
       if ((nu.kind == kStats || nu.kind == kGrad) && r < learnt) {
         n_token = learnt == p.T ? r : p.token[r];
@@ -805,6 +801,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       return true;
+    };
+    // staging: row (lane) of 128 bytes, its 16-byte chunk j at j ^ (row
+    // mod 8), the layout a 128-byte-swizzle TMA store reads
+    unsigned char* stg = smem + Sh::kOffStaging + (warp - 2) * kStagingBytes;
+    const uint32_t stg_s =
+        sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
+    // 32 columns of fp32: one staged block
+    auto stage_32 = [&](const float* f) {
+      if (lane == 0) bulk_wait_group_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+            make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
     };
     const bool deep = DEEP && phase > 0 && walk.deep(kDeepSteps);
     bool more = look_ahead(std::false_type());
@@ -820,7 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           token = n_token;
           seen = n_seen;
         }
-        const int r = u.tm * kVocabTile + (int)rank * kHalf + q * 32 + lane;
+        const int m0 = u.tm * kVocabTile + (int)rank * kHalf + q * 32;
+        const int r = row0 + m0 + lane;
         const int half = u.wide >> 1;  // this warp's columns
         const int n0 = u.tn * u.wide + h * half;
         uint32_t acc = my_tmem;
@@ -837,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc += h * half;
         }
         float peak = -INFINITY, sum = 0.f;
+        float slant = 0.f, largest = -INFINITY;  // (SCORE)
 #pragma unroll 1
         for (int c = 0; c < half; c += 32) {
           const int n = n0 + c;
@@ -860,6 +874,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             next = __reduce_min_sync(0xffffffffu, e.id[0]);
           }
+          if (SCORE && p.logits) {
+            stage_32(f);
+            if (lane == 0) {
+              if (!first_pass && m0 < all_rows)
+                tma_store_2d(&maps.logits, stg_s, n, m0);
+              bulk_commit_group();
+            }
+          }
           if (n + 32 > p.V) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -874,9 +896,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a stretch of -Inf only: every term is 0, not exp(-Inf + Inf)
           const float ref = now == -INFINITY ? 0.f : now;
           scale_add_32(f, c2, -ref);
+          if constexpr (SCORE) {
+            // Σ e·log2 e, e = 2^(z·c2 - ref): from the last reference to this
+            // one a term's logarithm moves by d.  A logit of -Inf has e = 0,
+            // and no logarithm below -1e30, so that their product is 0.
+            const float d = fmaxf(peak - ref, -1e30f), keep = exp2_fast(d);
+            float e[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = exp2_fast(f[j]);
-          sum = sum * exp2_fast(peak - ref) + sum_32(f);
+            for (int j = 0; j < 32; ++j) {
+              e[j] = exp2_fast(f[j]);
+              f[j] = fmaxf(f[j], -1e30f);
+            }
+            slant = keep * (slant + d * sum) + dot_32(e, f);
+            sum = sum * keep + sum_32(e);
+            largest = fmaxf(largest, here);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = exp2_fast(f[j]);
+            sum = sum * exp2_fast(peak - ref) + sum_32(f);
+          }
           peak = now;
         }
         if (first_pass || n0 >= p.V) continue;
@@ -886,14 +924,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     8ll * ((2ll * p.V + u.wide - 1) / u.wide) * learnt,
                     wc.status))
           *to = make_float2(peak, sum);
+        if constexpr (SCORE) {
+          float2* to2 = p.slants + (to - p.stats);
+          if (r < learnt &&
+              span_ok(to2, 8, p.slants,
+                      8ll * ((2ll * p.V + u.wide - 1) / u.wide) * learnt,
+                      wc.status))
+            *to2 = make_float2(slant, largest);
+        }
       }
+      if (SCORE && lane == 0) bulk_wait_group<0>();
     } else {
-      // staging: row (lane) of 128 bytes, its 16-byte chunk j at j ^ (row
-      // mod 8), the layout a 128-byte-swizzle TMA store reads
-      unsigned char* stg =
-          smem + Sh::kOffStaging + (warp - 2) * kStagingBytes;
-      const uint32_t stg_s =
-          sbase + Sh::kOffStaging + (warp - 2) * kStagingBytes;
       const float inv_scale = header->inv_scale;
       const float grad_scale = p.tau * header->scale;
       const bool dw_direct = !vocab_maps(p.dW, p.lddw);
@@ -1026,17 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 32; ++j) f[j] = 0.f;
             }
             if (wide) {
-              // fp32, 32 columns: one staged block
-              if (lane == 0) bulk_wait_group_read<0>();
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4*>(stg + lane * 128 +
-                                           ((j ^ (lane & 7)) << 4)) =
-                    make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2],
-                                f[4 * j + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
+              stage_32(f);
               if (lane == 0) {
                 if (u.kind == kDx) {
                   if (!first_pass && m0 < all_rows) {
@@ -1161,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           epilogues(std::integral_constant<Loop, kShallow>());
         }
       }
-      if (phase < p.pieces)
+      if (phase < p.pieces && !p.logits)
         epilogues(std::integral_constant<Loop, kLogits>());
       if (lane == 0) bulk_wait_group<0>();
     }
@@ -1225,6 +1256,9 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   // X as given may have no tensor map: then only the packed copy is read
   if (vocab_maps(p.X, p.ldx))
     ok = ok && encode(&maps->x, t16, 2, p.X, p.D, p.T, p.ldx, 64);
+  if (!grad && p.logits)
+    ok = ok && encode(&maps->logits, t32, 4, p.logits, p.V, p.chunk,
+                      p.ld_logits, 32);
   if (!grad) return ok;
   const long long g_rows = (p.pieces > 1 ? 2ll : 1ll) * p.g_rows;
   ok = ok && encode(&maps->g_in, t16, 2, p.G, p.piece, g_rows, p.piece, 64) &&
@@ -1239,19 +1273,24 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
   return ok;
 }
 
-template <int AB_TYPE, bool FORWARD, bool DEEP = false, bool FEW = false>
-cudaError_t launch(const VocabCall& p, const WaitCfg& wc,
-                   cudaStream_t stream) {
-  using Sh = Shape<FORWARD>;
+// Launches first to last - 1.
+template <int AB_TYPE, bool FORWARD, bool DEEP = false, bool FEW = false,
+          bool SCORE = false>
+cudaError_t launch(const VocabCall& p, const WaitCfg& wc, cudaStream_t stream,
+                   int first = 0, int last = 1) {
+  using Sh = Shape<!FORWARD || SCORE>;
   Maps maps;
   if (!make_maps<AB_TYPE>(p, !FORWARD, &maps)) return cudaErrorInvalidValue;
-  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD, DEEP, FEW>;
+  auto fn = vocab_gemm_kernel<AB_TYPE, FORWARD, DEEP, FEW, SCORE>;
   cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(fn), Sh::kSmemBytes);
-  const int phases = FORWARD ? 1 : p.pieces + 1;
-  for (int phase = 0; phase < phases && e == cudaSuccess; ++phase)
-    e = launch_pdl_cluster(fn, dim3(2 * p.pairs), dim3(kThreads),
-                           Sh::kSmemBytes, stream, 2, maps, p, phase, wc);
+  for (int phase = first; phase < last && e == cudaSuccess; ++phase) {
+    if (!FORWARD && p.logits)  // the piece's G
+      e = vocab_score_g(p, phase - 1, 2 * p.pairs, stream);
+    if (e == cudaSuccess)
+      e = launch_pdl_cluster(fn, dim3(2 * p.pairs), dim3(kThreads),
+                             Sh::kSmemBytes, stream, 2, maps, p, phase, wc);
+  }
   return e;
 }
 
@@ -1263,19 +1302,32 @@ cudaError_t vocab_forward(const VocabCall& c, const WaitCfg& wc,
                                        : vocab::launch<0, true>(c, wc, stream);
 }
 
+cudaError_t vocab_score(const VocabCall& c, const WaitCfg& wc, int phase,
+                        cudaStream_t stream) {
+  using vocab::launch;
+  return c.type == GEMM_F32_MIXED_BF16
+             ? launch<1, true, false, false, true>(c, wc, stream, phase,
+                                                   phase + 1)
+             : launch<0, true, false, false, true>(c, wc, stream, phase,
+                                                   phase + 1);
+}
+
 cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
                             cudaStream_t stream) {
   // dW sums over the tokens, dX over a piece's words
   const bool deep =
       std::max(vocab_steps(c.T), vocab_steps(c.piece)) > vocab::kDeepSteps;
   const bool few = c.T <= kVocabFewTokens;
+  // (of kept logits, no launch makes G alone)
+  const int first = c.logits ? 1 : 0, last = c.pieces + 1;
+  using vocab::launch;
   if (c.type == GEMM_F32_MIXED_BF16)
-    return few    ? vocab::launch<1, false, true, true>(c, wc, stream)
-           : deep ? vocab::launch<1, false, true>(c, wc, stream)
-                  : vocab::launch<1, false>(c, wc, stream);
-  return few    ? vocab::launch<0, false, true, true>(c, wc, stream)
-         : deep ? vocab::launch<0, false, true>(c, wc, stream)
-                : vocab::launch<0, false>(c, wc, stream);
+    return few    ? launch<1, false, true, true>(c, wc, stream, first, last)
+           : deep ? launch<1, false, true>(c, wc, stream, first, last)
+                  : launch<1, false>(c, wc, stream, first, last);
+  return few    ? launch<0, false, true, true>(c, wc, stream, first, last)
+         : deep ? launch<0, false, true>(c, wc, stream, first, last)
+                : launch<0, false>(c, wc, stream, first, last);
 }
 
 }  // namespace gemm_f32_impl

@@ -1,6 +1,7 @@
-// Vocabulary losses: softmax cross entropy and distillation of z = X·Wᵀ,
-// forward and backward (the definitions are in include/gemm_f32.h): argument
-// checks, workspace and launch.
+// Vocabulary losses and log probabilities: softmax cross entropy and
+// distillation of z = X·Wᵀ, the log probabilities of given words with entropy
+// and the likeliest others, forward and backward (the definitions are in
+// include/gemm_f32.h): argument checks, workspace and launch.
 //
 // Both losses are one computation.  Token t has a sparse target distribution
 // q_t (one entry for cross entropy, the teacher's softmax over its entries
@@ -17,6 +18,8 @@
 //      those rows only);
 //   2. the products (vocab_gemm.cu);
 //   3. the results from the products' partial ones.
+// Log probabilities are cross entropy with more results, and with the logits
+// kept for the gradients (vocab_score.cu).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -114,28 +117,6 @@ __global__ void __launch_bounds__(32 * kTeacherWarps)
   }
 }
 
-// Eight 16-bit elements from column c of n of a row, zeros past the end.
-// vec: the row is 16-byte aligned; else it is read in the aligned 4-byte
-// words that hold it (a word that lies partly outside the row is read as
-// single elements).
-__device__ __forceinline__ uint4 read_8(const uint16_t* __restrict__ src,
-                                        int c, int n, bool vec) {
-  if (vec && c + 8 <= n) return *reinterpret_cast<const uint4*>(src + c);
-  const int odd = (reinterpret_cast<uintptr_t>(src) >> 1) & 1;
-  if (c >= odd && c + 8 + odd <= n) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(src + c - odd);
-    const uint32_t a = w[0], b = w[1], d = w[2], e = w[3];
-    if (!odd) return make_uint4(a, b, d, e);
-    return make_uint4(__funnelshift_r(a, b, 16), __funnelshift_r(b, d, 16),
-                      __funnelshift_r(d, e, 16), __funnelshift_r(e, w[4], 16));
-  }
-  uint32_t e[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) e[j] = c + j < n ? src[c + j] : 0;
-  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
-                    e[6] | e[7] << 16);
-}
-
 // Rows first, first + stride, ... below `rows` of src, or those of them that
 // `to` numbers (to[row] >= 0: the row's place in dst), to 16-byte aligned
 // rows; a warp each, four chunks of 16 bytes a lane at a time.
@@ -222,7 +203,9 @@ __device__ void share_out(const VocabCall& p, int rows, int* s_end) {
   const int tiles = vocab_tiles(rows) * vocab_tiles(p.D);
   const int tall = vocab_tiles(p.piece), line = vocab_steps(p.piece);
   const int tiles_w = tall * ((p.D + dw_wide - 1) / dw_wide) * splits;
-  const int tiles_g = p.pieces > 1 ? vocab_tiles(rows) * tall : 0;
+  // (G of kept logits is made outside)
+  const int tiles_g =
+      p.pieces > 1 && !p.logits ? vocab_tiles(rows) * tall : 0;
   const int cost_w = max(
       1, tile_cost(vocab_steps(rows) / splits) * dw_wide / kVocabTile);
   const int cost_g = tile_cost(vocab_steps(p.D));
@@ -325,7 +308,10 @@ __global__ void __launch_bounds__(1024)
     all += learnt;
     before += learnt && t < own0;
     // (read whether learnt or not, so that no load waits for another)
-    const float g = scaled ? fabsf(p.grad_loss[t * p.grad_stride]) : 0.f;
+    float g = scaled ? fabsf(p.grad_loss[t * p.grad_stride]) : 0.f;
+    // (p·|log p + H| is at most 1/e + H)
+    if (scaled && p.grad_entropy)
+      g += fabsf(p.grad_entropy[t * p.entropy_stride]) * (0.4f + p.entropy[t]);
     most = fmaxf(most, learnt ? g : 0.f);
   }
   all = __reduce_add_sync(0xffffffffu, all);
@@ -358,6 +344,7 @@ __global__ void __launch_bounds__(1024)
           if (forward && !learnt) {
             p.loss[t] = 0.f;
             p.lse_out[t] = 0.f;
+            if (p.entropy_out) vocab_unscored(p, t);
           }
         }
       }
@@ -397,7 +384,7 @@ __global__ void __launch_bounds__(1024)
       share_out(p, vocab_rows(all, lo), s_end);
     if (threadIdx.x == 1023) {  // (a warp that does not share out)
       for (int w = 0; w < 31; ++w) most = fmaxf(most, s_most[w]);
-      most *= p.tau;
+      most *= p.entropy ? p.inv_tau : p.tau;
       // 0, Inf and NaN: no scale; outside 2^±100 only its power of two
       const float top = p.type == GEMM_F32_MIXED_F16 ? 16384.f : 1.f;
       float scale = 1.f, inv_scale = 1.f;
@@ -627,10 +614,12 @@ __global__ void __launch_bounds__(256)
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // Places a call's state in its workspace (c.token .. c.dw_max_splits), from
-// T, V, D and top alone; returns its bytes.  The pointers are offsets from
-// `ws` and only numbers where it is null.
+// T, V, D, top and what follows them alone; returns its bytes.  The pointers
+// are offsets from `ws` and only numbers where it is null.  alternatives: of
+// log probabilities (-1: of a loss), whose logits are kept or not.
 int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
-                int64_t top, bool grad, bool pack_w) {
+                int64_t top, bool grad, bool pack_w, int64_t alternatives = -1,
+                bool keep = false) {
   // A piece's G: small enough that it and its part of W stay near the L2
   // they are read from again (1800 learnt tokens of 6000, 65537 × 2048: 32,
   // 64, 128, 256 MB 1560, 1400, 1350, 1500 us a step), large enough that a
@@ -640,6 +629,9 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   constexpr int64_t kMostG = 128ll << 20;
   constexpr int64_t kMostSlots = 768ll << 20;
   constexpr int64_t kMostDwSlots = 128ll << 20;
+  // Logits of which the largest are looked for: those of as many tokens (but
+  // 256 at least) are stored at a time.
+  constexpr int64_t kMostLogits = 1ll << 30;
   const int64_t rows = std::max<int64_t>(T, 1);
   int64_t at = 0;
   auto take = [&](auto** to, int64_t bytes) {
@@ -654,7 +646,7 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   take(&c->ids, rows * top * 4);
   take(&c->weights, rows * top * 4);
   c->blocks = (int)((V + 127) / 128);
-  take(&c->starts, rows * c->blocks * 4);
+  take(&c->starts, alternatives < 0 ? rows * c->blocks * 4 : 0);
   c->ldxp = up(D, 8);
   char* bytes = nullptr;
   c->xp_rows = grad && T <= kVocabFewTokens ? 2 * up(rows, 32) : up(rows, 64);
@@ -671,8 +663,20 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
     // rounds of 256 × 256 tiles hold all logits
     const int64_t narrow = std::min<int64_t>(
         (V + 31) / 32 * rows, 2 * kVocabMaxPairs * 8 * kVocabTile);
-    take(&c->stats, std::max((V + 127) / 128 * rows, narrow) * 8);
+    const int64_t halves = std::max((V + 127) / 128 * rows, narrow);
+    take(&c->stats, halves * 8);
     take(&c->picked, rows * top * 4);
+    if (alternatives < 0) return at;
+    take(&c->slants, halves * 8);
+    c->chunk = (int)rows;
+    c->ld_logits = up(V, 8);
+    if (alternatives > 0 && !keep) {
+      c->chunk = (int)std::min<int64_t>(
+          rows, std::max<int64_t>(
+                    kVocabTile, kMostLogits / (4 * c->ld_logits) /
+                                    kVocabTile * kVocabTile));
+      take(&c->logits, c->chunk * c->ld_logits * 4);
+    }
     return at;
   }
   // equal pieces, whole tiles, of at most kMostG bytes of G
@@ -736,6 +740,15 @@ struct Request {
   int64_t lddx;
   void* dW;
   int64_t lddw;
+  // log probabilities
+  bool score;
+  float *entropy_out, *top_logp;
+  int64_t* top_out;
+  int64_t alternatives;
+  void* kept;
+  int64_t kept_bytes;
+  const float *entropy, *grad_entropy;
+  int64_t entropy_stride;
   void* ws;
   int64_t ws_bytes;
   gemm_f32_stream_t stream;
@@ -745,6 +758,28 @@ struct Request {
 bool countable(int64_t T, int64_t V, int64_t D) {
   return T <= kVocabMost && V <= kVocabMost && D <= kVocabMost &&
          T * D <= kVocabMostElements && V * D <= kVocabMostElements;
+}
+
+bool logits_countable(int64_t T, int64_t V) {
+  return vocab_tiles(T) * (V / kVocabTile + 1) <= 1 << 30;
+}
+
+// Bytes of the kept logits: whole rows on 32-byte boundaries.
+int64_t kept_bytes(int64_t T, int64_t V) { return T * up(V, 8) * 4; }
+
+// What log probabilities are given besides.
+int check_score(const Request& r) {
+  if (r.kept_bytes < 0 || (reinterpret_cast<uintptr_t>(r.kept) & 15u) != 0)
+    return GEMM_F32_ERR_INVALID_ARG;
+  if (r.alternatives < 0 || r.alternatives > kVocabMaxTop ||
+      r.alternatives > r.V || r.entropy_stride < 0)
+    return GEMM_F32_ERR_INVALID_ARG;
+  if (r.T == 0) return GEMM_F32_OK;
+  if (r.grad ? (!r.entropy || !r.kept) : !r.entropy_out)
+    return GEMM_F32_ERR_INVALID_ARG;
+  if (r.alternatives > 0 && (!r.top_logp || !r.top_out))
+    return GEMM_F32_ERR_INVALID_ARG;
+  return GEMM_F32_OK;
 }
 
 int check(const Request& r) {
@@ -768,7 +803,15 @@ int check(const Request& r) {
     if (r.grad ? (!r.lse || !r.grad_loss || !r.dX) : (!r.loss || !r.lse_out))
       return GEMM_F32_ERR_INVALID_ARG;
   }
+  if (r.score) {
+    const int st = check_score(r);
+    if (st != GEMM_F32_OK) return st;
+  }
   if (!countable(r.T, r.V, r.D)) return GEMM_F32_ERR_UNSUPPORTED;
+  if (r.kept && (!logits_countable(r.T, r.V)))
+    return GEMM_F32_ERR_UNSUPPORTED;
+  if (r.kept && r.kept_bytes < kept_bytes(r.T, r.V))
+    return GEMM_F32_ERR_INVALID_ARG;
   return GEMM_F32_OK;
 }
 
@@ -776,7 +819,7 @@ int check(const Request& r) {
 bool tiles_countable(const VocabCall& c, const Request& r) {
   const int64_t most = 1 << 30;
   const int64_t rows = vocab_tiles(r.T), wide = vocab_tiles(r.D);
-  if (rows * (r.V / kVocabTile + 1) > most) return false;
+  if (!logits_countable(r.T, r.V)) return false;
   if (!r.grad) return true;
   const int64_t tall = vocab_tiles(c.piece), line = vocab_steps(c.piece);
   return rows * wide * line <= most && tall * wide * vocab_steps(r.T) <= most &&
@@ -807,9 +850,19 @@ cudaError_t run_forward(VocabCall& c, int sms, const WaitCfg& wc,
   // One row of tiles takes its time whichever of its tokens are learnt from
   // (a row's statistics are its own): nothing is numbered, the results skip
   // the others.
-  if (c.T <= kVocabTile && !c.Wp && vocab_maps(c.X, c.ldx))
+  // (Kept logits have a row for each that is learnt from.)
+  const bool score = c.entropy_out != nullptr;
+  if (c.T <= kVocabTile && !c.Wp && vocab_maps(c.X, c.ldx) && !c.keep)
     c.header = nullptr;
   cudaError_t e = launch_targets(c, true, sms, stream);
+  if (score) {
+    for (int phase = 0; e == cudaSuccess && phase * (int64_t)c.chunk < c.T;
+         ++phase) {
+      e = vocab_score(c, wc, phase, stream);
+      if (e == cudaSuccess) e = vocab_score_results(c, phase, sms, stream);
+    }
+    return e;
+  }
   if (e == cudaSuccess) e = vocab_forward(c, wc, stream);
   if (e != cudaSuccess) return e;
   // a thread's share of a row: a few statistics
@@ -850,7 +903,8 @@ int run(const Request& r) {
   VocabCall c = {};
   const int64_t need =
       lay_out(&c, static_cast<char*>(r.ws), r.T, r.V, r.D, r.top, r.grad,
-              !vocab_maps(r.W, r.ldw));
+              !vocab_maps(r.W, r.ldw), r.score ? r.alternatives : -1,
+              r.kept != nullptr);
   if (!r.ws || (reinterpret_cast<uintptr_t>(r.ws) & 15u) != 0 ||
       r.ws_bytes < need)
     return GEMM_F32_ERR_INVALID_ARG;
@@ -879,6 +933,17 @@ int run(const Request& r) {
   c.grad_loss = r.grad_loss, c.grad_stride = r.grad_stride;
   c.dX = r.dX, c.lddx = r.lddx;
   c.dW = r.dW, c.lddw = r.lddw;
+  if (r.kept) {
+    c.logits = static_cast<float*>(r.kept);
+    c.ld_logits = up(r.V, 8);
+    c.chunk = c.T;
+    c.keep = 1;
+  }
+  c.entropy_out = r.entropy_out;
+  c.top_logp = r.top_logp, c.top_out = r.top_out;
+  c.alternatives = (int)r.alternatives;
+  c.entropy = r.entropy, c.grad_entropy = r.grad_entropy;
+  c.entropy_stride = r.entropy_stride;
   c.pairs = vocab_pairs(sms);
   c.status = wc.status;
   c.wide = c.pieces > 1 ? kVocabTile
@@ -965,6 +1030,71 @@ int gemm_f32_vocab_distill_grad(
   c.ws = workspace, c.ws_bytes = workspace_bytes;
   c.stream = stream;
   return run(c);
+}
+
+int gemm_f32_vocab_score(int type, int64_t T, int64_t V, int64_t D,
+                         const void* X, int64_t ldx, const void* W, int64_t ldw,
+                         const int64_t* ids, float temperature, int64_t top,
+                         float* logp, float* lse, float* entropy,
+                         float* top_logp, int64_t* top_ids, void* kept,
+                         int64_t kept_bytes, void* workspace,
+                         int64_t workspace_bytes, gemm_f32_stream_t stream) {
+  Request c = {};
+  c.type = type, c.T = T, c.V = V, c.D = D;
+  c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
+  c.targets = ids, c.top = 1, c.tau = temperature;
+  c.loss = logp, c.lse_out = lse;
+  c.score = true, c.entropy_out = entropy, c.alternatives = top;
+  c.top_logp = top_logp, c.top_out = top_ids;
+  c.kept = kept, c.kept_bytes = kept_bytes;
+  c.ws = workspace, c.ws_bytes = workspace_bytes;
+  c.stream = stream;
+  return run(c);
+}
+
+int gemm_f32_vocab_score_grad(
+    int type, int64_t T, int64_t V, int64_t D, const void* X, int64_t ldx,
+    const void* W, int64_t ldw, const int64_t* ids, float temperature,
+    const float* lse, const float* entropy, const void* kept,
+    int64_t kept_bytes, const float* grad_logp, int64_t logp_stride,
+    const float* grad_entropy, int64_t entropy_stride, void* dX, int64_t lddx,
+    void* dW, int64_t lddw, void* workspace, int64_t workspace_bytes,
+    gemm_f32_stream_t stream) {
+  Request c = {};
+  c.type = type, c.T = T, c.V = V, c.D = D;
+  c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
+  c.targets = ids, c.top = 1, c.tau = temperature;
+  c.grad = true, c.lse = lse, c.grad_loss = grad_logp, c.grad_stride = logp_stride;
+  c.dX = dX, c.lddx = lddx, c.dW = dW, c.lddw = lddw;
+  c.score = true, c.entropy = entropy, c.grad_entropy = grad_entropy;
+  c.entropy_stride = entropy_stride;
+  c.kept = const_cast<void*>(kept), c.kept_bytes = kept_bytes;
+  c.ws = workspace, c.ws_bytes = workspace_bytes;
+  c.stream = stream;
+  return run(c);
+}
+
+int64_t gemm_f32_vocab_score_kept_size(int64_t T, int64_t V) {
+  if (T < 0 || V < 1) return -GEMM_F32_ERR_INVALID_ARG;
+  if (!countable(T, V, 1) || !logits_countable(T, V))
+    return -GEMM_F32_ERR_UNSUPPORTED;
+  return kept_bytes(T, V);
+}
+
+int64_t gemm_f32_vocab_score_workspace_size(int64_t T, int64_t V, int64_t D,
+                                            int64_t top, int keep, int grad,
+                                            int aligned) {
+  if (T < 0 || V < 1 || D < 1 || top < 0 || top > kVocabMaxTop || top > V ||
+      (keep != 0 && keep != 1) || (grad != 0 && grad != 1) ||
+      (aligned != 0 && aligned != 1))
+    return -GEMM_F32_ERR_INVALID_ARG;
+  if (!countable(T, V, D)) return -GEMM_F32_ERR_UNSUPPORTED;
+  VocabCall c = {};
+  int64_t n =
+      lay_out(&c, nullptr, T, V, D, 1, false, aligned == 0, top, keep != 0);
+  if (grad)  // (room for either call)
+    n = std::max(n, lay_out(&c, nullptr, T, V, D, 1, true, aligned == 0, 0));
+  return n;
 }
 
 int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V, int64_t D,

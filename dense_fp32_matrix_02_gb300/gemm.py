@@ -134,6 +134,18 @@ def lib() -> ctypes.CDLL:
         L.gemm_f32_vocab_workspace_size.restype = i64
         L.gemm_f32_vocab_workspace_size.argtypes = [i64, i64, i64, i64, ci,
                                                     ci]
+        L.gemm_f32_vocab_score.restype = ci
+        L.gemm_f32_vocab_score.argtypes = head + [vp, cf, i64, vp, vp, vp, vp,
+                                                  vp, vp, i64, vp, i64, vp]
+        L.gemm_f32_vocab_score_grad.restype = ci
+        L.gemm_f32_vocab_score_grad.argtypes = head + [
+            vp, cf, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+            i64, vp]
+        L.gemm_f32_vocab_score_kept_size.restype = i64
+        L.gemm_f32_vocab_score_kept_size.argtypes = [i64, i64]
+        L.gemm_f32_vocab_score_workspace_size.restype = i64
+        L.gemm_f32_vocab_score_workspace_size.argtypes = [i64, i64, i64, i64,
+                                                          ci, ci, ci]
         L.gemm_f32_grad_norm.restype = ci
         L.gemm_f32_grad_norm.argtypes = [i64, vp, vp, vp, i64, vp]
         L.gemm_f32_grad_clip.restype = ci

@@ -20,7 +20,7 @@ import array
 import torch
 
 from . import gemm as _g
-from .loss import _new, _on, _stream
+from .loss import _bytes, _new, _on, _stream
 
 __all__ = ["global_norm", "clip_", "workspace_size"]
 
@@ -101,18 +101,10 @@ def _table(tensors, out):
 
 
 def _scratch(workspace, n, device, stream):
+    """(workspace, pointer, bytes), allocated when not given."""
     if workspace is None:
-        size = workspace_size(n)
-        workspace = _new(size, torch.uint8, device, stream)
-    else:
-        if not isinstance(workspace, torch.Tensor):
-            raise TypeError("workspace must be a torch tensor")
-        if workspace.device != device:
-            raise ValueError("workspace must live on the gradients' device")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        size = workspace.numel() * workspace.element_size()
-    return workspace, workspace.data_ptr() or None, size
+        workspace = _new(workspace_size(n), torch.uint8, device, stream)
+    return _bytes(workspace, "workspace", device, "the gradients'")
 
 
 def global_norm(tensors, workspace=None, stream=None):

@@ -1,16 +1,22 @@
-"""Vocabulary losses of torch CUDA tensors (argument marshalling only).
+"""Vocabulary losses and log probabilities of torch CUDA tensors (argument
+marshalling only).
 
 The last product of a language model, logits = x·wᵀ with x (tokens × width)
 the hidden states and w (vocab × width) the output matrix, together with its
-loss: softmax cross entropy, or distillation from a teacher's top logits.
-The logits are never stored; ``include/gemm_f32.h`` (gemm_f32_vocab_*) gives
-the formulas.  Like every call of the binding these are asynchronous on
+loss: softmax cross entropy, or distillation from a teacher's top logits; or
+with the log probabilities of given words, their distribution's entropy and
+the likeliest other words.  The losses never store the logits;
+``include/gemm_f32.h`` (gemm_f32_vocab_*) gives the formulas.  Like every call of the binding these are asynchronous on
 ``stream`` (None: the current one), raise ``GemmError`` for a status other
 than 0, and take an optional ``workspace`` (a CUDA tensor of at least
 ``workspace_size`` bytes; allocated here when None).
 
     loss, lse = cross_entropy(x, w, targets)             # per token, fp32
     dx, dw = cross_entropy_grad(x, w, targets, lse, grad_loss)
+
+    s = log_probs(x, w, ids, top=5)        # s.logp, s.entropy, s.top_ids, …
+    s = log_probs(x, w, ids, keep=True)    # with the logits, for the gradients
+    dx, dw = log_probs_grad(x, w, ids, s, grad_logp, grad_entropy)
 
 Autograd records none of this: results of inputs that require gradients have
 no graph, and the gradients come from the _grad calls, which overwrite dx and
@@ -21,12 +27,14 @@ from __future__ import annotations
 
 import contextlib
 import functools
+import typing
 
 import torch
 
 from . import gemm as _g
 
 __all__ = ["cross_entropy", "cross_entropy_grad", "distill", "distill_grad",
+           "LogProbs", "log_probs", "log_probs_grad", "score_workspace_size",
            "workspace_size"]
 
 _TYPES = {torch.bfloat16: _g.MIXED_BF16, torch.float16: _g.MIXED_F16}
@@ -50,6 +58,23 @@ def workspace_size(tokens, vocab, width, top=1, grad=False,
     rows are multiples of 8 elements apart."""
     return _size(int(tokens), int(vocab), int(width), int(top),
                  int(bool(grad)), int(bool(aligned)))
+
+
+@functools.lru_cache(maxsize=256)
+def _score_size(tokens, vocab, width, top, keep, grad, aligned):
+    n = int(_g.lib().gemm_f32_vocab_score_workspace_size(
+        tokens, vocab, width, top, keep, grad, aligned))
+    if n < 0:
+        _g._check(-n, "gemm_f32_vocab_score_workspace_size")
+    return n
+
+
+def score_workspace_size(tokens, vocab, width, top=0, keep=False, grad=False,
+                         aligned=True) -> int:
+    """Workspace bytes of log_probs, or of log_probs_grad with ``grad``;
+    ``aligned`` as for workspace_size."""
+    return _score_size(int(tokens), int(vocab), int(width), int(top),
+                       int(bool(keep)), int(bool(grad)), int(bool(aligned)))
 
 
 def _matrix(t, name, dtypes, like=None):
@@ -138,20 +163,23 @@ def _out(t, shape, dtype, device, name, stream):
     return t, p, ld
 
 
+def _bytes(t, name, device, whose="x's"):
+    """(tensor, pointer, bytes) of a buffer."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must live on {whose} device")
+    if not t.is_contiguous():  # (an expanded one has fewer bytes)
+        raise ValueError(f"{name} must be contiguous")
+    return t, t.data_ptr() or None, t.numel() * t.element_size()
+
+
 def _scratch(workspace, head, top, grad, aligned, device, stream):
     """(workspace, pointer, bytes), allocated when not given."""
     if workspace is None:
         n = _size(head[1], head[2], head[3], top, grad, aligned)
         workspace = _new(n, torch.uint8, device, stream)
-    else:
-        if not isinstance(workspace, torch.Tensor):
-            raise TypeError("workspace must be a torch tensor")
-        if workspace.device != device:
-            raise ValueError("workspace must live on x's device")
-        if not workspace.is_contiguous():  # (an expanded one has fewer bytes)
-            raise ValueError("workspace must be contiguous")
-        n = workspace.numel() * workspace.element_size()
-    return workspace, workspace.data_ptr() or None, n
+    return _bytes(workspace, "workspace", device)
 
 
 def _stream(stream, device):
@@ -240,3 +268,95 @@ def distill_grad(x, w, top_logits, top_ids, lse, grad_loss, temperature=1.0,
     return _backward("gemm_f32_vocab_distill_grad", x, w, head, aligned,
                      teacher[0], (*teacher, float(temperature)), lse,
                      grad_loss, dx, dw, workspace, stream)
+
+
+class LogProbs(typing.NamedTuple):
+    """What log_probs returns: float32 values per token, top_logp and
+    top_ids (int64) tokens × top or None, and the kept logits or None."""
+    logp: torch.Tensor
+    lse: torch.Tensor
+    entropy: torch.Tensor
+    top_logp: torch.Tensor | None
+    top_ids: torch.Tensor | None
+    kept: torch.Tensor | None
+
+
+def log_probs(x, w, ids, top=0, temperature=1.0, keep=False, workspace=None,
+              stream=None):
+    """LogProbs of one given word per token (ids: int64) under
+    softmax(logits/temperature): its log probability, lse = log Σ
+    exp(logits/temperature), the distribution's entropy and, with ``top``, the
+    likeliest words, largest first, equal logits by the lower id.  A token
+    whose id is outside [0, vocab) is not scored (zeros; ids of -1).  ``keep``:
+    the logits stay in memory (4 bytes each) for log_probs_grad."""
+    head, aligned = _operands(x, w)
+    device, T, V = x.device, head[1], head[2]
+    y, _ = _vector(ids, "ids", T, torch.int64, device)
+    top, keep = int(top), int(bool(keep))
+    if top < 0:
+        raise ValueError("top must not be negative")
+    with _on(device):
+        # (one allocation for the three: they are views of it)
+        out = _new((3, T), torch.float32, device, stream)
+        logp, lse, entropy = out.unbind()
+        top_logp = top_ids = kept = None
+        tp = ip = kp = None
+        kn = 0
+        if top:
+            top_logp = _new((T, top), torch.float32, device, stream)
+            top_ids = _new((T, top), torch.int64, device, stream)
+            tp, ip = top_logp.data_ptr() or None, top_ids.data_ptr() or None
+        if keep:
+            kn = int(_g.lib().gemm_f32_vocab_score_kept_size(T, V))
+            if kn < 0:
+                _g._check(-kn, "gemm_f32_vocab_score_kept_size")
+            kept = _new(kn, torch.uint8, device, stream)
+            kp = kept.data_ptr() or None
+        if workspace is None:
+            workspace = _new(_score_size(T, V, head[3], top, keep, 0, aligned),
+                             torch.uint8, device, stream)
+        workspace, wp, n = _bytes(workspace, "workspace", device)
+        op = out.data_ptr()
+        st = _g.lib().gemm_f32_vocab_score(
+            *head, y, float(temperature), top, op or None,
+            op + 4 * T or None, op + 8 * T or None, tp, ip, kp, kn, wp, n,
+            _stream(stream, device))
+    if st:
+        _g._check(st, "gemm_f32_vocab_score")
+    return LogProbs(logp, lse, entropy, top_logp, top_ids, kept)
+
+
+def log_probs_grad(x, w, ids, scores, grad_logp, grad_entropy=None,
+                   temperature=1.0, dx=None, dw=None, workspace=None,
+                   stream=None):
+    """(dx, dw) in x's dtype from the gradients of each token's logp and
+    entropy (float32; an expanded scalar is taken as it is; None: 0).
+    ``scores``: what log_probs returned for the same operands, ids and
+    temperature with ``keep``."""
+    head, aligned = _operands(x, w)
+    device, (_, T, V, D) = x.device, head[:4]
+    y, _ = _vector(ids, "ids", T, torch.int64, device)
+    if scores.kept is None:
+        raise ValueError("the gradients need the logits: log_probs(keep=True)")
+    lp, _ = _vector(scores.lse, "lse", T, torch.float32, device)
+    hp, _ = _vector(scores.entropy, "entropy", T, torch.float32, device)
+    _, kp, kn = _bytes(scores.kept, "kept", device)
+    ap, a_step = _vector(grad_logp, "grad_logp", T, torch.float32, device,
+                         expand=True)
+    bp, b_step = None, 0
+    if grad_entropy is not None:
+        bp, b_step = _vector(grad_entropy, "grad_entropy", T, torch.float32,
+                             device, expand=True)
+    with _on(device):
+        dx, dxp, lddx = _out(dx, (T, D), x.dtype, device, "dx", stream)
+        dw, dwp, lddw = _out(dw, (V, D), x.dtype, device, "dw", stream)
+        if workspace is None:
+            workspace = _new(_score_size(T, V, D, 0, 1, 1, aligned),
+                             torch.uint8, device, stream)
+        workspace, wp, n = _bytes(workspace, "workspace", device)
+        st = _g.lib().gemm_f32_vocab_score_grad(
+            *head, y, float(temperature), lp, hp, kp, kn, ap, a_step, bp,
+            b_step, dxp, lddx, dwp, lddw, wp, n, _stream(stream, device))
+    if st:
+        _g._check(st, "gemm_f32_vocab_score_grad")
+    return dx, dw

@@ -517,6 +517,71 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
                                                    int64_t D, int64_t top,
                                                    int grad, int aligned);
 
+/*
+ * Log probabilities of given words, with entropy and the likeliest others.
+ *
+ * X, W, type and z = X·Wᵀ as for the losses above, τ the temperature:
+ *   lse_t     = log Σ_v exp(z[t][v]/τ),
+ *   logp_t    = z[t][ids[t]]/τ − lse_t,
+ *   entropy_t = −Σ_v p·log p,  p = exp(z[t][v]/τ − lse_t)  (0·log 0 = 0),
+ * and for top > 0 the `top` words of the largest logits, largest first, equal
+ * ones by the lower id: top_ids[t·top + j] and their log probabilities
+ * top_logp[t·top + j].  They are ranked by Σ_k X·W as the operands give it (to
+ * 2^-46 of the sum's terms) among the top + 8 largest of the fp32 logits, so
+ * that neither rank nor log probability hangs on the order of a sum; a logit
+ * that is NaN ranks last.  0 <= top <= min(256, V); top_logp and top_ids may
+ * be NULL for top = 0.  A token whose id is outside [0, V) is not scored: its
+ * logp, lse, entropy and top_logp are 0, its top_ids -1, whatever its row of X
+ * holds.
+ *
+ * `kept`, where it is not NULL, receives the logits for the gradients: 16-byte
+ * aligned device memory of at least gemm_f32_vocab_score_kept_size(T, V) bytes
+ * (4 an element), whose layout is the library's own.
+ *
+ * gemm_f32_vocab_score_grad takes ids, lse, entropy and kept as the forward
+ * call of the same operands left them, and the gradients of logp
+ * (a_t = grad_logp[t·logp_stride]) and entropy (b_t =
+ * grad_entropy[t·entropy_stride], 0 where grad_entropy is NULL); strides of 0
+ * give every token one value.  It writes
+ *   G[t][v] = (a_t·([v = ids[t]] − p) − b_t·p·(log p + entropy_t)) / τ,
+ *   dX = G·W (T×D, lddx),   dW = Gᵀ·X (V×D, lddw)
+ * as the losses' _grad forms do (rounding, order and overlap included; G's
+ * scale goes by the largest (|a_t| + |b_t|·(0.4 + entropy_t))/τ).
+ *
+ * Workspace, limits, empty calls and errors are those of the losses, with
+ * gemm_f32_vocab_score_workspace_size bytes; for top > 0 without `kept` it
+ * holds the logits of as many tokens at a time as 1 GB takes (256 at least).
+ * GEMM_F32_ERR_INVALID_ARG also for top outside [0, min(256, V)], a kept that
+ * is misaligned, too small or (gradients) NULL, and a negative stride.
+ */
+GEMM_F32_API int gemm_f32_vocab_score(
+    int type, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
+    const void *W, int64_t ldw, const int64_t *ids, float temperature,
+    int64_t top, float *logp, float *lse, float *entropy, float *top_logp,
+    int64_t *top_ids, void *kept, int64_t kept_bytes, void *workspace,
+    int64_t workspace_bytes, gemm_f32_stream_t stream);
+
+GEMM_F32_API int gemm_f32_vocab_score_grad(
+    int type, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
+    const void *W, int64_t ldw, const int64_t *ids, float temperature,
+    const float *lse, const float *entropy, const void *kept,
+    int64_t kept_bytes, const float *grad_logp, int64_t logp_stride,
+    const float *grad_entropy, int64_t entropy_stride, void *dX, int64_t lddx,
+    void *dW, int64_t lddw, void *workspace, int64_t workspace_bytes,
+    gemm_f32_stream_t stream);
+
+/* Bytes of the kept logits of T tokens (no device call).  Minus a status on
+ * error. */
+GEMM_F32_API int64_t gemm_f32_vocab_score_kept_size(int64_t T, int64_t V);
+
+/* Workspace bytes of the log probabilities (no device call): the forward call
+ * (grad = 0; keep = 1: with `kept`) or the gradients (grad = 1; enough for the
+ * forward call of the same arguments too); `aligned` as for
+ * gemm_f32_vocab_workspace_size.  Minus a status on error. */
+GEMM_F32_API int64_t gemm_f32_vocab_score_workspace_size(
+    int64_t T, int64_t V, int64_t D, int64_t top, int keep, int grad,
+    int aligned);
+
 /* Element types of a gradient (the first two: gemm_f32_mixed_type's). */
 typedef enum {
     GEMM_F32_GRAD_BF16 = 0,
