@@ -78,7 +78,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // itself, with one sum in Grad 2048 to 4096 deep).  So the rule goes by what
 // both calls see: all tokens where the forward call may number none.
 __device__ __forceinline__ int sum_steps(const VocabCall& p, int learnt) {
-  return p.T <= 8 ? 4 : learnt <= kVocabTile ? 8 : 16;
+  return p.T <= 8 ? 4 : learnt <= kVocabTile || p.slants ? 8 : 16;
 }
 
 // Steps that an accumulator sums for dW and dX, whose results are rounded to
@@ -180,6 +180,23 @@ __device__ __forceinline__ void tma_add_2d(const void* tmap, uint32_t src,
       "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group "
       "[%0, {%2, %3}], [%1];\n" ::"l"(tmap),
       "r"(src), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// Stores a block that is not read for long: its lines are the first to leave
+// L2.
+__device__ __forceinline__ uint64_t leave_first() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void tma_store_2d_hint(const void* tmap, uint32_t src,
+                                                  int c0, int c1,
+                                                  uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group"
+      ".L2::cache_hint [%0, {%2, %3}], [%1], %4;\n" ::"l"(tmap),
+      "r"(src), "r"(c0), "r"(c1), "l"(policy)
       : "memory");
 }
 
@@ -878,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage_32(f);
             if (lane == 0) {
               if (!first_pass && m0 < all_rows)
-                tma_store_2d(&maps.logits, stg_s, n, m0);
+                tma_store_2d_hint(&maps.logits, stg_s, n, m0, leave_first());
               bulk_commit_group();
             }
           }

@@ -11,7 +11,7 @@
 // (half tiles) with the largest maxima, of equal ones the first: any element
 // elsewhere has k larger ones before it, or equal ones with lower ids.  So the
 // logits are stored, of some tokens at a time, and of each row only those
-// stretches are read, k·128 of V logits.  Storing costs the products nothing
+// stretches are read, about k·128 of V logits.  Storing costs the products nothing
 // where they are bound by the tensor cores, and 2·T/D of the weights' bytes
 // where they are bound by those.
 //   The rank of two logits should not hang on how a sum rounds (on the tile it
@@ -34,6 +34,14 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718056f;
 
+// Numbers in the order of the floats, from kLowest on; a NaN counts as -Inf.
+constexpr uint32_t kLowest = 0x007fffffu;
+__device__ __forceinline__ uint32_t order_of(float f) {
+  if (f != f) return kLowest;
+  const uint32_t u = __float_as_uint(f + 0.f);  // (-0 as 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
 // ------------------------------------------------------------- statistics
 struct Stat {
   float m, s, e;  // r, S, E
@@ -55,6 +63,7 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b) {
 }
 
 __device__ __forceinline__ Stat merge_over(Stat st, int from) {
+#pragma unroll 1
   for (int o = from; o < 32; o <<= 1) {
     Stat b;
     b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
@@ -63,6 +72,65 @@ __device__ __forceinline__ Stat merge_over(Stat st, int from) {
     st = merge(st, b);
   }
   return st;
+}
+
+// The same over all lanes, in one step: the references first.
+__device__ __forceinline__ float reference_of(uint32_t order) {
+  const uint32_t u = order & 0x80000000u ? order ^ 0x80000000u : ~order;
+  return __uint_as_float(u);
+}
+__device__ __forceinline__ Stat merge_warp(Stat st) {
+  const float m = reference_of(
+      __reduce_max_sync(0xffffffffu, order_of(st.m)));
+  const float ref = m == -INFINITY ? 0.f : m;
+  const float d = moved(st.m, ref), keep = exp2f(d);
+  float e = keep * (st.e + d * st.s), s = keep * st.s;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    e += __shfl_xor_sync(0xffffffffu, e, o);
+  }
+  return Stat{m, s, e};
+}
+
+// The statistics first, first + step, ... of row r, with what each addition
+// rounds off kept (a large vocabulary is many additions); each one's largest
+// logit goes to `largest`.
+template <typename Largest>
+__device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
+                                         int parts, int step, int learnt,
+                                         Largest largest) {
+  Stat st = {-INFINITY, 0.f, 0.f};
+  float lost = 0.f, lost_e = 0.f;
+#pragma unroll 4
+  for (int g = first; g < parts; g += step) {
+    const long long i = (long long)g * learnt + r;
+    const float2 b = p.stats[i], more2 = p.slants[i];
+    largest(g, more2.y);
+    const float m = fmaxf(st.m, b.x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float da = moved(st.m, ref), db = moved(b.x, ref);
+    const float ka = exp2f(da), kb = exp2f(db);
+    const float was = st.s * ka, was_e = ka * (st.e + da * st.s);
+    const float more = b.y * kb - lost * ka;
+    const float more_e = kb * (more2.x + db * b.y) - lost_e * ka;
+    st = Stat{m, was + more, was_e + more_e};
+    lost = (st.s - was) - more;
+    lost_e = (st.e - was_e) - more_e;
+  }
+  return st;
+}
+
+// A row's results; at: its word's logit / τ.
+__device__ __forceinline__ float store_results(const VocabCall& p, long long t,
+                                               bool scored, Stat st, float at) {
+  const float log_sum = logf(st.s), l = st.m * kLn2 + log_sum;
+  // (the difference of equal numbers where one word has all: not below 0)
+  const float entropy = log_sum - kLn2 * (st.e / st.s);
+  p.loss[t] = scored ? at - l : 0.f;
+  p.lse_out[t] = scored ? l : 0.f;
+  p.entropy_out[t] = scored && !(entropy < 0.f) ? entropy : 0.f;
+  return l;
 }
 
 // logp, lse and entropy of the rows from row0 on: 8 rows a block, blockDim / 8
@@ -87,28 +155,8 @@ __global__ void __launch_bounds__(1024)
     if (!p.header) scored = vocab_is_learnt(p, t);
     if (scored) at = p.picked[r];
   }
-  // This thread's share, with what each addition rounds off kept (a large
-  // vocabulary is many additions).
-  Stat st = {-INFINITY, 0.f, 0.f};
-  float lost = 0.f, lost_e = 0.f;
-  if (here) {
-#pragma unroll 4
-    for (int g = slice; g < parts; g += blockDim.x >> 3) {
-      const long long i = (long long)g * learnt + r;
-      const float2 b = p.stats[i];
-      const float be = p.slants[i].x;
-      const float m = fmaxf(st.m, b.x);
-      const float ref = m == -INFINITY ? 0.f : m;
-      const float da = moved(st.m, ref), db = moved(b.x, ref);
-      const float ka = exp2f(da), kb = exp2f(db);
-      const float was = st.s * ka, was_e = ka * (st.e + da * st.s);
-      const float more = b.y * kb - lost * ka;
-      const float more_e = kb * (be + db * b.y) - lost_e * ka;
-      st = Stat{m, was + more, was_e + more_e};
-      lost = (st.s - was) - more;
-      lost_e = (st.e - was_e) - more_e;
-    }
-  }
+  Stat st = share_of(p, r, here ? slice : parts, parts, blockDim.x >> 3, learnt,
+                     [](int, float) {});
   st = merge_over(st, 8);
   const int warps = blockDim.x >> 5;
   if (warps > 1) {
@@ -121,63 +169,50 @@ __global__ void __launch_bounds__(1024)
     st = merge_over(st, 8);
   }
   if (!here || lane >= 8) return;
-  const float log_sum = logf(st.s), l = st.m * kLn2 + log_sum;
-  p.loss[t] = scored ? at - l : 0.f;
-  p.lse_out[t] = scored ? l : 0.f;
-  // (the difference of equal numbers where one word has all: not below 0)
-  const float entropy = log_sum - kLn2 * (st.e / st.s);
-  p.entropy_out[t] = scored && !(entropy < 0.f) ? entropy : 0.f;
+  store_results(p, t, scored, st, at);
 }
 
 // ------------------------------------------------------- likeliest words
-constexpr int kTopThreads = 256;
-constexpr int kSpare = 8;       // ranked beyond those asked for
+constexpr int kSpare = 8;  // ranked beyond those asked for
 constexpr int kMostRanked = kVocabMaxTop + kSpare;
-constexpr int kCandidates = 1024;
+constexpr int kStretches = 512;    // read at most, but for equal maxima
+constexpr int kCandidates = 1024;  // ranked at most, but for equal logits
 constexpr int kHeldKeys = 2048;
-
-// Numbers in the order of the floats, from kLowest on; a NaN counts as -Inf.
-constexpr uint32_t kLowest = 0x007fffffu;
-__device__ __forceinline__ uint32_t order_of(float f) {
-  if (f != f) return kLowest;
-  const uint32_t u = __float_as_uint(f + 0.f);  // (-0 as 0)
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
 
 struct SelectState {
   int hist[256];
   int digit, left;
-  int gt[kTopThreads / 32], eq[kTopThreads / 32];
+  int gt[32], eq[32];
 };
 
-// The k-th largest of n >= k keys, and how many of those equal to it are
-// among the k: the digits of its number, 8 bits at a time, from a histogram of
-// the keys that begin as it does.
-template <typename Key>
+// The k-th largest of n >= k keys, and how many of those equal to it are among
+// the k: 8 bits at a time, from a histogram of the keys that begin as it does.
+template <int THREADS, typename Key>
 __device__ __forceinline__ uint32_t kth_largest(SelectState& s, int n, int k,
                                                 Key key, int& equal) {
+  const int tid = threadIdx.x;
   uint32_t prefix = 0;
   int left = k;
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    s.hist[threadIdx.x] = 0;
+    for (int b = tid; b < 256; b += THREADS) s.hist[b] = 0;
     __syncthreads();
 #pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kTopThreads) {
+    for (int i = tid; i < n; i += THREADS) {
       const uint32_t x = key(i);
       if (shift == 24 || (x ^ prefix) >> (shift + 8) == 0)
         atomicAdd(&s.hist[(x >> shift) & 255], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {  // 8 bins a lane, the largest first
-      const int top = 255 - 8 * (int)threadIdx.x;
+    if (tid < 32) {  // 8 bins a lane, the largest first
+      const int top = 255 - 8 * tid;
       int sum = 0;
 #pragma unroll
       for (int b = 0; b < 8; ++b) sum += s.hist[top - b];
       int upto = sum;
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if ((int)threadIdx.x >= o) upto += v;
+        if (tid >= o) upto += v;
       }
       int before = upto - sum;
       if (before < left && left <= upto) {
@@ -196,16 +231,65 @@ __device__ __forceinline__ uint32_t kth_largest(SelectState& s, int n, int k,
   return prefix;
 }
 
+// A bound that at least k of n >= k keys in [low, high] reach, and not many
+// more: the range in 256 steps, and the step with the k-th largest in 256
+// again while it holds many.  (Keys of one row mostly differ in their last 24
+// bits: a histogram of the first 8 would have one bin, and every atomic on it
+// in turn.)
+template <int THREADS, typename Key>
+__device__ __forceinline__ uint32_t reached_by(SelectState& s, int n, int k,
+                                               uint32_t low, uint32_t high,
+                                               Key key) {
+  constexpr int kEnough = 32;
+  const int tid = threadIdx.x;
+  for (;;) {
+    const int shift = max(0, 24 - __clz(high - low));
+    for (int b = tid; b < 256; b += THREADS) s.hist[b] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < n; i += THREADS) {
+      const uint32_t x = key(i);
+      // (what is above the range is in the last bin)
+      if (x >= low) atomicAdd(&s.hist[min((x - low) >> shift, 255u)], 1);
+    }
+    __syncthreads();
+    if (tid < 32) {  // 8 bins a lane, the largest first
+      const int top = 255 - 8 * tid;
+      int sum = 0;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) sum += s.hist[top - b];
+      int upto = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (tid >= o) upto += v;
+      }
+      int before = upto - sum;
+      if (before < k && k <= upto) {
+        int b = 0;
+        while (before + s.hist[top - b] < k) before += s.hist[top - b++];
+        s.digit = top - b;
+        s.left = s.hist[top - b];
+      }
+    }
+    __syncthreads();
+    const uint32_t step = low + ((uint32_t)s.digit << shift);
+    if (s.left <= kEnough || shift == 0) return step;
+    low = step;
+    high = min(high, step + (1u << shift) - 1u);
+    __syncthreads();
+  }
+}
+
 // put(place, i) for the keys above `least` and the first `equal` of those
 // equal to it, in order.
-template <typename Key, typename Put>
+template <int THREADS, typename Key, typename Put>
 __device__ __forceinline__ void in_order(SelectState& s, int n, int k,
                                          uint32_t least, int equal, Key key,
                                          Put put) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int gt0 = 0, eq0 = 0;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n && gt0 + min(eq0, equal) < k; i0 += kTopThreads) {
+  for (int i0 = 0; i0 < n && gt0 + min(eq0, equal) < k; i0 += THREADS) {
     const int i = i0 + threadIdx.x;
     const uint32_t x = i < n ? key(i) : 0;
     const bool gt = i < n && x > least, eq = i < n && x == least;
@@ -219,7 +303,7 @@ __device__ __forceinline__ void in_order(SelectState& s, int n, int k,
     int gt_at = gt0 + __popc(gts & ((1u << lane) - 1u));
     int eq_at = eq0 + __popc(eqs & ((1u << lane) - 1u));
 #pragma unroll
-    for (int w = 0; w < kTopThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) gt_at += s.gt[w], eq_at += s.eq[w];
       gt0 += s.gt[w];
       eq0 += s.eq[w];
@@ -245,15 +329,26 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
   asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t v;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(v) : "l"(a), "l"(b));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(v) : "l"(a), "l"(b), "l"(c));
   return v;
 }
-__device__ __forceinline__ double both(uint64_t v) {
-  float a, b;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
-  return (double)a + (double)b;
+__device__ __forceinline__ float2 apart(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+// a + b as the sum of two numbers, x its rounding to fp32 (Knuth's two-sum).
+// Of two such sums the larger has the larger x, or the same and the larger y.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float x = a + b, part = x - a;
+  return make_float2(x, (a - (x - part)) + (b - part));
+}
+__device__ __forceinline__ float2 add_exactly(float2 a, float2 b) {
+  const float2 sum = two_sum(a.x, b.x);
+  return two_sum(sum.x, sum.y + (a.y + b.y));
 }
 
 template <int AB_TYPE>
@@ -265,154 +360,298 @@ __device__ __forceinline__ uint64_t widen(uint32_t w) {
 }
 
 // Σ x·w over a warp: a product of two 16-bit floats is exact in fp32; each
-// addition keeps what it rounds off (Knuth's two-sum), in a second sum.
-template <int AB_TYPE>
-__device__ __forceinline__ double exact_dot(const uint16_t* x, const uint16_t* w,
-                                            int n, int lane) {
-  const bool vx = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-  const bool vw = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+// addition keeps what it rounds off, in a second sum.  (In fp64 this took
+// twice the time: two additions a clock and SM.)
+struct ExactSum {
   uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll 2
-  for (int c = 8 * lane; c < n; c += 256) {
-    const uint4 a = read_8(x, c, n, vx), b = read_8(w, c, n, vw);
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w};
-    const uint32_t bv[4] = {b.x, b.y, b.z, b.w};
+  template <int AB_TYPE>
+  __device__ __forceinline__ void add(uint4 x, uint4 w) {
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      // (h + a·b, its product exact; with back = -part of the two-sum)
       uint64_t &h = hi[j & 1], &l = lo[j & 1];
-      const uint64_t term = mul2(widen<AB_TYPE>(av[j]), widen<AB_TYPE>(bv[j]));
-      const uint64_t sum = add2(h, term), part = sub2(sum, h);
-      l = add2(l, add2(sub2(h, sub2(sum, part)), sub2(term, part)));
+      const uint64_t a = widen<AB_TYPE>(xs[j]), b = widen<AB_TYPE>(ws[j]);
+      const uint64_t sum = fma2(a, b, h), back = sub2(h, sum);
+      l = add2(l, sub2(h, add2(sum, back)));
+      l = add2(l, fma2(a, b, back));
       h = sum;
     }
   }
-  double v = (both(hi[0]) + both(hi[1])) + (both(lo[0]) + both(lo[1]));
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+};
+// WORDS rows of W at a time, AHEAD loads of each side by side (a row of W comes from far).
+template <int AB_TYPE, int WORDS, int AHEAD>
+__device__ __forceinline__ void exact_dots(const uint16_t* x,
+                                           const uint16_t* const (&w)[WORDS],
+                                           int n, int lane,
+                                           float2 (&v)[WORDS]) {
+  bool even = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i)
+    even = even && (reinterpret_cast<uintptr_t>(w[i]) & 15u) == 0;
+  ExactSum sum[WORDS];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int whole = even ? n & ~7 : 0;
+#pragma unroll 1
+  for (int c = 8 * lane; c < whole; c += 256 * AHEAD) {
+    uint4 b[WORDS][AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int at = c + 256 * j;
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i)
+        b[i][j] = at < whole ? *reinterpret_cast<const uint4*>(w[i] + at) : zero;
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {  // (x is near)
+      const int at = c + 256 * j;
+      const uint4 a =
+          at < whole ? *reinterpret_cast<const uint4*>(x + at) : zero;
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) sum[i].template add<AB_TYPE>(a, b[i][j]);
+    }
+  }
+#pragma unroll 1
+  for (int c = whole + 8 * lane; c < n; c += 256) {
+    const uint4 a = read_8(x, c, n, false);
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      sum[i].template add<AB_TYPE>(a, read_8(w[i], c, n, false));
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    const float2 h0 = apart(sum[i].hi[0]), h1 = apart(sum[i].hi[1]);
+    const float2 l0 = apart(sum[i].lo[0]), l1 = apart(sum[i].lo[1]);
+    v[i] = add_exactly(
+        add_exactly(two_sum(h0.x, l0.x), two_sum(h0.y, l0.y)),
+        add_exactly(two_sum(h1.x, l1.x), two_sum(h1.y, l1.y)));
+  }
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      v[i] = add_exactly(v[i],
+                         make_float2(__shfl_xor_sync(0xffffffffu, v[i].x, o),
+                                     __shfl_xor_sync(0xffffffffu, v[i].y, o)));
 }
 
-// A row a block.
-template <int AB_TYPE>
-__global__ void __launch_bounds__(kTopThreads)
+// A row a block: its results, and its likeliest words.
+template <int AB_TYPE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     top_kernel(const __grid_constant__ VocabCall p, int row0) {
+  constexpr int kWarps = THREADS / 32;
   __shared__ SelectState s;
+  __shared__ Stat s_stat[kWarps];
+  __shared__ uint2 s_range[kWarps];
   __shared__ uint32_t s_key[kHeldKeys];  // of the stretches, then candidates
-  __shared__ int s_stretch[kMostRanked], s_id[kMostRanked];
-  __shared__ int s_candidate[kCandidates], s_count;
-  __shared__ double s_value[kMostRanked];
+  __shared__ int s_stretch[kStretches], s_id[kMostRanked];
+  __shared__ int s_candidate[kCandidates], s_stretches, s_count;
+  __shared__ float2 s_value[kMostRanked];
   static_assert(kCandidates <= kHeldKeys, "candidates' keys");
   griddep_wait();
   griddep_launch_dependents();
   const int learnt = p.header ? p.header->learnt : p.T;
   const int wide = p.header ? p.header->wide : p.wide;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = row0 + blockIdx.x;
   if (r >= learnt) return;
   const long long t = learnt != p.T ? p.token[r] : r;
   if (!p.header && !vocab_is_learnt(p, t)) {
-    if (threadIdx.x == 0) vocab_unscored(p, t);
+    if (tid == 0) {
+      store_results(p, t, false, Stat{0.f, 1.f, 0.f}, 0.f);
+      vocab_unscored(p, t);
+    }
     return;
   }
   const int bits = 30 - __clz(wide), half = 1 << bits;  // a stretch
   const int parts = (int)((2ll * p.V + wide - 1) / wide);
   const int k = min(p.alternatives + kSpare, p.V);
   const float* z = p.logits + (long long)blockIdx.x * p.ld_logits;
-  const int tid = threadIdx.x;
+  if (tid == 0) s_stretches = s_count = 0;
 
-  // the stretches
-  uint32_t least = 0;
-  int stretches = parts;
-  if (parts > k) {
-    auto maximum = [&](int g) {
-      return order_of(p.slants[(long long)g * learnt + r].y);
-    };
-    const bool held = parts <= kHeldKeys;
-    if (held) {
-#pragma unroll 4
-      for (int g = tid; g < parts; g += kTopThreads) s_key[g] = maximum(g);
-      __syncthreads();
-    }
-    auto key = [&](int g) { return held ? s_key[g] : maximum(g); };
-    int equal;
-    least = kth_largest(s, parts, k, key, equal);
-    in_order(s, parts, k, least, equal, key,
-             [&](int at, int g) { s_stretch[at] = g; });
-    stretches = k;
-  } else {
-    for (int g = tid; g < parts; g += kTopThreads) s_stretch[g] = g;
+  // the statistics, and the stretches' maxima
+  const bool held = parts <= kHeldKeys;
+  uint32_t low = 0xffffffffu, high = 0;
+  Stat st = share_of(p, r, tid, parts, THREADS, learnt, [&](int g, float z) {
+    const uint32_t x = order_of(z);
+    if (held) s_key[g] = x;
+    low = min(low, x);
+    high = max(high, x);
+  });
+  st = merge_warp(st);
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    s_stat[warp] = st;
+    s_range[warp] = make_uint2(low, high);
   }
-  if (tid == 0) s_count = 0;
   __syncthreads();
+  st = Stat{-INFINITY, 0.f, 0.f};
+  if (lane < kWarps) {
+    st = s_stat[lane];
+    low = s_range[lane].x;
+    high = s_range[lane].y;
+  }
+  st = merge_warp(st);
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  const float lse = __shfl_sync(0xffffffffu, st.m * kLn2 + logf(st.s), 0);
+  if (tid == 0) store_results(p, t, true, st, p.picked[r]);
 
-  // Their elements; past the vocabulary none, which no k elements need.
-  const int n = stretches << bits;
-  auto column = [&](int i) {
-    return (s_stretch[i >> bits] << bits) + (i & (half - 1));
+  auto maximum = [&](int g) {
+    return held ? s_key[g] : order_of(p.slants[(long long)g * learnt + r].y);
   };
-  auto key = [&](int i) -> uint32_t {
-    const int v = column(i);
-    return v < p.V &&
-                   span_ok(z + v, 4, p.logits, 4ll * p.chunk * p.ld_logits,
-                           p.status)
-               ? order_of(z[v])
-               : 0u;
+  auto logit = [&](int v) -> uint32_t {  // past the vocabulary below all others
+    const float* at = z + min(v, p.V - 1);
+    float f = 0.f;
+    if (span_ok(at, 4, p.logits, 4ll * p.chunk * p.ld_logits, p.status))
+      f = *at;
+    return v < p.V ? order_of(f) : 0u;
   };
-  // Those that the smallest of the maxima leaves are few, unless many are
-  // equal or the stretches are all there are.
-  bool few = parts > k;
-  if (few) {
-#pragma unroll 4
-    for (int i = tid; i < n; i += kTopThreads) {
-      const uint32_t x = key(i);
-      if (x >= least) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kCandidates) {
-          s_key[at] = x;
-          s_candidate[at] = column(i);
+  auto candidate = [&](int v, uint32_t x) {
+    const int at = atomicAdd(&s_count, 1);
+    if (at < kCandidates) {
+      s_key[at] = x;
+      s_candidate[at] = v;
+    }
+  };
+  // A bound that k elements reach: one that k maxima reach, or elements where
+  // there are fewer stretches.  Little more than k reach it, unless many are
+  // equal.
+  bool few;
+  if (parts > k) {
+    const uint32_t least =
+        reached_by<THREADS>(s, parts, k, low, high, maximum);
+    for (int g = tid; g < parts; g += THREADS)
+      if (maximum(g) >= least) {
+        const int at = atomicAdd(&s_stretches, 1);
+        if (at < kStretches) s_stretch[at] = g;
+      }
+    __syncthreads();
+    const int stretches = s_stretches;
+    few = stretches <= kStretches;
+    if (few) {
+      // (128 columns a warp at a time, of one stretch or of several narrow
+      // ones, and of four such runs side by side)
+      const int per = 128 >> bits, sub = lane >> (bits - 2);
+      const int in = 4 * (lane & ((half >> 2) - 1));
+      const int runs = (stretches + per - 1) / per;
+#pragma unroll 1
+      for (int i = warp; i < runs; i += 4 * kWarps) {
+        float4 f[4];
+        int v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = (i + j * kWarps) * per + sub;
+          v[j] = (s_stretch[min(at, stretches - 1)] << bits) + in;
+          const float* from = z + min(v[j], (p.V - 1) & ~3);
+          f[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (span_ok(from, 16, p.logits, 4ll * p.chunk * p.ld_logits, p.status))
+            f[j] = *reinterpret_cast<const float4*>(from);
+          if (at >= stretches) v[j] = p.V;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float g[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t x = order_of(g[q]);
+            if (x >= least && v[j] + q < p.V) candidate(v[j] + q, x);
+          }
         }
       }
     }
-    __syncthreads();
-    few = s_count <= kCandidates;
+  } else {
+    const uint32_t least =
+        reached_by<THREADS>(s, p.V, k, kLowest, high, logit);
+#pragma unroll 4
+    for (int v = tid; v < p.V; v += THREADS) {
+      const uint32_t x = logit(v);
+      if (x >= least) candidate(v, x);
+    }
+    few = true;
   }
+  __syncthreads();
+  const int count = s_count;
+  few = few && count <= kCandidates;
   if (few) {
-    const int count = s_count;
-    for (int c = tid; c < count; c += kTopThreads) {
+    for (int c = tid; c < count; c += THREADS) {
       const uint32_t x = s_key[c];
       const int id = s_candidate[c];
       int rank = 0;
+#pragma unroll 4
       for (int o = 0; o < count; ++o)
         rank += s_key[o] > x || (s_key[o] == x && s_candidate[o] < id);
       if (rank < k) s_id[rank] = id;
     }
   } else {
-    int equal;
-    least = kth_largest(s, n, k, key, equal);
-    in_order(s, n, k, least, equal, key,
-             [&](int at, int i) { s_id[at] = column(i); });
+    // Many are equal: the k first stretches, in order, and of their elements
+    // the k first.
+    int stretches = parts, equal;
+    auto largest = [&](int g) {  // (what is held of them is gone)
+      return order_of(p.slants[(long long)g * learnt + r].y);
+    };
+    __syncthreads();
+    if (parts > k) {
+      stretches = k;
+      const uint32_t least =
+          kth_largest<THREADS>(s, parts, k, largest, equal);
+      in_order<THREADS>(s, parts, k, least, equal, largest,
+                        [&](int at, int g) { s_stretch[at] = g; });
+    } else {
+      for (int g = tid; g < parts; g += THREADS) s_stretch[g] = g;
+      __syncthreads();
+    }
+    const int n = stretches << bits;
+    auto column = [&](int i) {
+      return (s_stretch[i >> bits] << bits) + (i & (half - 1));
+    };
+    auto element = [&](int i) { return logit(column(i)); };
+    const uint32_t least = kth_largest<THREADS>(s, n, k, element, equal);
+    in_order<THREADS>(s, n, k, least, equal, element,
+                      [&](int at, int i) { s_id[at] = column(i); });
   }
   __syncthreads();
 
   // ranked by their values before any rounding
   const uint16_t* x = static_cast<const uint16_t*>(p.X) + t * p.ldx;
-  for (int c = tid >> 5; c < k; c += kTopThreads / 32) {
-    const int id = s_id[c];
-    double v = exact_dot<AB_TYPE>(
-        x, static_cast<const uint16_t*>(p.W) + id * p.ldw, p.D, tid & 31);
-    if (v != v) v = z[id];  // (infinities: the sum's, not of what it rounds off)
-    if (v != v) v = -INFINITY;
-    if ((tid & 31) == 0) s_value[c] = v;
+  // (many rows: two words a warp, which share x; few: one, with more of it
+  // side by side)
+  constexpr int kWords = THREADS == 1024 ? 1 : 2;
+  for (int c0 = warp * kWords; c0 < k; c0 += kWarps * kWords) {
+    const uint16_t* w[kWords];
+    float2 v[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      w[i] = static_cast<const uint16_t*>(p.W) + s_id[min(c0 + i, k - 1)] * p.ldw;
+    exact_dots<AB_TYPE, kWords, kWords == 1 ? 4 : 2>(x, w, p.D, lane, v);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (lane == i && c0 + i < k) {
+        // (an infinity has no remainder; a NaN is ranked last)
+        if (!(fabsf(v[i].x) < INFINITY))
+          v[i] = make_float2(z[s_id[c0 + i]], 0.f);
+        if (v[i].x != v[i].x) v[i].x = -INFINITY;
+        s_value[c0 + i] = v[i];
+      }
   }
   __syncthreads();
-  for (int c = tid; c < k; c += kTopThreads) {
-    const double v = s_value[c];
+  for (int c = tid; c < k; c += THREADS) {
+    const float2 v = s_value[c];
     const int id = s_id[c];
     int rank = 0;
-    for (int o = 0; o < k; ++o)
-      rank += s_value[o] > v || (s_value[o] == v && s_id[o] < id);
+#pragma unroll 4
+    for (int o = 0; o < k; ++o) {
+      const float2 w = s_value[o];
+      const bool equal = w.x == v.x;
+      rank += w.x > v.x || (equal && (w.y > v.y || (w.y == v.y && s_id[o] < id)));
+    }
     if (rank < p.alternatives) {
       p.top_out[t * p.alternatives + rank] = id;
+      // v / τ − lse, the quotient with its remainder
+      const float q = v.x / p.tau, rest = fmaf(-q, p.tau, v.x) + v.y;
       p.top_logp[t * p.alternatives + rank] =
-          (float)(v / (double)p.tau - (double)p.lse_out[t]);
+          fabsf(q) < INFINITY ? (q - lse) + rest / p.tau : q - lse;
     }
   }
 }
@@ -514,17 +753,24 @@ __global__ void __launch_bounds__(kGThreads)
 cudaError_t vocab_score_results(const VocabCall& c, int phase, int sms,
                                 cudaStream_t stream) {
   const int row0 = phase * c.chunk, rows = std::min(c.chunk, c.T - row0);
-  // a thread's share of a row: a few statistics
-  const int parts = (c.V + 127) / 128;
-  const int threads = parts <= 16 ? 32 : parts <= 128 ? 256 : 1024;
-  cudaError_t e = launch_pdl(finish_score_kernel, dim3((rows + 7) / 8),
-                             dim3(threads), 0, stream, c, row0);
-  if (e != cudaSuccess || c.alternatives == 0) return e;
-  return c.type == GEMM_F32_MIXED_BF16
-             ? launch_pdl(top_kernel<1>, dim3(rows), dim3(kTopThreads), 0,
-                          stream, c, row0)
-             : launch_pdl(top_kernel<0>, dim3(rows), dim3(kTopThreads), 0,
-                          stream, c, row0);
+  if (c.alternatives == 0) {
+    // a thread's share of a row: a few statistics
+    const int parts = (c.V + 127) / 128;
+    const int threads = parts <= 16 ? 32 : parts <= 128 ? 256 : 1024;
+    return launch_pdl(finish_score_kernel, dim3((rows + 7) / 8), dim3(threads),
+                      0, stream, c, row0);
+  }
+  // A block's warps each sum one word's exact logit at a time.  Where there is
+  // about a row to an SM, nothing else hides the wait for their rows of W.
+  const bool wide = rows <= 2 * sms;
+  auto launch = [&](auto* fn, int threads) {
+    return launch_pdl(fn, dim3(rows), dim3(threads), 0, stream, c, row0);
+  };
+  if (c.type == GEMM_F32_MIXED_BF16)
+    return wide ? launch(top_kernel<1, 1024>, 1024)
+                : launch(top_kernel<1, 256>, 256);
+  return wide ? launch(top_kernel<0, 1024>, 1024)
+              : launch(top_kernel<0, 256>, 256);
 }
 
 cudaError_t vocab_score_g(const VocabCall& c, int piece, int sms,
