@@ -161,6 +161,8 @@ struct VocabCall {
   int chunk, keep;      // of `chunk` in turn; or null
   // gradients
   int piece, pieces;  // columns of G; the pieces of the vocabulary
+  float4* terms;      // log probabilities: what G needs of each learnt row
+  int* goals;         // (score_terms), and its word
   void* G;            // [2 · g_rows][piece]: two pieces' G in turn (one
                       // piece: [g_rows][piece])
   int g_rows;
@@ -246,6 +248,84 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// Log probabilities' G = (a·([v = y] − p) − b·p·(log p + H))/τ, of the kept
+// logits z: with t = z·c − lse·log2 e, c = log2 e / τ, p = 2^t,
+//   G = p·(A + B·t) + [v = y]·a,  A = −(a + b·H),  B = −b·ln 2
+// (a, b: times 1/τ and the scale of G).  Of a row: A, B, a, −lse·log2 e.
+__device__ __forceinline__ float4 score_terms(const VocabCall& p, long long t) {
+  const float scale = p.header->scale * p.inv_tau;
+  const float a = p.grad_loss[t * p.grad_stride] * scale;
+  const float b =
+      p.grad_entropy ? p.grad_entropy[t * p.entropy_stride] * scale : 0.f;
+  return make_float4(-(a + b * p.entropy[t]), -b * 0.69314718056f, a,
+                     -p.lse[t] * 1.4426950408889634f);
+}
+
+// A warp's part of G: 1024 columns from c0 on of row r in a piece of the
+// vocabulary that starts at v0 and has `cols` columns, with zeros up to `all`;
+// of few tokens (lo > 0) in two parts.  here: the row is a token's.
+constexpr int kVocabGRun = 1024;
+template <int AB_TYPE, typename Terms>
+__device__ __forceinline__ void score_g_run(const VocabCall& p, uint16_t* G,
+                                            int r, int c0, int v0, int cols,
+                                            int all, int lo, bool here,
+                                            int lane, Terms terms_of) {
+  constexpr int kRuns = kVocabGRun / 256;
+  const float c2 = p.inv_tau * 1.4426950408889634f;
+  const float* z = p.logits + (long long)r * p.ld_logits + v0;
+  float f[kRuns][8];
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    const int c = c0 + 256 * i + 8 * lane;
+    if (here && c + 8 <= cols) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(z + c));
+      const float4 y = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
+      f[i][0] = x.x, f[i][1] = x.y, f[i][2] = x.z, f[i][3] = x.w;
+      f[i][4] = y.x, f[i][5] = y.y, f[i][6] = y.z, f[i][7] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[i][j] = here && c + j < cols ? z[c + j] : -INFINITY;
+    }
+  }
+  float4 of = make_float4(0.f, 0.f, 0.f, 0.f);
+  int goal = -1;
+  if (here) terms_of(of, goal);
+  goal -= v0;
+  const long long extent = 2ll * (p.pieces > 1 ? 2 : 1) * p.g_rows * p.piece;
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    const int c = c0 + 256 * i + 8 * lane;
+    if (c >= all) break;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = fmaf(f[i][j], c2, of.w), e = exp2_fast(t);
+      // (2^-200 is 0: an infinity's product with it would not be)
+      const float g = e * fmaf(of.y, fmaxf(t, -200.f), of.x);
+      f[i][j] = here && c + j < cols ? g : 0.f;
+    }
+    if (goal >= c && goal < c + 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (goal == c + j) f[i][j] += of.z;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = pack16<AB_TYPE>(f[i][2 * j], f[i][2 * j + 1]);
+    uint16_t* to = G + (long long)r * p.piece + c;
+    if (!span_ok(to, 16, p.G, extent, p.status)) continue;
+    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (!lo) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = pack16_rest<AB_TYPE>(f[i][2 * j], f[i][2 * j + 1], w[j]);
+    to += (long long)lo * p.piece;
+    if (span_ok(to, 16, p.G, extent, p.status))
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // What a token that is not scored is given besides.
 __device__ __forceinline__ void vocab_unscored(const VocabCall& c,
                                                long long t) {

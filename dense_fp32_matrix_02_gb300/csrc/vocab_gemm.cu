@@ -549,7 +549,8 @@ __device__ __forceinline__ float pick(const float* f, int i) {
 
 
 // DEEP: sums of dW or dX may be more than kDeepSteps deep.  FEW: G is in two
-// parts (kVocabFewTokens).  SCORE: log probabilities, chunk `phase` of the rows.
+// parts (kVocabFewTokens).  SCORE: log probabilities; forward, chunk `phase` of
+// the rows; gradients, where the epilogue warps make the next piece's G.
 template <int AB_TYPE, bool FORWARD, bool DEEP, bool FEW, bool SCORE>
 __global__ void __launch_bounds__(kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ Maps maps,
@@ -607,10 +608,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const VocabHeader* header = p.header;
   const int learnt = header ? header->learnt : p.T;
   const int lo = FEW ? header->lo : 0;
-  const int row0 = SCORE ? (int)min((long long)phase * p.chunk, (long long)learnt)
+  constexpr bool CHUNK = FORWARD && SCORE;
+  const int row0 = CHUNK ? (int)min((long long)phase * p.chunk, (long long)learnt)
                          : 0;
   const int all_rows =
-      SCORE ? min(learnt - row0, p.chunk) : vocab_rows(learnt, lo);
+      CHUNK ? min(learnt - row0, p.chunk) : vocab_rows(learnt, lo);
   Walk<FORWARD> walk(p, all_rows, phase, pair, pairs);
   Unit u;
   int it = 0, i = 0;  // steps and sums so far
@@ -737,9 +739,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (warp - 2) >> 2;  // column half
     const uint32_t my_tmem = tmem + ((uint32_t)(q * 32) << 16);
     const float c2 = p.inv_tau * kLog2e;
-    // waits for the next sum; its accumulator's address
-    auto arrived = [&](uint32_t& acc) -> bool {
+    // G of the next piece, of kept logits: runs of columns of it, every
+    // warp's in turn, while it has nothing else to do.  (As a kernel of its own
+    // it took 61 us beside 132 us of products, 8192 × 32000 × 768.)
+    constexpr bool MAKE_G = !FORWARD && SCORE;
+    long long run = 0, run_end = 0;
+    int runs = 1;
+    if (MAKE_G && phase < p.pieces) {
+      runs = (min(p.piece, p.V - walk.grad_v0) + kVocabGRun - 1) / kVocabGRun;
+      run = (long long)blockIdx.x * kEpiWarps + warp - 2;
+      run_end = (long long)((learnt + 63) / 64 * 64) * runs;
+    }
+    auto make_run = [&]() {
+      const int r = (int)(run / runs), at = (int)(run - (long long)r * runs);
+      const int cols = min(p.piece, p.V - walk.grad_v0);
+      score_g_run<AB_TYPE>(
+          p, static_cast<uint16_t*>(p.G) + (long long)g_out * p.piece, r,
+          at * kVocabGRun, walk.grad_v0, cols, (cols + 63) / 64 * 64, 0,
+          r < learnt, lane, [&](float4& of, int& goal) {
+            of = p.terms[r];
+            goal = p.goals[r];
+          });
+      run += (long long)gridDim.x * kEpiWarps;
+    };
+    // waits for the next sum; its accumulator's address.  (between: of a tile's
+    // sums, whose join is in registers)
+    auto arrived = [&](uint32_t& acc, auto between) -> bool {
       const int b = i & 1;
+      if constexpr (MAKE_G && !decltype(between)::value) {
+        while (ok && run < run_end &&
+               !__any_sync(0xffffffffu,
+                           mbar_test_wait(acc_full(b), (i >> 1) & 1)))
+          make_run();
+      }
       const bool here = ok && bounded_wait(acc_full(b), (i >> 1) & 1,
                                            wc.limit, abort, kSleepNs);
       if (!__all_sync(0xffffffffu, here)) {
@@ -764,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (acc: its address, this warp's columns.)
     auto join_sums = [&](int half, int steps, int most,
                          uint32_t& acc) -> bool {
-      if (!arrived(acc)) return false;
+      if (!arrived(acc, std::false_type())) return false;
       acc += h * half;
       float f[128];
 #pragma unroll
@@ -782,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (steps <= most) break;
         release();
-        if (!arrived(acc)) return false;
+        if (!arrived(acc, std::true_type())) return false;
         acc += h * half;
       }
 #pragma unroll
@@ -863,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the warp's first entry: most stretches of columns have none
         int next = __reduce_min_sync(0xffffffffu, e.id[0]);
         if (!several) {
-          if (!first_pass && !arrived(acc)) break;
+          if (!first_pass && !arrived(acc, std::false_type())) break;
           acc += h * half;
         }
         float peak = -INFINITY, sum = 0.f;
@@ -1006,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool wide =
               !LOGITS && (u.kind == kDx || header->dw_splits > 1);
           if (!several) {
-            if (!first_pass && !arrived(acc)) break;
+            if (!first_pass && !arrived(acc, std::false_type())) break;
             acc += h * half;
           }
           if (!LOGITS && u.kind == kDw && !wide && !dw_direct) {
@@ -1209,8 +1241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           epilogues(std::integral_constant<Loop, kShallow>());
         }
       }
-      if (phase < p.pieces && !p.logits)
+      if constexpr (MAKE_G) {
+        while (ok && run < run_end) make_run();
+      } else if (phase < p.pieces && !p.logits) {
         epilogues(std::integral_constant<Loop, kLogits>());
+      }
       if (lane == 0) bulk_wait_group<0>();
     }
   }
@@ -1302,7 +1337,8 @@ cudaError_t launch(const VocabCall& p, const WaitCfg& wc, cudaStream_t stream,
   cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(fn), Sh::kSmemBytes);
   for (int phase = first; phase < last && e == cudaSuccess; ++phase) {
-    if (!FORWARD && p.logits)  // the piece's G
+    // the piece's G, but where the launch before made it
+    if (!FORWARD && p.logits && (!SCORE || phase == first))
       e = vocab_score_g(p, phase - 1, 2 * p.pairs, stream);
     if (e == cudaSuccess)
       e = launch_pdl_cluster(fn, dim3(2 * p.pairs), dim3(kThreads),
@@ -1338,6 +1374,17 @@ cudaError_t vocab_gradients(const VocabCall& c, const WaitCfg& wc,
   // (of kept logits, no launch makes G alone)
   const int first = c.logits ? 1 : 0, last = c.pieces + 1;
   using vocab::launch;
+  if (c.logits && !few) {
+    if (c.type == GEMM_F32_MIXED_BF16)
+      return deep ? launch<1, false, true, false, true>(c, wc, stream, first,
+                                                        last)
+                  : launch<1, false, false, false, true>(c, wc, stream, first,
+                                                         last);
+    return deep ? launch<0, false, true, false, true>(c, wc, stream, first,
+                                                      last)
+                : launch<0, false, false, false, true>(c, wc, stream, first,
+                                                       last);
+  }
   if (c.type == GEMM_F32_MIXED_BF16)
     return few    ? launch<1, false, true, true>(c, wc, stream, first, last)
            : deep ? launch<1, false, true>(c, wc, stream, first, last)

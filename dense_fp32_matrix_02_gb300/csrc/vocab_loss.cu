@@ -679,6 +679,8 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
     }
     return at;
   }
+  take(&c->terms, alternatives < 0 ? 0 : rows * 16);
+  take(&c->goals, alternatives < 0 ? 0 : rows * 4);
   // equal pieces, whole tiles, of at most kMostG bytes of G
   const int64_t g_rows = up(rows, kVocabTile);
   const int64_t widest = std::max<int64_t>(

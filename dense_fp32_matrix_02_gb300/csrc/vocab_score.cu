@@ -20,9 +20,11 @@
 // bits), and ranked by that.
 //
 // Gradients.  G = (a·([v = y] − p) − b·p·(log p + H))/τ from the kept logits,
-// one pass bound by memory (4 bytes read and 2 written an element), a piece of
-// the vocabulary at a time, which then is in L2 for the products.  Making the
-// logits again would cost 2·D operations an element instead.
+// 4 bytes read and 2 written an element, a piece of the vocabulary at a time,
+// which then is in L2 for the products: the first piece by a kernel of its own,
+// bound by memory, the later ones by the products' epilogue warps, which
+// otherwise wait for the tensor cores most of the time (vocab_gemm.cu).  Making
+// the logits again would cost 2·D operations an element instead.
 #include <algorithm>
 
 #include "gemm_f32.h"
@@ -32,7 +34,7 @@
 namespace gemm_f32_impl {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718056f;
+constexpr float kLn2 = 0.69314718056f;
 
 // Numbers in the order of the floats, from kLowest on; a NaN counts as -Inf.
 constexpr uint32_t kLowest = 0x007fffffu;
@@ -657,13 +659,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 }
 
 // ------------------------------------------------------------- gradients
-constexpr int kGThreads = 256, kGColumns = 16 * kGThreads;
-
 // G of a piece's columns, in the rows of the learnt tokens, with zeros up to
 // the multiples of 64 that its products sum over; of few tokens in two parts
-// (VocabHeader::lo).  With p = 2^t, t = z·c − lse·log2 e,
-//   G = p·(A + B·t) + [v = y]·a,  A = −(a + b·H),  B = −b·ln 2
-// (a, b: times 1/τ and the scale of G).
+// (VocabHeader::lo).  Of the first piece, with what the later ones need of
+// each row.
+constexpr int kGThreads = 256;
+
 template <int AB_TYPE>
 __global__ void __launch_bounds__(kGThreads)
     score_g_kernel(const __grid_constant__ VocabCall p, int piece) {
@@ -673,78 +674,28 @@ __global__ void __launch_bounds__(kGThreads)
   const int learnt = h->learnt, lo = h->lo;
   const int rows = lo ? lo : (learnt + 63) / 64 * 64;
   const int v0 = piece * p.piece, cols = min(p.piece, p.V - v0);
-  const int all = (cols + 63) / 64 * 64, segments = (all + kGColumns - 1) / kGColumns;
-  const float c2 = p.inv_tau * kLog2e, scale = h->scale * p.inv_tau;
+  const int all = (cols + 63) / 64 * 64;
+  const int runs = (all + kVocabGRun - 1) / kVocabGRun;
   uint16_t* G = static_cast<uint16_t*>(p.G) +
                 (long long)(piece & 1) * p.g_rows * p.piece;
-  const long long extent = 2ll * p.g_rows * p.piece;
+  const int lane = threadIdx.x & 31;
+  const long long first =
+      (long long)blockIdx.x * (kGThreads / 32) + (threadIdx.x >> 5);
 #pragma unroll 1
-  for (long long u = blockIdx.x; u < (long long)rows * segments;
-       u += gridDim.x) {
-    const int r = (int)(u / segments), seg = (int)(u - (long long)r * segments);
-    float A = 0.f, B = 0.f, a = 0.f, shift = 0.f;
-    int target = -1;
-    const bool here = r < learnt;
-    if (here) {
-      const long long t = learnt != p.T ? p.token[r] : r;
-      const float entropy = p.entropy[t];
-      a = p.grad_loss[t * p.grad_stride] * scale;
-      const float b =
-          p.grad_entropy ? p.grad_entropy[t * p.entropy_stride] * scale : 0.f;
-      A = -(a + b * entropy);
-      B = -b * kLn2;
-      shift = -p.lse[t] * kLog2e;
-      target = (int)p.targets[t] - v0;
-    }
-    const float* z = p.logits + (long long)r * p.ld_logits + v0;
-    const int c0 = seg * kGColumns + 8 * threadIdx.x;
-    float f[2][8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = c0 + 8 * kGThreads * i;
-      if (here && c + 8 <= cols) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(z + c));
-        const float4 y = __ldcs(reinterpret_cast<const float4*>(z + c + 4));
-        f[i][0] = x.x, f[i][1] = x.y, f[i][2] = x.z, f[i][3] = x.w;
-        f[i][4] = y.x, f[i][5] = y.y, f[i][6] = y.z, f[i][7] = y.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          f[i][j] = here && c + j < cols ? z[c + j] : -INFINITY;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = c0 + 8 * kGThreads * i;
-      if (c >= all) break;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = fmaf(f[i][j], c2, shift), e = exp2_fast(t);
-        // (2^-200 is 0: an infinity's product with it would not be)
-        const float g = e * fmaf(B, fmaxf(t, -200.f), A);
-        f[i][j] = here && c + j < cols ? g : 0.f;
-      }
-      if (target >= c && target < c + 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (target == c + j) f[i][j] += a;
-      }
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = pack16<AB_TYPE>(f[i][2 * j], f[i][2 * j + 1]);
-      uint16_t* to = G + (long long)r * p.piece + c;
-      if (!span_ok(to, 16, p.G, (p.pieces > 1 ? 2 : 1) * extent, p.status))
-        continue;
-      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (!lo) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = pack16_rest<AB_TYPE>(f[i][2 * j], f[i][2 * j + 1], w[j]);
-      to += (long long)lo * p.piece;
-      if (span_ok(to, 16, p.G, (p.pieces > 1 ? 2 : 1) * extent, p.status))
-        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+  for (long long u = first; u < (long long)rows * runs;
+       u += (long long)gridDim.x * (kGThreads / 32)) {
+    const int r = (int)(u / runs), run = (int)(u - (long long)r * runs);
+    score_g_run<AB_TYPE>(
+        p, G, r, run * kVocabGRun, v0, cols, all, lo, r < learnt, lane,
+        [&](float4& of, int& goal) {
+          const long long t = learnt != p.T ? p.token[r] : r;
+          of = score_terms(p, t);
+          goal = (int)p.targets[t];
+          if (run == 0 && piece == 0 && lane == 0) {
+            p.terms[r] = of;
+            p.goals[r] = goal;
+          }
+        });
   }
 }
 
@@ -777,8 +728,9 @@ cudaError_t vocab_score_g(const VocabCall& c, int piece, int sms,
                           cudaStream_t stream) {
   const int64_t cols = std::min(c.piece, c.V - piece * c.piece);
   const int64_t rows = (c.T + 63) / 64 * 64;
-  const int64_t units = rows * ((cols + kGColumns - 1) / kGColumns);
-  const unsigned blocks = (unsigned)std::min<int64_t>(units, 8ll * sms);
+  const int64_t units = rows * ((cols + kVocabGRun - 1) / kVocabGRun);
+  const unsigned blocks = (unsigned)std::min<int64_t>(
+      (units + kGThreads / 32 - 1) / (kGThreads / 32), 8ll * sms);
   return c.type == GEMM_F32_MIXED_BF16
              ? launch_pdl(score_g_kernel<1>, dim3(blocks), dim3(kGThreads), 0,
                           stream, c, piece)

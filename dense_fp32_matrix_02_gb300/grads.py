@@ -16,6 +16,7 @@ nothing.  Autograd records none of this.
 from __future__ import annotations
 
 import array
+import itertools
 
 import torch
 
@@ -35,69 +36,81 @@ def workspace_size(tensors) -> int:
     return n
 
 
-def _rows(t, name):
-    """(rows, columns, leading dimension): one row of a contiguous tensor."""
-    if t.is_contiguous():
-        n = t.numel()
-        return 1, n, n
-    if t.dim() == 2:
-        rows, cols = t.shape
+def _row_step(t, shape, name):
+    """The leading dimension of a matrix whose rows are apart."""
+    if len(shape) == 2:
         step, one = t.stride()
-        if (one == 1 or cols == 1) and (step >= cols or rows == 1):
-            return rows, cols, step if rows > 1 else cols
+        if (one == 1 or shape[1] == 1) and step >= shape[1]:
+            return step
     raise ValueError(f"{name} must be contiguous, or a matrix whose rows "
                      "are, one behind the other")
 
 
+_ptr, _device = torch.Tensor.data_ptr, torch.Tensor.get_device
+_numel, _whole = torch.Tensor.numel, torch.Tensor.is_contiguous
+_ONES = itertools.repeat(1)
+
+
+def _checked(tensors, name):
+    """(device index, data types) of a list of CUDA tensors."""
+    if not all(issubclass(k, torch.Tensor) for k in set(map(type, tensors))):
+        raise TypeError(f"{name} must be torch tensors")
+    kinds = [t.dtype for t in tensors]
+    if not _TYPES.keys() >= set(kinds):
+        raise TypeError(f"{name} must be bfloat16, float16 or float32 torch "
+                        "tensors")
+    where = set(map(_device, tensors))
+    if min(where) < 0 or not tensors[0].is_cuda:  # (-1: the host's)
+        raise ValueError(f"{name} must live on a CUDA device")
+    if len(where) > 1:
+        raise ValueError(f"{name} must live on one device")
+    return where.pop(), kinds
+
+
 def _table(tensors, out):
-    """gemm_f32_grad of each tensor, and their device."""
+    """gemm_f32_grad of each tensor, and their device.  (A column of the table
+    at a time: a model has hundreds of gradients, and what is done for each is
+    the time of a call.)"""
     tensors = list(tensors)
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
-            raise TypeError("gradients must be bfloat16, float16 or float32 "
-                            "torch tensors")
-        if not t.is_cuda:
-            raise ValueError("gradients must live on a CUDA device")
     if not tensors:
         raise ValueError("no gradients: the device of their norm is unknown")
-    device = tensors[0].device
-    index = device.index
-    targets = tensors
+    index, kinds = _checked(tensors, "gradients")
+    n = len(tensors)
+    whole, whole_out = list(map(_whole, tensors)), _ONES
+    at, sizes = list(map(_ptr, tensors)), list(map(_numel, tensors))
+    targets, to = tensors, at
     if out is not None:
         targets = list(out)
-        if len(targets) != len(tensors):
+        if len(targets) != n:
             raise ValueError("out must have a tensor for each gradient")
-    table = array.array("q")
-    for t, o in zip(tensors, targets):
-        if t.get_device() != index:
-            raise ValueError("gradients must live on one device")
-        if o is t:
-            if t.is_contiguous():
-                p, n = t.data_ptr(), t.numel()
-                table.extend((p, p, 1, n, n, n, _TYPES[t.dtype]))
+        where, kinds_out = _checked(targets, "out")
+        if where != index:
+            raise ValueError("out must live on the gradients' device")
+        if kinds_out != kinds:
+            raise TypeError("out must have the gradients' types")
+        if list(map(_numel, targets)) != sizes:
+            raise ValueError("out must have the gradients' shapes")
+        to = list(map(_ptr, targets))
+        whole_out = list(map(_whole, targets))
+    table = array.array("q", itertools.chain.from_iterable(
+        zip(at, to, _ONES, sizes, sizes, sizes, map(_TYPES.get, kinds))))
+    if not (all(whole) and (whole_out is _ONES or all(whole_out))):
+        if whole_out is _ONES:
+            whole_out = whole
+        for i, (t, o) in enumerate(zip(tensors, targets)):
+            if whole[i] and whole_out[i]:
                 continue
-            rows, cols, ld = _rows(t, "a gradient")
-            p, q, ld_out = t.data_ptr(), t.data_ptr(), ld
-        else:
-            if not isinstance(o, torch.Tensor) or o.dtype != t.dtype:
-                raise TypeError("out must have the gradients' types")
-            if o.shape != t.shape:
+            shape = t.shape
+            if o is not t and o.shape != shape:
                 raise ValueError("out must have the gradients' shapes")
-            if o.get_device() != index:
-                raise ValueError("out must live on the gradients' device")
-            p, q = t.data_ptr(), o.data_ptr()
-            if t.is_contiguous() and o.is_contiguous():
-                n = t.numel()
-                table.extend((p, q, 1, n, n, n, _TYPES[t.dtype]))
-                continue
-            rows, cols, ld = _rows(t, "a gradient")
-            rows2, cols2, ld_out = _rows(o, "out")
-            if rows2 != rows:  # one of them is one row: cut it up
-                rows, cols = t.shape
-                ld = cols if rows2 != 1 else ld
-                ld_out = cols if rows2 == 1 else ld_out
-        table.extend((p, q, rows, cols, ld, ld_out, _TYPES[t.dtype]))
-    return table, len(tensors), device
+            ld = 0 if whole[i] else _row_step(t, shape, "gradients")
+            ld_out = ld if o is t else \
+                0 if whole_out[i] else _row_step(o, shape, "out")
+            rows, cols = shape
+            k = 7 * i
+            table[k + 2], table[k + 3] = rows, cols
+            table[k + 4], table[k + 5] = ld or cols, ld_out or cols
+    return table, n, tensors[0].device
 
 
 def _scratch(workspace, n, device, stream):
@@ -123,8 +136,10 @@ def global_norm(tensors, workspace=None, stream=None):
 
 def clip_(tensors, max_norm, out=None, workspace=None, stream=None):
     """Scales the tensors by min(1, max_norm / norm), in place or into
-    ``out`` (a tensor for each, in memory of its own); returns their norm
-    before it (float32, one element)."""
+    ``out``; returns their norm before it (float32, one element).  out: a
+    tensor for each, of its type and shape and in memory of its own (of a
+    contiguous gradient also another shape of as many elements, as a piece of
+    a flat buffer)."""
     table, n, device = _table(tensors, out)
     with _on(device):
         norm = _new(1, torch.float32, device, stream)

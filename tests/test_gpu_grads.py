@@ -122,6 +122,14 @@ def test_contiguous_beside_rows():
         check_clipped([src], [dst], 1.0, norm_of([src]))
     with pytest.raises(ValueError, match="contiguous"):
         C.global_norm([tensor(8, 8, BF16, 1).t()[:, 1:]])
+    flat = torch.zeros(100, dtype=BF16, device=DEV)  # pieces of one buffer
+    src = [tensor(3, 7, BF16, 2), tensor(5, 4, BF16, 3)]
+    C.clip_(src, 1.0, out=[flat[1:22], flat[22:42]])
+    check_clipped(src, [flat[1:22].view(3, 7), flat[22:42].view(5, 4)], 1.0,
+                  norm_of(src))
+    assert float(flat[0]) == 0.0 and bool((flat[42:] == 0).all())
+    with pytest.raises(ValueError, match="shapes"):  # rows of another width
+        C.clip_([tensor(6, 4, BF16, 1, pad=1)], 1.0, out=[flat[:24]])
     x = tensor(4, 6, F32, 3).view(2, 2, 6)  # any shape, contiguous
     check([x, tensor(1, 1, F32, 2).reshape(())], 1.0)
 
