@@ -155,7 +155,8 @@ struct VocabCall {
   float2* stats;  // [half tiles' columns][learnt]: (max, sum), powers of 2
   float* picked;  // [T][top]: logits / τ of the entries
   // log probabilities
-  float2* slants;  // beside stats: Σ e·log2 e of its terms e, the largest logit
+  float4* sums;    // in place of stats, [learnt][half tiles' columns]: (max,
+                   // sum, Σ e·log2 e of its terms e, the largest logit)
   float* logits;   // [chunk][ld_logits]: the logits of the learnt tokens, of
   long long ld_logits;  // all (kept for the gradients) or, for their largest,
   int chunk, keep;      // of `chunk` in turn; or null

@@ -78,7 +78,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // itself, with one sum in Grad 2048 to 4096 deep).  So the rule goes by what
 // both calls see: all tokens where the forward call may number none.
 __device__ __forceinline__ int sum_steps(const VocabCall& p, int learnt) {
-  return p.T <= 8 ? 4 : learnt <= kVocabTile || p.slants ? 8 : 16;
+  return p.T <= 8 ? 4 : learnt <= kVocabTile || p.sums ? 8 : 16;
 }
 
 // Steps that an accumulator sums for dW and dX, whose results are rounded to
@@ -967,19 +967,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           peak = now;
         }
         if (first_pass || n0 >= p.V) continue;
-        float2* to = p.stats + (long long)(u.tn * 2 + h) * learnt + r;
-        if (r < learnt &&
-            span_ok(to, 8, p.stats,
-                    8ll * ((2ll * p.V + u.wide - 1) / u.wide) * learnt,
-                    wc.status))
-          *to = make_float2(peak, sum);
+        const int parts = (int)((2ll * p.V + u.wide - 1) / u.wide);
         if constexpr (SCORE) {
-          float2* to2 = p.slants + (to - p.stats);
+          // (a row's are read together)
+          float4* to = p.sums + (long long)r * parts + u.tn * 2 + h;
           if (r < learnt &&
-              span_ok(to2, 8, p.slants,
-                      8ll * ((2ll * p.V + u.wide - 1) / u.wide) * learnt,
-                      wc.status))
-            *to2 = make_float2(slant, largest);
+              span_ok(to, 16, p.sums, 16ll * parts * learnt, wc.status))
+            *to = make_float4(peak, sum, slant, largest);
+        } else {
+          float2* to = p.stats + (long long)(u.tn * 2 + h) * learnt + r;
+          if (r < learnt &&
+              span_ok(to, 8, p.stats, 8ll * parts * learnt, wc.status))
+            *to = make_float2(peak, sum);
         }
       }
       if (SCORE && lane == 0) bulk_wait_group<0>();

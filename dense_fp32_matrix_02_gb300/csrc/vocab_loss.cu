@@ -630,8 +630,10 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   constexpr int64_t kMostSlots = 768ll << 20;
   constexpr int64_t kMostDwSlots = 128ll << 20;
   // Logits of which the largest are looked for: those of as many tokens (but
-  // 256 at least) are stored at a time.
-  constexpr int64_t kMostLogits = 1ll << 30;
+  // 256 at least) are stored at a time.  (Each time is a launch, with its ends,
+  // and reads W again: 8192 × 100000 × 2048, one word each: 2560 us with 1 GB
+  // at a time, 2533 with 4.)
+  constexpr int64_t kMostLogits = 4ll << 30;
   const int64_t rows = std::max<int64_t>(T, 1);
   int64_t at = 0;
   auto take = [&](auto** to, int64_t bytes) {
@@ -664,10 +666,10 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
     const int64_t narrow = std::min<int64_t>(
         (V + 31) / 32 * rows, 2 * kVocabMaxPairs * 8 * kVocabTile);
     const int64_t halves = std::max((V + 127) / 128 * rows, narrow);
-    take(&c->stats, halves * 8);
+    if (alternatives < 0) take(&c->stats, halves * 8);
     take(&c->picked, rows * top * 4);
     if (alternatives < 0) return at;
-    take(&c->slants, halves * 8);
+    take(&c->sums, halves * 16);
     c->chunk = (int)rows;
     c->ld_logits = up(V, 8);
     if (alternatives > 0 && !keep) {

@@ -55,28 +55,7 @@ __device__ __forceinline__ float moved(float m, float ref) {
   return fmaxf(m - ref, -1e30f);
 }
 
-__device__ __forceinline__ Stat merge(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
-  const float ref = m == -INFINITY ? 0.f : m;
-  const float da = moved(a.m, ref), db = moved(b.m, ref);
-  const float ka = exp2f(da), kb = exp2f(db);
-  return Stat{m, a.s * ka + b.s * kb,
-              ka * (a.e + da * a.s) + kb * (b.e + db * b.s)};
-}
-
-__device__ __forceinline__ Stat merge_over(Stat st, int from) {
-#pragma unroll 1
-  for (int o = from; o < 32; o <<= 1) {
-    Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    b.e = __shfl_xor_sync(0xffffffffu, st.e, o);
-    st = merge(st, b);
-  }
-  return st;
-}
-
-// The same over all lanes, in one step: the references first.
+// The statistics of all lanes joined.
 __device__ __forceinline__ float reference_of(uint32_t order) {
   const uint32_t u = order & 0x80000000u ? order ^ 0x80000000u : ~order;
   return __uint_as_float(u);
@@ -100,22 +79,22 @@ __device__ __forceinline__ Stat merge_warp(Stat st) {
 // logit goes to `largest`.
 template <typename Largest>
 __device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
-                                         int parts, int step, int learnt,
+                                         int parts, int step,
                                          Largest largest) {
+  const float4* sums = p.sums + (long long)r * parts;
   Stat st = {-INFINITY, 0.f, 0.f};
   float lost = 0.f, lost_e = 0.f;
 #pragma unroll 4
   for (int g = first; g < parts; g += step) {
-    const long long i = (long long)g * learnt + r;
-    const float2 b = p.stats[i], more2 = p.slants[i];
-    largest(g, more2.y);
+    const float4 b = sums[g];
+    largest(g, b.w);
     const float m = fmaxf(st.m, b.x);
     const float ref = m == -INFINITY ? 0.f : m;
     const float da = moved(st.m, ref), db = moved(b.x, ref);
     const float ka = exp2f(da), kb = exp2f(db);
     const float was = st.s * ka, was_e = ka * (st.e + da * st.s);
     const float more = b.y * kb - lost * ka;
-    const float more_e = kb * (more2.x + db * b.y) - lost_e * ka;
+    const float more_e = kb * (b.z + db * b.y) - lost_e * ka;
     st = Stat{m, was + more, was_e + more_e};
     lost = (st.s - was) - more;
     lost_e = (st.e - was_e) - more_e;
@@ -135,43 +114,30 @@ __device__ __forceinline__ float store_results(const VocabCall& p, long long t,
   return l;
 }
 
-// logp, lse and entropy of the rows from row0 on: 8 rows a block, blockDim / 8
-// threads a row that share out its statistics and join them in a fixed order.
-__global__ void __launch_bounds__(1024)
+// logp, lse and entropy of the rows from row0 on, a block each.
+constexpr int kFinishThreads = 256;
+__global__ void __launch_bounds__(kFinishThreads)
     finish_score_kernel(const __grid_constant__ VocabCall p, int row0) {
-  __shared__ Stat s_part[32][8];
+  __shared__ Stat s_part[kFinishThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int learnt = p.header ? p.header->learnt : p.T;
   const int wide = p.header ? p.header->wide : p.wide;
   const int parts = (int)((2ll * p.V + wide - 1) / wide);  // half tiles
-  const int in = blockIdx.x * 8 + (threadIdx.x & 7), r = row0 + in;
-  const int slice = threadIdx.x >> 3, warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const bool here = in < p.chunk && r < learnt;
-  long long t = r;
-  bool scored = here;
-  float at = 0.f;
-  if (warp == 0 && here) {  // ahead of the statistics' loads
-    if (learnt != p.T) t = p.token[r];
-    if (!p.header) scored = vocab_is_learnt(p, t);
-    if (scored) at = p.picked[r];
-  }
-  Stat st = share_of(p, r, here ? slice : parts, parts, blockDim.x >> 3, learnt,
-                     [](int, float) {});
-  st = merge_over(st, 8);
-  const int warps = blockDim.x >> 5;
-  if (warps > 1) {
-    if (lane < 8) s_part[warp][lane] = st;
-    __syncthreads();
-    if (warp > 0) return;
-    st = Stat{-INFINITY, 0.f, 0.f};
-    for (int w = lane >> 3; w < warps; w += 4)
-      st = merge(st, s_part[w][lane & 7]);
-    st = merge_over(st, 8);
-  }
-  if (!here || lane >= 8) return;
-  store_results(p, t, scored, st, at);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = row0 + blockIdx.x;
+  if (r >= learnt) return;
+  const long long t = learnt != p.T ? p.token[r] : r;
+  const bool scored = p.header || vocab_is_learnt(p, t);
+  const float at = scored ? p.picked[r] : 0.f;
+  Stat st = merge_warp(share_of(p, r, threadIdx.x, parts, kFinishThreads,
+                                [](int, float) {}));
+  if (lane == 0) s_part[warp] = st;
+  __syncthreads();
+  if (warp > 0) return;
+  st = lane < kFinishThreads / 32 ? s_part[lane] : Stat{-INFINITY, 0.f, 0.f};
+  st = merge_warp(st);
+  if (lane == 0) store_results(p, t, scored, st, at);
 }
 
 // ------------------------------------------------------- likeliest words
@@ -381,6 +347,11 @@ struct ExactSum {
     }
   }
 };
+__device__ __forceinline__ float2 across(float2 v, int o) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                     __shfl_xor_sync(0xffffffffu, v.y, o));
+}
+
 // WORDS rows of W at a time, AHEAD loads of each side by side (a row of W comes from far).
 template <int AB_TYPE, int WORDS, int AHEAD>
 __device__ __forceinline__ void exact_dots(const uint16_t* x,
@@ -428,13 +399,67 @@ __device__ __forceinline__ void exact_dots(const uint16_t* x,
         add_exactly(two_sum(h0.x, l0.x), two_sum(h0.y, l0.y)),
         add_exactly(two_sum(h1.x, l1.x), two_sum(h1.y, l1.y)));
   }
-#pragma unroll 1
-  for (int o = 16; o; o >>= 1)
+  // Halves of the lanes sum halves of the words, down to one: v[0] is that of
+  // word lane / (32 / WORDS).
+  int o = 16;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      v[i] = add_exactly(v[i],
-                         make_float2(__shfl_xor_sync(0xffffffffu, v[i].x, o),
-                                     __shfl_xor_sync(0xffffffffu, v[i].y, o)));
+  for (int n = WORDS / 2; n; n >>= 1, o >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool upper = lane & o;
+      const float2 mine = upper ? v[n + i] : v[i];
+      v[i] = add_exactly(mine, across(upper ? v[i] : v[n + i], o));
+    }
+#pragma unroll 1
+  for (; o; o >>= 1) v[0] = add_exactly(v[0], across(v[0], o));
+}
+
+// The logits of words c0 to c0 + WORDS - 1 of k in `ids`, before any rounding.
+template <int AB_TYPE, int WORDS, int AHEAD>
+__device__ __forceinline__ void exact_logits(const VocabCall& p, long long t,
+                                             const float* z, const int* ids,
+                                             int c0, int k, int lane,
+                                             float2* value) {
+  const uint16_t* w[WORDS];
+  float2 v[WORDS];
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i)  // (past the end, the last again)
+    w[i] = static_cast<const uint16_t*>(p.W) + ids[min(c0 + i, k - 1)] * p.ldw;
+  exact_dots<AB_TYPE, WORDS, AHEAD>(
+      static_cast<const uint16_t*>(p.X) + t * p.ldx, w, p.D, lane, v);
+  const int c = c0 + lane / (32 / WORDS);
+  if (lane % (32 / WORDS) == 0 && c < k) {
+    // (an infinity has no remainder; a NaN is ranked last)
+    if (!(fabsf(v[0].x) < INFINITY)) v[0] = make_float2(z[ids[c]], 0.f);
+    if (v[0].x != v[0].x) v[0].x = -INFINITY;
+    value[c] = v[0];
+  }
+}
+
+// The first of k words, by value and id.
+template <int THREADS>
+__device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
+                                             const int* ids,
+                                             const float2* value, int k,
+                                             int thread, float lse) {
+  for (int c = thread; c < k; c += THREADS) {
+    const float2 v = value[c];
+    const int id = ids[c];
+    int rank = 0;
+#pragma unroll 4
+    for (int o = 0; o < k; ++o) {
+      const float2 w = value[o];
+      rank += w.x > v.x ||
+              (w.x == v.x && (w.y > v.y || (w.y == v.y && ids[o] < id)));
+    }
+    if (rank < p.alternatives) {
+      p.top_out[t * p.alternatives + rank] = id;
+      // v / τ − lse, the quotient with its remainder
+      const float q = v.x / p.tau, rest = fmaf(-q, p.tau, v.x) + v.y;
+      p.top_logp[t * p.alternatives + rank] =
+          fabsf(q) < INFINITY ? (q - lse) + rest / p.tau : q - lse;
+    }
+  }
 }
 
 // A row a block: its results, and its likeliest words.
@@ -474,7 +499,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   // the statistics, and the stretches' maxima
   const bool held = parts <= kHeldKeys;
   uint32_t low = 0xffffffffu, high = 0;
-  Stat st = share_of(p, r, tid, parts, THREADS, learnt, [&](int g, float z) {
+  Stat st = share_of(p, r, tid, parts, THREADS, [&](int g, float z) {
     const uint32_t x = order_of(z);
     if (held) s_key[g] = x;
     low = min(low, x);
@@ -501,7 +526,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   if (tid == 0) store_results(p, t, true, st, p.picked[r]);
 
   auto maximum = [&](int g) {
-    return held ? s_key[g] : order_of(p.slants[(long long)g * learnt + r].y);
+    return held ? s_key[g] : order_of(p.sums[(long long)r * parts + g].w);
   };
   auto logit = [&](int v) -> uint32_t {  // past the vocabulary below all others
     const float* at = z + min(v, p.V - 1);
@@ -548,7 +573,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
           v[j] = (s_stretch[min(at, stretches - 1)] << bits) + in;
           const float* from = z + min(v[j], (p.V - 1) & ~3);
           f[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (span_ok(from, 16, p.logits, 4ll * p.chunk * p.ld_logits, p.status))
+          if (i + j * kWarps < runs &&
+              span_ok(from, 16, p.logits, 4ll * p.chunk * p.ld_logits,
+                      p.status))
             f[j] = *reinterpret_cast<const float4*>(from);
           if (at >= stretches) v[j] = p.V;
         }
@@ -591,7 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     // the k first.
     int stretches = parts, equal;
     auto largest = [&](int g) {  // (what is held of them is gone)
-      return order_of(p.slants[(long long)g * learnt + r].y);
+      return order_of(p.sums[(long long)r * parts + g].w);
     };
     __syncthreads();
     if (parts > k) {
@@ -620,42 +647,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   // (many rows: two words a warp, which share x; few: one, with more of it
   // side by side)
   constexpr int kWords = THREADS == 1024 ? 1 : 2;
-  for (int c0 = warp * kWords; c0 < k; c0 += kWarps * kWords) {
-    const uint16_t* w[kWords];
-    float2 v[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-      w[i] = static_cast<const uint16_t*>(p.W) + s_id[min(c0 + i, k - 1)] * p.ldw;
-    exact_dots<AB_TYPE, kWords, kWords == 1 ? 4 : 2>(x, w, p.D, lane, v);
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-      if (lane == i && c0 + i < k) {
-        // (an infinity has no remainder; a NaN is ranked last)
-        if (!(fabsf(v[i].x) < INFINITY))
-          v[i] = make_float2(z[s_id[c0 + i]], 0.f);
-        if (v[i].x != v[i].x) v[i].x = -INFINITY;
-        s_value[c0 + i] = v[i];
-      }
-  }
+  for (int c0 = warp * kWords; c0 < k; c0 += kWarps * kWords)
+    exact_logits<AB_TYPE, kWords, kWords == 1 ? 4 : 2>(p, t, z, s_id, c0, k,
+                                                       lane, s_value);
   __syncthreads();
-  for (int c = tid; c < k; c += THREADS) {
-    const float2 v = s_value[c];
-    const int id = s_id[c];
-    int rank = 0;
-#pragma unroll 4
-    for (int o = 0; o < k; ++o) {
-      const float2 w = s_value[o];
-      const bool equal = w.x == v.x;
-      rank += w.x > v.x || (equal && (w.y > v.y || (w.y == v.y && s_id[o] < id)));
-    }
-    if (rank < p.alternatives) {
-      p.top_out[t * p.alternatives + rank] = id;
-      // v / τ − lse, the quotient with its remainder
-      const float q = v.x / p.tau, rest = fmaf(-q, p.tau, v.x) + v.y;
-      p.top_logp[t * p.alternatives + rank] =
-          fabsf(q) < INFINITY ? (q - lse) + rest / p.tau : q - lse;
-    }
-  }
+  write_ranked<THREADS>(p, t, s_id, s_value, k, tid, lse);
 }
 
 // ------------------------------------------------------------- gradients
@@ -704,24 +700,22 @@ __global__ void __launch_bounds__(kGThreads)
 cudaError_t vocab_score_results(const VocabCall& c, int phase, int sms,
                                 cudaStream_t stream) {
   const int row0 = phase * c.chunk, rows = std::min(c.chunk, c.T - row0);
-  if (c.alternatives == 0) {
-    // a thread's share of a row: a few statistics
-    const int parts = (c.V + 127) / 128;
-    const int threads = parts <= 16 ? 32 : parts <= 128 ? 256 : 1024;
-    return launch_pdl(finish_score_kernel, dim3((rows + 7) / 8), dim3(threads),
-                      0, stream, c, row0);
-  }
-  // A block's warps each sum one word's exact logit at a time.  Where there is
-  // about a row to an SM, nothing else hides the wait for their rows of W.
-  const bool wide = rows <= 2 * sms;
   auto launch = [&](auto* fn, int threads) {
     return launch_pdl(fn, dim3(rows), dim3(threads), 0, stream, c, row0);
   };
-  if (c.type == GEMM_F32_MIXED_BF16)
-    return wide ? launch(top_kernel<1, 1024>, 1024)
-                : launch(top_kernel<1, 256>, 256);
-  return wide ? launch(top_kernel<0, 1024>, 1024)
-              : launch(top_kernel<0, 256>, 256);
+  if (c.alternatives == 0) return launch(finish_score_kernel, kFinishThreads);
+  // A block's warps each sum words' exact logits.  Where there is about a row
+  // to an SM, nothing else hides the wait for their rows of W: 32 warps, one
+  // word each (304 tokens, 100000 × 2048, 64 words: 210 us; 512 tokens 268 us,
+  // 230 with 8 warps).  With several rows to an SM 8 warps (400 tokens 223 us,
+  // 267 with 4), with many 4, of which more blocks overlap (4096 tokens, 32000
+  // × 768, 5 words: 268 us with 8, 246 with 4).
+  auto pick = [&](auto bf16, auto f16, int threads) {
+    return launch(c.type == GEMM_F32_MIXED_BF16 ? bf16 : f16, threads);
+  };
+  if (rows <= 2 * sms) return pick(top_kernel<1, 1024>, top_kernel<0, 1024>, 1024);
+  if (rows <= 5 * sms) return pick(top_kernel<1, 256>, top_kernel<0, 256>, 256);
+  return pick(top_kernel<1, 128>, top_kernel<0, 128>, 128);
 }
 
 cudaError_t vocab_score_g(const VocabCall& c, int piece, int sms,

@@ -550,7 +550,7 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  *
  * Workspace, limits, empty calls and errors are those of the losses, with
  * gemm_f32_vocab_score_workspace_size bytes; for top > 0 without `kept` it
- * holds the logits of as many tokens at a time as 1 GB takes (256 at least).
+ * holds the logits of as many tokens at a time as 4 GB take (256 at least).
  * GEMM_F32_ERR_INVALID_ARG also for top outside [0, min(256, V)], a kept that
  * is misaligned, too small or (gradients) NULL, and a negative stride.
  */

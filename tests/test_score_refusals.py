@@ -92,12 +92,12 @@ def test_sizes(built_lib):  # noqa: F811
                 (4, 8, 8, 0, 2, 0, 1), (4, 8, 8, 0, 0, 2, 1),
                 (4, 8, 8, 0, 0, 0, 2)):
         assert size(*bad) == -BAD, bad
-    # the logits in the workspace: 1 GB at most, or 256 tokens' of them
-    few = size(8192, 128000, 64, 0, 0, 0, 1)
-    assert size(8192, 128000, 64, 5, 1, 0, 1) == few
-    assert few < size(8192, 128000, 64, 5, 0, 0, 1) <= few + 2**30
-    wide = size(8192, 2**21, 64, 5, 0, 0, 1) - size(8192, 2**21, 64, 0, 0, 0, 1)
-    assert wide == 256 * 2**21 * 4
+    # the logits in the workspace: 4 GB at most, or 256 tokens' of them
+    few = size(16384, 128000, 64, 0, 0, 0, 1)
+    assert size(16384, 128000, 64, 5, 1, 0, 1) == few
+    assert few < size(16384, 128000, 64, 5, 0, 0, 1) <= few + 2**32
+    wide = size(8192, 2**23, 64, 5, 0, 0, 1) - size(8192, 2**23, 64, 0, 0, 0, 1)
+    assert wide == 256 * 2**23 * 4
     for T, V in ((1, 1), (300, 900), (0, 100), (8192, 1000)):
         for al in (0, 1):
             assert size(T, V, 72, 1, 1, 1, al) >= size(T, V, 72, 1, 1, 0, al)
