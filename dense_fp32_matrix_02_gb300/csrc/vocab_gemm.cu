@@ -183,23 +183,6 @@ __device__ __forceinline__ void tma_add_2d(const void* tmap, uint32_t src,
       : "memory");
 }
 
-// Stores a block that is not read for long: its lines are the first to leave
-// L2.
-__device__ __forceinline__ uint64_t leave_first() {
-  uint64_t policy;
-  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(policy));
-  return policy;
-}
-__device__ __forceinline__ void tma_store_2d_hint(const void* tmap, uint32_t src,
-                                                  int c0, int c1,
-                                                  uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group"
-      ".L2::cache_hint [%0, {%2, %3}], [%1], %4;\n" ::"l"(tmap),
-      "r"(src), "r"(c0), "r"(c1), "l"(policy)
-      : "memory");
-}
-
 // f[i] = f[i]·m + a for 32 values, two to an instruction.
 __device__ __forceinline__ void scale_add_32(float* f, float m, float a) {
   uint64_t mm, aa;
@@ -927,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage_32(f);
             if (lane == 0) {
               if (!first_pass && m0 < all_rows)
-                tma_store_2d_hint(&maps.logits, stg_s, n, m0, leave_first());
+                tma_store_2d(&maps.logits, stg_s, n, m0);
               bulk_commit_group();
             }
           }
@@ -947,16 +930,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           scale_add_32(f, c2, -ref);
           if constexpr (SCORE) {
             // Σ e·log2 e, e = 2^(z·c2 - ref): from the last reference to this
-            // one a term's logarithm moves by d.  A logit of -Inf has e = 0,
-            // and no logarithm below -1e30, so that their product is 0.
+            // one a term's logarithm moves by d.
             const float d = fmaxf(peak - ref, -1e30f), keep = exp2_fast(d);
             float e[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              e[j] = exp2_fast(f[j]);
-              f[j] = fmaxf(f[j], -1e30f);
+            for (int j = 0; j < 32; ++j) e[j] = exp2_fast(f[j]);
+            float more = dot_32(e, f);
+            if (more != more) {
+              // A logit of -Inf has e = 0, and here no logarithm below -1e30:
+              // their product is 0.  (A NaN stays in e.  The limit on every
+              // logit took 2 % more time: 8192 × 32000 × 768 292 us.)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = fmaxf(f[j], -1e30f);
+              more = dot_32(e, f);
             }
-            slant = keep * (slant + d * sum) + dot_32(e, f);
+            slant = keep * (slant + d * sum) + more;
             sum = sum * keep + sum_32(e);
             largest = fmaxf(largest, here);
           } else {

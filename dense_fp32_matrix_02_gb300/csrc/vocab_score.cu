@@ -11,9 +11,9 @@
 // (half tiles) with the largest maxima, of equal ones the first: any element
 // elsewhere has k larger ones before it, or equal ones with lower ids.  So the
 // logits are stored, of some tokens at a time, and of each row only those
-// stretches are read, about k·128 of V logits.  Storing costs the products nothing
-// where they are bound by the tensor cores, and 2·T/D of the weights' bytes
-// where they are bound by those.
+// stretches are read, about k·128 of V logits.  (Storing them costs the products
+// 5 % at width 4096 and 28 % at width 768, 4096 and 8192 tokens; for few tokens
+// 2·T/D of the weights' bytes.)
 //   The rank of two logits should not hang on how a sum rounds (on the tile it
 // was made in, so on the batch): the k + kSpare largest are computed again
 // from the operands, products exact in fp32, summed in pairs of fp32 (48
@@ -102,16 +102,19 @@ __device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
   return st;
 }
 
+__device__ __forceinline__ float lse_of(Stat st) {
+  return st.m * kLn2 + logf(st.s);
+}
+
 // A row's results; at: its word's logit / τ.
-__device__ __forceinline__ float store_results(const VocabCall& p, long long t,
-                                               bool scored, Stat st, float at) {
-  const float log_sum = logf(st.s), l = st.m * kLn2 + log_sum;
+__device__ __forceinline__ void store_results(const VocabCall& p, long long t,
+                                              bool scored, Stat st, float lse,
+                                              float at) {
   // (the difference of equal numbers where one word has all: not below 0)
-  const float entropy = log_sum - kLn2 * (st.e / st.s);
-  p.loss[t] = scored ? at - l : 0.f;
-  p.lse_out[t] = scored ? l : 0.f;
+  const float entropy = logf(st.s) - kLn2 * (st.e / st.s);
+  p.loss[t] = scored ? at - lse : 0.f;
+  p.lse_out[t] = scored ? lse : 0.f;
   p.entropy_out[t] = scored && !(entropy < 0.f) ? entropy : 0.f;
-  return l;
 }
 
 // logp, lse and entropy of the rows from row0 on, a block each.
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (warp > 0) return;
   st = lane < kFinishThreads / 32 ? s_part[lane] : Stat{-INFINITY, 0.f, 0.f};
   st = merge_warp(st);
-  if (lane == 0) store_results(p, t, scored, st, at);
+  if (lane == 0) store_results(p, t, scored, st, lse_of(st), at);
 }
 
 // ------------------------------------------------------- likeliest words
@@ -436,15 +439,19 @@ __device__ __forceinline__ void exact_logits(const VocabCall& p, long long t,
   }
 }
 
-// The first of k words, by value and id.
+// The first of k words, by value and id.  Their log probabilities are those of
+// the fp32 logits, as the given word's is: lse is made of them, and what the
+// tensor cores drop, towards 0, shrinks both (exact logits beside it were up to
+// 1.8 times as far off as fp32 sums that round to nearest).
 template <int THREADS>
 __device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
-                                             const int* ids,
+                                             const float* z, const int* ids,
                                              const float2* value, int k,
                                              int thread, float lse) {
   for (int c = thread; c < k; c += THREADS) {
     const float2 v = value[c];
     const int id = ids[c];
+    const float at = __fmul_rn(z[id], p.inv_tau);  // (as it is picked)
     int rank = 0;
 #pragma unroll 4
     for (int o = 0; o < k; ++o) {
@@ -454,10 +461,7 @@ __device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
     }
     if (rank < p.alternatives) {
       p.top_out[t * p.alternatives + rank] = id;
-      // v / τ − lse, the quotient with its remainder
-      const float q = v.x / p.tau, rest = fmaf(-q, p.tau, v.x) + v.y;
-      p.top_logp[t * p.alternatives + rank] =
-          fabsf(q) < INFINITY ? (q - lse) + rest / p.tau : q - lse;
+      p.top_logp[t * p.alternatives + rank] = at - lse;
     }
   }
 }
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const long long t = learnt != p.T ? p.token[r] : r;
   if (!p.header && !vocab_is_learnt(p, t)) {
     if (tid == 0) {
-      store_results(p, t, false, Stat{0.f, 1.f, 0.f}, 0.f);
+      store_results(p, t, false, Stat{0.f, 1.f, 0.f}, 0.f, 0.f);
       vocab_unscored(p, t);
     }
     return;
@@ -522,8 +526,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   st = merge_warp(st);
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
-  const float lse = __shfl_sync(0xffffffffu, st.m * kLn2 + logf(st.s), 0);
-  if (tid == 0) store_results(p, t, true, st, p.picked[r]);
+  const float lse = __shfl_sync(0xffffffffu, lse_of(st), 0);
+  if (tid == 0) store_results(p, t, true, st, lse, p.picked[r]);
 
   auto maximum = [&](int g) {
     return held ? s_key[g] : order_of(p.sums[(long long)r * parts + g].w);
@@ -643,7 +647,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   __syncthreads();
 
   // ranked by their values before any rounding
-  const uint16_t* x = static_cast<const uint16_t*>(p.X) + t * p.ldx;
   // (many rows: two words a warp, which share x; few: one, with more of it
   // side by side)
   constexpr int kWords = THREADS == 1024 ? 1 : 2;
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     exact_logits<AB_TYPE, kWords, kWords == 1 ? 4 : 2>(p, t, z, s_id, c0, k,
                                                        lane, s_value);
   __syncthreads();
-  write_ranked<THREADS>(p, t, s_id, s_value, k, tid, lse);
+  write_ranked<THREADS>(p, t, z, s_id, s_value, k, tid, lse);
 }
 
 // ------------------------------------------------------------- gradients

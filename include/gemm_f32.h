@@ -528,8 +528,10 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  * ones by the lower id: top_ids[t·top + j] and their log probabilities
  * top_logp[t·top + j].  They are ranked by Σ_k X·W as the operands give it (to
  * 2^-46 of the sum's terms) among the top + 8 largest of the fp32 logits, so
- * that neither rank nor log probability hangs on the order of a sum; a logit
- * that is NaN ranks last.  0 <= top <= min(256, V); top_logp and top_ids may
+ * that the rank does not hang on how a sum rounds; the log probabilities are
+ * those of the fp32 logits, the given word's to the bit (two that differ by
+ * less than these round may stand the other way round).  A logit that is NaN
+ * ranks last.  0 <= top <= min(256, V); top_logp and top_ids may
  * be NULL for top = 0.  A token whose id is outside [0, V) is not scored: its
  * logp, lse, entropy and top_logp are 0, its top_ids -1, whatever its row of X
  * holds.

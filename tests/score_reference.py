@@ -9,8 +9,7 @@ the sums of a few hundred terms add to a logarithm.
   * entropy: its derivative with respect to log p_v is −p_v·(log p_v + H), whose
     sizes add up to at most 2·H; so 2·H·(d + e), plus what the two terms whose
     difference it is (log S and E/S, each at most log V) round: 2e-6·log V + e;
-  * top_logp: the logit is exact before it is rounded, so lse's error and
-    1e-6·(|z/τ| + |lse|);
+  * top_logp: as logp, a logit and lse: d + lse's + 1e-6·|z/τ| + e;
   * G: one rounding, u·|G|; p's own error, a factor 1 ± (d + lse's + e); the
     error of log p + H in the second term; and binary16's smallest step under
     the scale that brings the largest (|a| + |b|·(0.4 + H))/τ to 2^14;
@@ -57,7 +56,7 @@ def scores(x, w, ids, tau=1.0, top=0):
         out["top_logp"] = torch.where(scored[:, None], best - lse[:, None], 0.0)
         out["top_logp_tol"] = torch.where(
             scored[:, None],
-            lse_tol[:, None] + 1e-6 * (best.abs() + lse.abs()[:, None]), 0.0)
+            (d + lse_tol + e)[:, None] + 1e-6 * best.abs(), 0.0)
     return out
 
 

@@ -70,6 +70,10 @@ def check_scores(x, w, ids, tau=1.0, top=0, **kw):
     if top:
         check(s._asdict(), want, ("top_logp",))
         assert torch.equal(s.top_ids, want["top_ids"])
+        # the given word among them has its own log probability, to the bit
+        own = s.top_ids == ids[:, None]
+        logp = s.logp[:, None].expand_as(s.top_logp)
+        assert torch.equal(s.top_logp[own], logp[own])
     else:
         assert s.top_ids is None and s.top_logp is None
     return s
