@@ -21,6 +21,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <functional>
+#include <memory>
+#include <new>
 #include <type_traits>
 
 #include "gemm_f32.h"
@@ -402,6 +405,19 @@ int check(const gemm_f32_grad& g, bool clip) {
   return GEMM_F32_OK;
 }
 
+// Whether two gradients go to the same place (one that is listed twice, as of
+// a shared weight, would be scaled twice or once).
+bool twice(int64_t n, const gemm_f32_grad* all) {
+  if (n < 2) return false;
+  std::unique_ptr<const void*[]> to(new (std::nothrow) const void*[n]);
+  if (!to) return false;  // (no memory for the check)
+  int64_t m = 0;
+  for (int64_t i = 0; i < n; ++i)
+    if (all[i].rows && all[i].cols) to[m++] = all[i].out;
+  std::sort(to.get(), to.get() + m, std::less<const void*>());
+  return std::adjacent_find(to.get(), to.get() + m) != to.get() + m;
+}
+
 Entry entry(const gemm_f32_grad& g, bool clip) {
   Entry e;
   e.in = static_cast<const char*>(g.data);
@@ -469,6 +485,7 @@ int run(int64_t n, const gemm_f32_grad* all, bool clip, float max_norm,
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15u) != 0 ||
       ws_bytes < gemm_f32_grad_workspace_size(n))
     return GEMM_F32_ERR_INVALID_ARG;
+  if (clip && twice(n, all)) return GEMM_F32_ERR_INVALID_ARG;
   int sms = 0, cc = 0;
   WaitCfg wc;
   cudaError_t e = device_facts(&sms, &cc, &wc);

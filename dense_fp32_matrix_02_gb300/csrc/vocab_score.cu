@@ -86,7 +86,8 @@ __device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
   float lost = 0.f, lost_e = 0.f;
 #pragma unroll 4
   for (int g = first; g < parts; g += step) {
-    const float4 b = sums[g];
+    float4 b = make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
+    if (span_ok(sums + g, 16, p.sums, 16ll * p.T * parts, p.status)) b = sums[g];
     largest(g, b.w);
     const float m = fmaxf(st.m, b.x);
     const float ref = m == -INFINITY ? 0.f : m;

@@ -2,10 +2,10 @@
 
 The hidden states of a batch of tokens are given (random here, leaning
 towards their own next token as a trained model's do); a teacher's output
-matrix exists.  Each step takes the cross entropy against the next tokens
-and the distillation from the teacher's best logits, adds their gradients and
-moves the matrix.  The logits of the student are never stored; the teacher's
-come once from the library's 16-bit product.
+matrix exists, of which each token's likeliest words are taken once.  Each step
+takes the cross entropy against the next tokens and the distillation from the
+teacher's words, clips both gradients by their common norm, adds them and moves
+the matrix.  The logits of the student are never stored.
 
     python examples/train_head.py [--steps 20] [--tokens 2048] [--vocab 8000]
 """
@@ -20,11 +20,11 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import torch  # noqa: E402
 
-from dense_fp32_matrix_02_gb300 import gemm, loss  # noqa: E402
+from dense_fp32_matrix_02_gb300 import gemm, grads, loss  # noqa: E402
 
 
 def train(steps=20, tokens=2048, vocab=8000, width=512, top=16,
-          temperature=2.0, rate=5.0, seed=0, device="cuda:0"):
+          temperature=2.0, rate=5.0, max_norm=10.0, seed=0, device="cuda:0"):
     """The (cross entropy, distillation) means before each step and after
     the last."""
     gen = torch.Generator(device=device).manual_seed(seed)
@@ -38,11 +38,10 @@ def train(steps=20, tokens=2048, vocab=8000, width=512, top=16,
     targets[: tokens // 8] = -100  # a prompt: not learnt from
     learnt = tokens - tokens // 8
 
-    # the teacher's best logits, once
-    logits = gemm.gemm_f32_mixed(x.float(), teacher.t().contiguous())
-    top_logits, top_ids = logits.topk(top)
-    del logits
-    top_ids[targets < 0] = -1
+    # the teacher's likeliest words, once (none of a token that is not learnt
+    # from; log probabilities are logits less a constant, which drops out)
+    best = loss.log_probs(x, gemm.round16(teacher), targets, top=top)
+    top_logits, top_ids = best.top_logp, best.top_ids
 
     master = torch.zeros(vocab, width, device=device)  # the student, in fp32
     mean = torch.tensor(1.0 / learnt, device=device).expand(tokens)
@@ -57,6 +56,7 @@ def train(steps=20, tokens=2048, vocab=8000, width=512, top=16,
         _, dw = loss.cross_entropy_grad(x, w, targets, ce_lse, mean)
         _, dw2 = loss.distill_grad(x, w, top_logits, top_ids, kd_lse, mean,
                                    temperature)
+        grads.clip_([dw, dw2], max_norm)
         master -= rate * (dw.float() + dw2.float())
 
 

@@ -595,7 +595,8 @@ typedef enum {
  * where it goes when it is clipped (rows ld_out apart; `data` itself with
  * ld_out = ld, or memory that no gradient of the call lies in).  Any element
  * boundary.  A gradient of one row has no need of ld and ld_out, one without
- * rows or columns of nothing.  The norm alone reads no out and ld_out. */
+ * rows or columns of nothing.  The norm alone reads no out and ld_out, and
+ * counts a gradient as often as it is listed. */
 typedef struct {
     const void *data;
     void *out;
@@ -621,9 +622,10 @@ typedef struct {
  * use until the stream passes the call.  n = 0: norm = 0.
  * GEMM_F32_ERR_INVALID_ARG also for an unknown type, negative sizes, leading
  * dimensions below the row width, a NULL or misaligned pointer and a max_norm
- * that is negative or NaN; GEMM_F32_ERR_UNSUPPORTED for more than 2^48 elements of a gradient or
- * its rows' span, or 2^31 rows, or columns of several rows that are not one behind the other,
- * or more gradients.
+ * that is negative or NaN, and for two gradients with the same out (other
+ * overlaps are not checked); GEMM_F32_ERR_UNSUPPORTED for more than 2^48
+ * elements of a gradient or between its first and last, for more than 2^31 - 1
+ * rows, or columns of several rows, and for more than 2^31 - 1 gradients.
  */
 GEMM_F32_API int gemm_f32_grad_norm(int64_t n, const gemm_f32_grad *grads,
                                     float *norm, void *workspace,

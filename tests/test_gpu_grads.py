@@ -264,3 +264,40 @@ def test_refusals():
     ws = torch.empty(64, dtype=torch.uint8, device=DEV)
     with pytest.raises(G.GemmError):
         C.clip_([a], 1.0, workspace=ws)
+    # a gradient that is listed twice: in the norm twice, never clipped
+    twice = math.sqrt(2) * norm_of([a])
+    assert abs(float(C.global_norm([a, a])) - twice) <= NORM_TOL * twice
+    keep = a.clone()
+    with pytest.raises(G.GemmError):
+        C.clip_([a, a], 1.0)
+    with pytest.raises(G.GemmError):
+        C.clip_([a, a.clone()], 1.0, out=[keep, keep])
+    assert torch.equal(a, keep)
+
+
+def test_columns_of_one_matrix():
+    """Gradients side by side in one matrix, each with its own columns."""
+    m = tensor(50, 96, BF16, 1)
+    parts = [m[:, :32], m[:, 32:41], m[:, 41:]]
+    before = [t.clone() for t in parts]
+    want = norm_of(parts)
+    assert abs(float(C.clip_(parts, want / 3)) - want) <= NORM_TOL * want
+    check_clipped(before, parts, want / 3, want)
+
+
+def test_checked_build_runs_clean():
+    """The checked build, in a process of its own: no index leaves its
+    buffer."""
+    import os
+    import subprocess
+    import sys
+
+    from dense_fp32_matrix_02_gb300 import build
+    path = build.build(checked=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k",
+         "not checked and not large", os.path.join(here, "test_gpu_grads.py")],
+        env=dict(os.environ, GEMM_F32_LIBRARY=path), cwd=here,
+        capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]

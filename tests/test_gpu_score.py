@@ -464,3 +464,59 @@ def test_refusals():
         L.log_probs_grad(x, w, ids, s, a, b.double())
     with pytest.raises(ValueError, match="ids"):
         L.log_probs(x, w, ids[:3])
+
+
+def test_checked_build_runs_clean():
+    """The checked build, in a process of its own: no index leaves its
+    buffer, and every result is in its tolerance."""
+    import os
+    import subprocess
+    import sys
+
+    from dense_fp32_matrix_02_gb300 import build
+    path = build.build(checked=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    which = ("sizes or unscored or boundaries or numbers or all_words or held"
+             " or lower or missing or masked or pieces or tokens_at_a_time")
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k", which,
+         os.path.join(here, "test_gpu_score.py")],
+        env=dict(os.environ, GEMM_F32_LIBRARY=path), cwd=here,
+        capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+
+
+def test_other_device_is_refused_or_used():
+    """Operands of another device than the current one are worked on there;
+    mixed devices are refused (here: the host beside the GPU)."""
+    x, w, ids, a, _ = case(4, 30, 8, BF16, 26)
+    with pytest.raises(ValueError, match="device"):
+        L.log_probs(x, w, ids.cpu())
+    with pytest.raises(ValueError):
+        L.log_probs(x, w.cpu(), ids)
+    s = L.log_probs(x, w, ids, keep=True)
+    with pytest.raises(ValueError, match="device"):
+        L.log_probs_grad(x, w, ids, s, a.cpu())
+    with pytest.raises(ValueError, match="device"):
+        L.log_probs_grad(x, w, ids, s._replace(kept=s.kept.cpu()), a)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, do not meet."""
+    cases = [case(300, 3000, 64, BF16, 30), case(77, 9000, 136, F16, 31)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    want = [L.log_probs(x, w, ids, top=6, keep=True)
+            for x, w, ids, _, _ in cases]
+    grads = [L.log_probs_grad(x, w, ids, s, a, b)
+             for s, (x, w, ids, a, b) in zip(want, cases)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for (x, w, ids, a, b), stream in zip(cases, streams):
+            with torch.cuda.stream(stream):
+                s = L.log_probs(x, w, ids, top=6, keep=True)
+                got.append((s, L.log_probs_grad(x, w, ids, s, a, b)))
+    torch.cuda.synchronize()
+    for i, (s, g) in enumerate(got):
+        for p, q in zip((*s[:5], *g), (*want[i % 2][:5], *grads[i % 2])):
+            assert torch.equal(p, q)

@@ -47,6 +47,16 @@ def test_refusals(built_lib):  # noqa: F811
     assert call(True, data=0, out=0, rows=0, ld=0, ld_out=0) == BAD
 
 
+def test_one_place_for_two_gradients(built_lib):  # noqa: F811
+    from dense_fp32_matrix_02_gb300 import gemm
+    lib = gemm.lib()
+    one = (P, P, 1, 4, 4, 4, 0)
+    for other in (one, (2 * P, P, 3, 5, 5, 5, 0)):
+        t = array.array("q", one + (4 * P, 4 * P, 1, 1, 1, 1, 2) + other)
+        assert lib.gemm_f32_grad_clip(3, t.buffer_info()[0], 1.0, P, P,
+                                      1 << 20, None) == BAD
+
+
 def test_workspace_size(built_lib):  # noqa: F811
     from dense_fp32_matrix_02_gb300 import gemm
     size = gemm.lib().gemm_f32_grad_workspace_size
