@@ -13,9 +13,10 @@
 // The list of gradients travels in the kernels' parameters, so that nothing
 // is copied to the device and a captured launch holds what it works on.  All
 // gradients are one line of 16-byte groups, cut into equal chunks; a block
-// takes every gridDim-th chunk and finds its gradient by bisection.  The
-// second launch takes the chunks from the last to the first: what the first
-// read last is still in L2.
+// takes every gridDim-th chunk and finds its gradient by bisection (chunks of 256 KB at most:
+// with 64 KB 1.3e9 elements took 1228 us, with 16 KB 1390).  The second launch
+// takes the chunks from the last to the first: what the first read last is still
+// in L2 (1e8 elements 110 us, 113 the other way).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,7 +36,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;  // 16-byte groups a thread loads side by side
 constexpr int kLeastChunk = kThreads;               // groups
-constexpr int kMostChunk = 4 * kAhead * kThreads;   // 64 KB
+constexpr int kRun = 4 * kAhead * kThreads;         // summed in fp32: 64 KB
+constexpr int kMostChunk = 4 * kRun;
 constexpr int kBlocksPerSm = 4;
 constexpr int kMaxBlocks = 2048;
 // Gradients of a launch: few (1.8 KB of parameters), or many (29 KB); more are
@@ -170,8 +172,22 @@ struct Chunk {
     }
     return v;
   }
-  // Streaming stores: nothing here reads the results, and L2 is better used
-  // by gradients that are still to be read again.
+  __device__ __forceinline__ void load_all(const Place (&p)[kAhead],
+                                           uint4 (&v)[kAhead],
+                                           unsigned int* status) const {
+    if (p[0].whole && p[1].whole && p[2].whole && p[3].whole) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {  // side by side
+        v[a] = make_uint4(0, 0, 0, 0);
+        if (span_ok(from(p[a]), 16, e.in, SIZE * ((e.rows - 1) * e.ld + e.cols),
+                    status))
+          v[a] = *reinterpret_cast<const uint4*>(from(p[a]));
+      }
+    } else {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) v[a] = load(p[a], status);
+    }
+  }
   __device__ __forceinline__ void store(const Place& p, uint4 v,
                                         unsigned int* status) const {
     Bits* to_ = to(p);
@@ -182,18 +198,18 @@ struct Chunk {
                    status))
         return;
       if (odd == 0) {
-        __stcs(reinterpret_cast<uint4*>(to_), v);
+        *reinterpret_cast<uint4*>(to_) = v;
         return;
       }
       if ((odd & 7u) == 0) {
-        __stcs(reinterpret_cast<uint2*>(to_), make_uint2(v.x, v.y));
-        __stcs(reinterpret_cast<uint2*>(to_) + 1, make_uint2(v.z, v.w));
+        reinterpret_cast<uint2*>(to_)[0] = make_uint2(v.x, v.y);
+        reinterpret_cast<uint2*>(to_)[1] = make_uint2(v.z, v.w);
         return;
       }
       if ((odd & 3u) == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          __stcs(reinterpret_cast<uint32_t*>(to_) + i, w[i]);
+          reinterpret_cast<uint32_t*>(to_)[i] = w[i];
         return;
       }
     }
@@ -204,11 +220,11 @@ struct Chunk {
         to_[i] = (Bits)(w[i * SIZE / 4] >> (i * SIZE % 4 * 8));
   }
 
-  // This thread's groups, kAhead at a time.
+  // This thread's groups from `first` to before `last`, kAhead at a time.
   template <typename Fn>
-  __device__ __forceinline__ void each(Fn fn) const {
+  __device__ __forceinline__ void each(int first, int last, Fn fn) const {
 #pragma unroll 1
-    for (int k0 = threadIdx.x; k0 < count; k0 += kAhead * kThreads) {
+    for (int k0 = first + threadIdx.x; k0 < last; k0 += kAhead * kThreads) {
       Place p[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) p[a] = place(k0 + a * kThreads);
@@ -217,31 +233,20 @@ struct Chunk {
   }
 };
 
-// The squares of a thread's part of a chunk are summed in fp32 (at most 16
-// groups, 128 squares, in 4 runs), the chunks in fp64.  Squares that
-// overflow fp32, or of which too little is left, show in the sum: those
-// groups are read again and summed in fp64, whose range holds them.
+// The squares of a thread's part of a run are summed in fp32 (at most 16
+// groups, 128 squares, in 4 sums), the runs in fp64.  Squares that overflow
+// fp32, or of which too little is left, show in the sum: those groups are read
+// again and summed in fp64, whose range holds them.
 template <int TYPE>
-__device__ __forceinline__ double sum_chunk(const Entry& e, long long chunk,
-                                            int size, unsigned int* status) {
-  const Chunk<TYPE> c(e, chunk, size);
+__device__ __forceinline__ double sum_run(const Chunk<TYPE>& c, int first,
+                                          int last, unsigned int* status) {
   constexpr int N = Chunk<TYPE>::N;
+  const Entry& e = c.e;
   float run[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t any = 0;
-  c.each([&](const Place(&p)[kAhead]) {
+  c.each(first, last, [&](const Place(&p)[kAhead]) {
     uint4 v[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) v[a] = make_uint4(0, 0, 0, 0);
-    if (p[0].whole && p[1].whole && p[2].whole && p[3].whole) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a)
-        if (span_ok(c.from(p[a]), 16, e.in,
-                    Chunk<TYPE>::SIZE * ((e.rows - 1) * e.ld + e.cols), status))
-          v[a] = *reinterpret_cast<const uint4*>(c.from(p[a]));
-    } else {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) v[a] = c.load(p[a], status);
-    }
+    c.load_all(p, v, status);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       any |= v[a].x | v[a].y | v[a].z | v[a].w;
@@ -256,7 +261,7 @@ __device__ __forceinline__ double sum_chunk(const Entry& e, long long chunk,
   if (any != 0 && !(sum >= 0x1p-96f && sum <= 1e37f)) {
     double wide = 0.0;
 #pragma unroll 1
-    for (int k = threadIdx.x; k < c.count; k += kThreads) {
+    for (int k = first + threadIdx.x; k < last; k += kThreads) {
       float f[N];
       unpack<TYPE>(c.load(c.place(k), status), f);
 #pragma unroll
@@ -264,6 +269,17 @@ __device__ __forceinline__ double sum_chunk(const Entry& e, long long chunk,
     }
     return wide;
   }
+  return sum;
+}
+
+template <int TYPE>
+__device__ __forceinline__ double sum_chunk(const Entry& e, long long chunk,
+                                            int size, unsigned int* status) {
+  const Chunk<TYPE> c(e, chunk, size);
+  double sum = 0.0;
+#pragma unroll 1
+  for (int k = 0; k < c.count; k += kRun)
+    sum += sum_run<TYPE>(c, k, min(k + kRun, c.count), status);
   return sum;
 }
 
@@ -282,36 +298,20 @@ __device__ __forceinline__ void scale_chunk(const Entry& e, long long chunk,
     for (int i = 0; i < N; ++i) f[i] *= factor;
     return pack<TYPE>(f);
   };
-  c.each([&](const Place(&p)[kAhead]) {
+  c.each(0, c.count, [&](const Place(&p)[kAhead]) {
     uint4 v[kAhead];
-    if (p[0].whole && p[1].whole && p[2].whole && p[3].whole) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        v[a] = make_uint4(0, 0, 0, 0);
-        if (span_ok(c.from(p[a]), 16, e.in,
-                    Chunk<TYPE>::SIZE * ((e.rows - 1) * e.ld + e.cols), status))
-          v[a] = *reinterpret_cast<const uint4*>(c.from(p[a]));
-      }
-    } else {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) v[a] = c.load(p[a], status);
-    }
+    c.load_all(p, v, status);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) c.store(p[a], scaled(v[a]), status);
   });
 }
 
-// The sum of a value over the block, in every thread.
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double part[kThreads / 32];
+// Sums of fp64 take 16 cycles a warp and addition, on one unit an SM: as few
+// as can be, by the first warp (every thread of every block adding up the
+// partial sums and dividing took 8 us of a call).
+__device__ __forceinline__ double warp_sum(double v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double all = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) all += part[w];
-  return all;
+  return v;
 }
 
 // The gradient of a chunk, and the chunk's number in it.
@@ -343,7 +343,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     else
       sum += sum_chunk<GEMM_F32_GRAD_F32>(e, chunk, list.chunk, list.status);
   }
-  sum = block_sum(sum);
+  __shared__ double part[kThreads];
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) sum += part[threadIdx.x + 32 * w];
+  sum = warp_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
@@ -355,12 +361,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 int partials, float max_norm, float* norm) {
   griddep_wait();
   griddep_launch_dependents();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
-  const double n = sqrt(block_sum(sum));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
-  const float factor =
-      n > (double)max_norm && n < INFINITY ? (float)(max_norm / n) : 1.f;
+  __shared__ float s_factor;
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < partials; i += 32) sum += partial[i];
+    sum = warp_sum(sum);
+    if (threadIdx.x == 0) {
+      const double n = sqrt(sum);
+      if (norm && blockIdx.x == 0) *norm = (float)n;
+      s_factor = n > (double)max_norm && n < INFINITY ? (float)(max_norm / n)
+                                                      : 1.f;
+    }
+  }
+  __syncthreads();
+  const float factor = s_factor;
   const long long last = list.first[list.n] - 1;
 #pragma unroll 1
   for (long long i = blockIdx.x; i <= last; i += gridDim.x) {
@@ -492,9 +507,9 @@ int run(int64_t n, const gemm_f32_grad* all, bool clip, float max_norm,
   if (e != cudaSuccess) return record_cuda_error(e);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int most = std::min(kBlocksPerSm * sms, kMaxBlocks);
-  // the largest chunks of which every block has four, or the least
+  // the largest chunks of which every block has two, or the least
   int chunk = kLeastChunk;
-  while (chunk < kMostChunk && total / (2 * chunk) >= 4ll * most) chunk *= 2;
+  while (chunk < kMostChunk && total / (2 * chunk) >= 2ll * most) chunk *= 2;
   double* partial = static_cast<double*>(ws);
   int partials = 0;
   auto sum = [&](const auto& list, int blocks) {
