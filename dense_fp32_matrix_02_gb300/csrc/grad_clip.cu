@@ -13,10 +13,10 @@
 // The list of gradients travels in the kernels' parameters, so that nothing
 // is copied to the device and a captured launch holds what it works on.  All
 // gradients are one line of 16-byte groups, cut into equal chunks; a block
-// takes every gridDim-th chunk and finds its gradient by bisection (chunks of 256 KB at most:
-// with 64 KB 1.3e9 elements took 1228 us, with 16 KB 1390).  The second launch
-// takes the chunks from the last to the first: what the first read last is still
-// in L2 (1e8 elements 110 us, 113 the other way).
+// takes every gridDim-th chunk and finds its gradient by bisection (chunks of
+// 256 KB at most: with 64 KB 1.3e9 elements took 1228 us, with 16 KB 1390).  The
+// second launch takes the chunks from the last to the first: what the first read
+// last is still in L2 (1e8 elements 110 us, 113 the other way).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -142,7 +142,8 @@ struct Chunk {
       p.row += more;
       j -= (long long)more * per;
     }
-    const uintptr_t row = reinterpret_cast<uintptr_t>(e.in) + p.row * e.ld * SIZE;
+    const uintptr_t row =
+        reinterpret_cast<uintptr_t>(e.in) + p.row * e.ld * SIZE;
     p.col = j * N - (long long)((row & 15u) / SIZE);
     p.here = k < count && p.col < e.cols;
     p.whole = p.here && p.col >= 0 && p.col + N <= e.cols;
@@ -565,7 +566,8 @@ int gemm_f32_grad_clip(int64_t n, const gemm_f32_grad* grads, float max_norm,
 int64_t gemm_f32_grad_workspace_size(int64_t n) {
   if (n < 0) return -GEMM_F32_ERR_INVALID_ARG;
   if (n > kMostRows) return -GEMM_F32_ERR_UNSUPPORTED;
-  return std::max<int64_t>(launches(n), 1) * kMaxBlocks * (int64_t)sizeof(double);
+  return std::max<int64_t>(launches(n), 1) * kMaxBlocks *
+         (int64_t)sizeof(double);
 }
 
 }  // extern "C"

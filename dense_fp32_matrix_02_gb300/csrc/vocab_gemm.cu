@@ -592,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int learnt = header ? header->learnt : p.T;
   const int lo = FEW ? header->lo : 0;
   constexpr bool CHUNK = FORWARD && SCORE;
-  const int row0 = CHUNK ? (int)min((long long)phase * p.chunk, (long long)learnt)
-                         : 0;
+  const int row0 =
+      CHUNK ? (int)min((long long)phase * p.chunk, (long long)learnt) : 0;
   const int all_rows =
       CHUNK ? min(learnt - row0, p.chunk) : vocab_rows(learnt, lo);
   Walk<FORWARD> walk(p, all_rows, phase, pair, pairs);

@@ -1068,7 +1068,8 @@ int gemm_f32_vocab_score_grad(
   c.type = type, c.T = T, c.V = V, c.D = D;
   c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
   c.targets = ids, c.top = 1, c.tau = temperature;
-  c.grad = true, c.lse = lse, c.grad_loss = grad_logp, c.grad_stride = logp_stride;
+  c.grad = true, c.lse = lse;
+  c.grad_loss = grad_logp, c.grad_stride = logp_stride;
   c.dX = dX, c.lddx = lddx, c.dW = dW, c.lddw = lddw;
   c.score = true, c.entropy = entropy, c.grad_entropy = grad_entropy;
   c.entropy_stride = entropy_stride;

@@ -11,9 +11,9 @@
 // (half tiles) with the largest maxima, of equal ones the first: any element
 // elsewhere has k larger ones before it, or equal ones with lower ids.  So the
 // logits are stored, of some tokens at a time, and of each row only those
-// stretches are read, about k·128 of V logits.  (Storing them costs the products
-// 5 % at width 4096 and 28 % at width 768, 4096 and 8192 tokens; for few tokens
-// 2·T/D of the weights' bytes.)
+// stretches are read, about k·128 of V logits.  (Storing them costs the
+// products 5 % at width 4096 and 28 % at width 768, 4096 and 8192 tokens; for
+// few tokens 2·T/D of the weights' bytes.)
 //   The rank of two logits should not hang on how a sum rounds (on the tile it
 // was made in, so on the batch): the k + kSpare largest are computed again
 // from the operands, products exact in fp32, summed in pairs of fp32 (48
@@ -87,7 +87,8 @@ __device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
 #pragma unroll 4
   for (int g = first; g < parts; g += step) {
     float4 b = make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
-    if (span_ok(sums + g, 16, p.sums, 16ll * p.T * parts, p.status)) b = sums[g];
+    if (span_ok(sums + g, 16, p.sums, 16ll * p.T * parts, p.status))
+      b = sums[g];
     largest(g, b.w);
     const float m = fmaxf(st.m, b.x);
     const float ref = m == -INFINITY ? 0.f : m;
@@ -356,7 +357,8 @@ __device__ __forceinline__ float2 across(float2 v, int o) {
                      __shfl_xor_sync(0xffffffffu, v.y, o));
 }
 
-// WORDS rows of W at a time, AHEAD loads of each side by side (a row of W comes from far).
+// WORDS rows of W at a time, AHEAD loads of each side by side (a row of W comes
+// from far).
 template <int AB_TYPE, int WORDS, int AHEAD>
 __device__ __forceinline__ void exact_dots(const uint16_t* x,
                                            const uint16_t* const (&w)[WORDS],
@@ -377,7 +379,8 @@ __device__ __forceinline__ void exact_dots(const uint16_t* x,
       const int at = c + 256 * j;
 #pragma unroll
       for (int i = 0; i < WORDS; ++i)
-        b[i][j] = at < whole ? *reinterpret_cast<const uint4*>(w[i] + at) : zero;
+        b[i][j] =
+            at < whole ? *reinterpret_cast<const uint4*>(w[i] + at) : zero;
     }
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {  // (x is near)
@@ -717,7 +720,8 @@ cudaError_t vocab_score_results(const VocabCall& c, int phase, int sms,
   auto pick = [&](auto bf16, auto f16, int threads) {
     return launch(c.type == GEMM_F32_MIXED_BF16 ? bf16 : f16, threads);
   };
-  if (rows <= 2 * sms) return pick(top_kernel<1, 1024>, top_kernel<0, 1024>, 1024);
+  if (rows <= 2 * sms)
+    return pick(top_kernel<1, 1024>, top_kernel<0, 1024>, 1024);
   if (rows <= 5 * sms) return pick(top_kernel<1, 256>, top_kernel<0, 256>, 256);
   return pick(top_kernel<1, 128>, top_kernel<0, 128>, 128);
 }

@@ -10,7 +10,8 @@ all of them together, and all of them scaled so that it is at most a bound;
 Gradients are CUDA tensors of bfloat16, float16 or float32, mixed as they
 come, all on one device: contiguous of any shape, or matrices with rows
 further apart (a view's, or a padded one's); a tensor that is to be clipped is
-listed once.  A norm that is not finite clips nothing.  Autograd records none of this.
+listed once.  A norm that is not finite clips nothing.  Autograd records none
+of this.
 """
 
 from __future__ import annotations

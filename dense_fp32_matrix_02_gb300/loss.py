@@ -5,9 +5,9 @@ The last product of a language model, logits = x·wᵀ with x (tokens × width)
 the hidden states and w (vocab × width) the output matrix, together with its
 loss: softmax cross entropy, or distillation from a teacher's top logits; or
 with the log probabilities of given words, their distribution's entropy and
-the likeliest other words.  The losses never store the logits;
-``include/gemm_f32.h`` (gemm_f32_vocab_*) gives the formulas.  Like every call of the binding these are asynchronous on
-``stream`` (None: the current one), raise ``GemmError`` for a status other
+the likeliest words.  The losses never store the logits;
+``include/gemm_f32.h`` (gemm_f32_vocab_*) gives the formulas.  Like every call
+of the binding these are asynchronous on ``stream`` (None: the current one), raise ``GemmError`` for a status other
 than 0, and take an optional ``workspace`` (a CUDA tensor of at least
 ``workspace_size`` bytes; allocated here when None).
 

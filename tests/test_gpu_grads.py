@@ -117,7 +117,8 @@ def test_numbers_of_gradients(count):
 def test_contiguous_beside_rows():
     """A gradient whose rows are apart, clipped into one whose are not."""
     a, b = tensor(37, 53, BF16, 1, pad=11), tensor(37, 53, BF16, 1)
-    for src, dst in ((a, torch.zeros_like(b)), (b, tensor(37, 53, BF16, 5, pad=3))):
+    for src, dst in ((a, torch.zeros_like(b)),
+                     (b, tensor(37, 53, BF16, 5, pad=3))):
         C.clip_([src], 1.0, out=[dst])
         check_clipped([src], [dst], 1.0, norm_of([src]))
     with pytest.raises(ValueError, match="contiguous"):
@@ -219,6 +220,23 @@ def test_same_bits_again_and_graph():
         t.mul_(2.0)
     graphs[0].replay()
     assert abs(float(norms[0]) - 2 * float(eager)) <= 4e-6 * float(eager)
+
+
+def test_many_gradients_in_a_graph():
+    """A captured launch holds its list of gradients, a long one too."""
+    ts = [tensor(1, 1 + (i * 37) % 500, F32, i)[0] for i in range(600)]
+    out = [torch.empty_like(t) for t in ts]
+    C.clip_(ts, 3.0, out=out)
+    keep = [o.clone() for o in out]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        C.clip_(ts, 3.0, out=out)
+    for o in out:
+        o.fill_(math.nan)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, k) for o, k in zip(out, keep))
 
 
 def test_streams():

@@ -145,7 +145,8 @@ def test_rows_off_boundaries(pad, skew, dtype):
 
 
 @pytest.mark.parametrize("top", [1, 2, 8, 31, 64, 100, 255, 256])
-@pytest.mark.parametrize("T,V", [(3, 256), (5, 300), (40, 5000), (300, 40000)])
+@pytest.mark.parametrize("T,V", [(3, 256), (5, 300), (40, 5000), (300, 40000),
+                                 (500, 20000), (1100, 700), (1500, 40000)])
 def test_numbers_of_words(T, V, top):
     """Vocabularies of fewer stretches than words asked for, of about as
     many, and of many more."""
@@ -170,7 +171,8 @@ def test_more_stretches_than_are_held():
 def test_equal_logits_by_the_lower_id():
     """Small integers: logits are exact, and most are equal to others."""
     gen = torch.Generator(device=DEV).manual_seed(4)
-    for T, V in ((1, 3000), (9, 700), (300, 12000)):
+    for T, V in ((1, 3000), (9, 700), (300, 12000), (500, 3000), (500, 40000),
+                 (1200, 700), (1200, 40000)):
         x = torch.randint(-1, 2, (T, 16), generator=gen, device=DEV).to(BF16)
         w = torch.randint(-1, 2, (V, 16), generator=gen, device=DEV).to(BF16)
         x[0] = 0  # every logit is 0
