@@ -153,7 +153,8 @@ struct VocabCall {
   void* Wp;              // W's packed copy, or null (W has a tensor map)
   // forward
   float2* stats;  // [half tiles' columns][learnt]: (max, sum), powers of 2
-  float* picked;  // [T][top]: logits / τ of the entries
+  float* picked;  // [T][top]: logits / τ of the entries (log probabilities:
+                  // logits)
   // log probabilities
   float4* sums;    // in place of stats, [learnt][half tiles' columns]: (max,
                    // sum, Σ e·log2 e of its terms e, the largest logit)

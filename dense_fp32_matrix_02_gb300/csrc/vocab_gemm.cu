@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e.id[0] < n + 32) {
               float* to = p.picked + (long long)r * p.top + e.at;
               if (span_ok(to, 4, p.picked, 4ll * p.T * p.top, wc.status))
-                *to = pick(f, e.id[0] - n) * p.inv_tau;
+                *to = pick(f, e.id[0] - n) * (SCORE ? 1.f : p.inv_tau);
               e.pass<false>();
             }
             next = __reduce_min_sync(0xffffffffu, e.id[0]);

@@ -3,9 +3,11 @@
 //
 // With z = X·Wᵀ, c = log2 e / τ and, per row, e_v = 2^(c·z_v − r), r = max c·z,
 //   S = Σ e_v,  E = Σ e_v·log2 e_v:
-//   lse = ln 2·(r + log2 S),   logp = z_y/τ − lse,
+//   lse = ln 2·(r + log2 S),   logp = ln 2·(c·z_y − r − log2 S),
 //   entropy = −Σ p·log p = ln 2·(log2 S − E/S).
-// The products leave S, E, r and the largest z of each half tile.
+// The products leave S, E, r and the largest z of each half tile.  (As z_y/τ −
+// lse, logp would have lse's rounding, 1e-6 of a probability near 1 whose
+// logarithm is 1e-2.)
 //
 // The likeliest words.  The k largest elements of a row lie in the k stretches
 // (half tiles) with the largest maxima, of equal ones the first: any element
@@ -34,7 +36,7 @@
 namespace gemm_f32_impl {
 namespace {
 
-constexpr float kLn2 = 0.69314718056f;
+constexpr float kLn2 = 0.69314718056f, kLog2e = 1.4426950408889634f;
 
 // Numbers in the order of the floats, from kLowest on; a NaN counts as -Inf.
 constexpr uint32_t kLowest = 0x007fffffu;
@@ -104,18 +106,20 @@ __device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
   return st;
 }
 
-__device__ __forceinline__ float lse_of(Stat st) {
-  return st.m * kLn2 + logf(st.s);
+// The log probability of a logit z in a row of reference m and log S.
+__device__ __forceinline__ float log_prob(const VocabCall& p, float z, float m,
+                                          float log_sum) {
+  return fmaf(kLn2, fmaf(z, p.inv_tau * kLog2e, -m), -log_sum);
 }
 
-// A row's results; at: its word's logit / τ.
+// A row's results; z: its word's logit.
 __device__ __forceinline__ void store_results(const VocabCall& p, long long t,
-                                              bool scored, Stat st, float lse,
-                                              float at) {
+                                              bool scored, Stat st,
+                                              float log_sum, float z) {
   // (the difference of equal numbers where one word has all: not below 0)
-  const float entropy = logf(st.s) - kLn2 * (st.e / st.s);
-  p.loss[t] = scored ? at - lse : 0.f;
-  p.lse_out[t] = scored ? lse : 0.f;
+  const float entropy = log_sum - kLn2 * (st.e / st.s);
+  p.loss[t] = scored ? log_prob(p, z, st.m, log_sum) : 0.f;
+  p.lse_out[t] = scored ? fmaf(kLn2, st.m, log_sum) : 0.f;
   p.entropy_out[t] = scored && !(entropy < 0.f) ? entropy : 0.f;
 }
 
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (r >= learnt) return;
   const long long t = learnt != p.T ? p.token[r] : r;
   const bool scored = p.header || vocab_is_learnt(p, t);
-  const float at = scored ? p.picked[r] : 0.f;
+  const float z = scored ? p.picked[r] : 0.f;
   Stat st = merge_warp(share_of(p, r, threadIdx.x, parts, kFinishThreads,
                                 [](int, float) {}));
   if (lane == 0) s_part[warp] = st;
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (warp > 0) return;
   st = lane < kFinishThreads / 32 ? s_part[lane] : Stat{-INFINITY, 0.f, 0.f};
   st = merge_warp(st);
-  if (lane == 0) store_results(p, t, scored, st, lse_of(st), at);
+  if (lane == 0) store_results(p, t, scored, st, logf(st.s), z);
 }
 
 // ------------------------------------------------------- likeliest words
@@ -444,18 +448,19 @@ __device__ __forceinline__ void exact_logits(const VocabCall& p, long long t,
 }
 
 // The first of k words, by value and id.  Their log probabilities are those of
-// the fp32 logits, as the given word's is: lse is made of them, and what the
+// the fp32 logits, as the given word's is: S is made of them, and what the
 // tensor cores drop, towards 0, shrinks both (exact logits beside it were up to
 // 1.8 times as far off as fp32 sums that round to nearest).
 template <int THREADS>
 __device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
                                              const float* z, const int* ids,
                                              const float2* value, int k,
-                                             int thread, float lse) {
+                                             int thread, float m,
+                                             float log_sum) {
   for (int c = thread; c < k; c += THREADS) {
     const float2 v = value[c];
     const int id = ids[c];
-    const float at = __fmul_rn(z[id], p.inv_tau);  // (as it is picked)
+    const float logit = z[id];
     int rank = 0;
 #pragma unroll 4
     for (int o = 0; o < k; ++o) {
@@ -465,7 +470,8 @@ __device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
     }
     if (rank < p.alternatives) {
       p.top_out[t * p.alternatives + rank] = id;
-      p.top_logp[t * p.alternatives + rank] = at - lse;
+      p.top_logp[t * p.alternatives + rank] =
+          log_prob(p, logit, m, log_sum);
     }
   }
 }
@@ -530,8 +536,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   st = merge_warp(st);
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
-  const float lse = __shfl_sync(0xffffffffu, lse_of(st), 0);
-  if (tid == 0) store_results(p, t, true, st, lse, p.picked[r]);
+  // (in every thread as the first has it)
+  st.m = __shfl_sync(0xffffffffu, st.m, 0);
+  const float log_sum = logf(__shfl_sync(0xffffffffu, st.s, 0));
+  if (tid == 0) store_results(p, t, true, st, log_sum, p.picked[r]);
 
   auto maximum = [&](int g) {
     return held ? s_key[g] : order_of(p.sums[(long long)r * parts + g].w);
@@ -658,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     exact_logits<AB_TYPE, kWords, kWords == 1 ? 4 : 2>(p, t, z, s_id, c0, k,
                                                        lane, s_value);
   __syncthreads();
-  write_ranked<THREADS>(p, t, z, s_id, s_value, k, tid, lse);
+  write_ranked<THREADS>(p, t, z, s_id, s_value, k, tid, st.m, log_sum);
 }
 
 // ------------------------------------------------------------- gradients

@@ -259,6 +259,33 @@ def test_sharp_and_flat_distributions():
 
 
 @TYPES
+def test_near_certain_words(dtype):
+    """Log probabilities near 0 keep their own digits, not lse's.  The logits
+    are exact (small integers over 4), so what is left is one exponential near
+    1 (2^-22), the sum of the others (1e-6 of it), the rounding of a sum near
+    1 and of its logarithm (2^-23 each): 6e-7, where lse's own rounding would
+    be 2e-6 of logits of 20."""
+    T, V, D = 64, 1000, 64
+    gen = torch.Generator(device=DEV).manual_seed(33)
+    x = torch.randint(-1, 2, (T, D), generator=gen, device=DEV).to(dtype)
+    w = (torch.randint(-4, 5, (V, D), generator=gen, device=DEV) / 4).to(dtype)
+    ids = torch.arange(T, device=DEV)
+    w[:T] = x / 2
+    s = L.log_probs(x, w, ids, top=3)
+    want = ref.scores(x, w, ids, 1.0, 3)
+    assert float(want["lse"].median()) > 18
+    assert float(want["logp"].median()) > -0.02
+    for got, exact in ((s.logp, want["logp"]), (s.entropy, want["entropy"]),
+                       (s.top_logp[:, 0], want["top_logp"][:, 0])):
+        close = want["logp"] > -0.05
+        err = (got.double() - exact).abs()[close]
+        assert int(close.sum()) > T // 2
+        # (entropy: the others' terms, each log p ~ -10 of them)
+        scale = 1.0 if got is not s.entropy else 10.0
+        assert float(err.max()) <= 6e-7 * scale
+
+
+@TYPES
 def test_no_gradient_of_entropy(dtype):
     """None, zeros and cross entropy's gradient of the opposite sign."""
     x, w, ids, a, _ = case(300, 900, 72, dtype, 13, 0.2)
