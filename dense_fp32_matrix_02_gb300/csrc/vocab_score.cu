@@ -719,17 +719,20 @@ cudaError_t vocab_score_results(const VocabCall& c, int phase, int sms,
     return launch_pdl(fn, dim3(rows), dim3(threads), 0, stream, c, row0);
   };
   if (c.alternatives == 0) return launch(finish_score_kernel, kFinishThreads);
-  // A block's warps each sum words' exact logits.  Where there is about a row
-  // to an SM, nothing else hides the wait for their rows of W: 32 warps, one
-  // word each (304 tokens, 100000 × 2048, 64 words: 210 us; 512 tokens 268 us,
-  // 230 with 8 warps).  With several rows to an SM 8 warps (400 tokens 223 us,
-  // 267 with 4), with many 4, of which more blocks overlap (4096 tokens, 32000
-  // × 768, 5 words: 268 us with 8, 246 with 4).
+  // A block's warps each sum words' exact logits.  As many as leave every row a
+  // place on an SM (1024 threads of 64 registers are all of one): with a row
+  // to an SM nothing else hides the wait for rows of W.  32 warps up to a row
+  // an SM; 16 up to two (256 tokens, 32000 × 768, 5 words: 41 us with 32, 35
+  // with 8, 33 with 16); 8 up to five (400 tokens, 100000 × 2048, 64 words: 223
+  // us, 267 with 4; 512 tokens 268 with 32); 4 beyond, of which more blocks
+  // overlap (4096 tokens, 32000 × 768, 5 words: 268 us with 8, 246 with 4).
   auto pick = [&](auto bf16, auto f16, int threads) {
     return launch(c.type == GEMM_F32_MIXED_BF16 ? bf16 : f16, threads);
   };
-  if (rows <= 2 * sms)
+  if (rows <= sms)
     return pick(top_kernel<1, 1024>, top_kernel<0, 1024>, 1024);
+  if (rows <= 2 * sms)
+    return pick(top_kernel<1, 512>, top_kernel<0, 512>, 512);
   if (rows <= 5 * sms) return pick(top_kernel<1, 256>, top_kernel<0, 256>, 256);
   return pick(top_kernel<1, 128>, top_kernel<0, 128>, 128);
 }
