@@ -144,6 +144,26 @@ def test_rows_off_boundaries(pad, skew, dtype):
         assert bool(gap.isnan().all())
 
 
+@TYPES
+@pytest.mark.parametrize("D,pad,skew", [
+    (505, 0, 0), (511, 0, 1), (512, 1, 2), (520, 3, 3), (1003, 0, 4),
+    (1019, 2, 5), (1025, 0, 6), (1031, 1, 7), (2045, 0, 0), (2050, 0, 0)])
+def test_long_rows_off_boundaries(D, pad, skew, dtype):
+    """Rows long enough to be packed piece by piece, from every element of a
+    16-byte boundary on; gradients in rows that start on even and odd
+    elements."""
+    for T in (3, 140):
+        x, w, ids, a, b = case(T, 333, D, dtype, D, 0.0, pad, skew)
+        check_scores(x, w, ids, 1.0, 4)
+        dx = matrix(T, D, dtype, 1, 1.0, pad, skew)
+        dw = matrix(333, D, dtype, 1, 1.0, pad, skew)
+        check_step(x, w, ids, a, b, dx=dx, dw=dw)
+        for m in (dx, dw) if pad else ():
+            gap = m.as_strided((m.shape[0] - 1, pad), (m.stride(0), 1),
+                               m.storage_offset() + D)
+            assert bool(gap.isnan().all())
+
+
 @pytest.mark.parametrize("top", [1, 2, 8, 31, 64, 100, 255, 256])
 @pytest.mark.parametrize("T,V", [(3, 256), (5, 300), (40, 5000), (300, 40000),
                                  (500, 20000), (1100, 700), (1500, 40000)])
@@ -505,7 +525,7 @@ def test_checked_build_runs_clean():
     from dense_fp32_matrix_02_gb300 import build
     path = build.build(checked=True)
     here = os.path.dirname(os.path.abspath(__file__))
-    which = ("sizes or unscored or boundaries or numbers or all_words or held"
+    which = ("sizes or unscored or off_boundaries or numbers or all_words or held"
              " or lower or missing or masked or pieces or tokens_at_a_time")
     r = subprocess.run(
         [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k", which,
