@@ -151,6 +151,7 @@ struct VocabCall {
   long long ldxp;        // zero rows up to a multiple of 64; or, few tokens,
   long long xp_rows;     // both twice (VocabHeader::lo)
   void* Wp;              // W's packed copy, or null (W has a tensor map)
+  int w_packed;       // that a call before has made
   // forward
   float2* stats;  // [half tiles' columns][learnt]: (max, sum), powers of 2
   float* picked;  // [T][top]: logits / τ of the entries (log probabilities:

@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(1024)
                                        forward ? 64 : 128, p.pairs);
     }
   }
+  if (p.w_packed) return;
   if (p.Wp && (p.D + 7) / 8 >= kLongRow)
     pack_long_rows(static_cast<const uint16_t*>(p.W), p.ldw, p.D,
                    static_cast<uint16_t*>(p.Wp), p.ldxp, nullptr,
@@ -841,8 +842,12 @@ bool logits_countable(int64_t T, int64_t V) {
   return vocab_tiles(T) * (V / kVocabTile + 1) <= 1 << 30;
 }
 
-// Bytes of the kept logits: whole rows on 32-byte boundaries.
-int64_t kept_bytes(int64_t T, int64_t V) { return T * up(V, 8) * 4; }
+// Bytes of the kept logits, whole rows on 32-byte boundaries, and of W's packed
+// copy behind them.
+int64_t kept_logits(int64_t T, int64_t V) { return up(T * up(V, 8) * 4, 256); }
+int64_t kept_bytes(int64_t T, int64_t V, int64_t D, bool pack_w) {
+  return kept_logits(T, V) + (pack_w ? V * up(D, 8) * 2 : 0);
+}
 
 // What log probabilities are given besides.
 int check_score(const Request& r) {
@@ -887,7 +892,8 @@ int check(const Request& r) {
   if (!countable(r.T, r.V, r.D)) return GEMM_F32_ERR_UNSUPPORTED;
   if (r.kept && (!logits_countable(r.T, r.V)))
     return GEMM_F32_ERR_UNSUPPORTED;
-  if (r.kept && r.kept_bytes < kept_bytes(r.T, r.V))
+  if (r.kept &&
+      r.kept_bytes < kept_bytes(r.T, r.V, r.D, !vocab_maps(r.W, r.ldw)))
     return GEMM_F32_ERR_INVALID_ARG;
   return GEMM_F32_OK;
 }
@@ -917,7 +923,9 @@ cudaError_t launch_targets(const VocabCall& c, bool forward, int sms,
   // (a block packs the rows of 32 tokens, or of 2 where there are few)
   const bool few = !forward && c.T <= kVocabFewTokens;
   const int blocks =
-      c.Wp ? sms : std::min(sms, few ? (c.T + 1) / 2 : (c.T + 31) / 32);
+      c.Wp && !c.w_packed
+          ? sms
+          : std::min(sms, few ? (c.T + 1) / 2 : (c.T + 31) / 32);
   return launch_pdl(number_tokens_kernel, dim3(blocks), dim3(1024), 0, stream,
                     c, forward ? 1 : 0);
 }
@@ -980,8 +988,8 @@ int run(const Request& r) {
   VocabCall c = {};
   const int64_t need =
       lay_out(&c, static_cast<char*>(r.ws), r.T, r.V, r.D, r.top, r.grad,
-              !vocab_maps(r.W, r.ldw), r.score ? r.alternatives : -1,
-              r.kept != nullptr);
+              !vocab_maps(r.W, r.ldw) && !r.kept,
+              r.score ? r.alternatives : -1, r.kept != nullptr);
   if (!r.ws || (reinterpret_cast<uintptr_t>(r.ws) & 15u) != 0 ||
       r.ws_bytes < need)
     return GEMM_F32_ERR_INVALID_ARG;
@@ -1015,6 +1023,10 @@ int run(const Request& r) {
     c.ld_logits = up(r.V, 8);
     c.chunk = c.T;
     c.keep = 1;
+    if (!vocab_maps(r.W, r.ldw)) {
+      c.Wp = static_cast<char*>(r.kept) + kept_logits(r.T, r.V);
+      c.w_packed = r.grad;
+    }
   }
   c.entropy_out = r.entropy_out;
   c.top_logp = r.top_logp, c.top_out = r.top_out;
@@ -1152,11 +1164,13 @@ int gemm_f32_vocab_score_grad(
   return run(c);
 }
 
-int64_t gemm_f32_vocab_score_kept_size(int64_t T, int64_t V) {
-  if (T < 0 || V < 1) return -GEMM_F32_ERR_INVALID_ARG;
-  if (!countable(T, V, 1) || !logits_countable(T, V))
+int64_t gemm_f32_vocab_score_kept_size(int64_t T, int64_t V, int64_t D,
+                                       int aligned) {
+  if (T < 0 || V < 1 || D < 1 || (aligned != 0 && aligned != 1))
+    return -GEMM_F32_ERR_INVALID_ARG;
+  if (!countable(T, V, D) || !logits_countable(T, V))
     return -GEMM_F32_ERR_UNSUPPORTED;
-  return kept_bytes(T, V);
+  return kept_bytes(T, V, D, aligned == 0);
 }
 
 int64_t gemm_f32_vocab_score_workspace_size(int64_t T, int64_t V, int64_t D,
@@ -1169,9 +1183,10 @@ int64_t gemm_f32_vocab_score_workspace_size(int64_t T, int64_t V, int64_t D,
   if (!countable(T, V, D)) return -GEMM_F32_ERR_UNSUPPORTED;
   VocabCall c = {};
   int64_t n =
-      lay_out(&c, nullptr, T, V, D, 1, false, aligned == 0, top, keep != 0);
-  if (grad)  // (room for either call)
-    n = std::max(n, lay_out(&c, nullptr, T, V, D, 1, true, aligned == 0, 0));
+      lay_out(&c, nullptr, T, V, D, 1, false, aligned == 0 && !keep, top,
+              keep != 0);
+  if (grad)  // (room for either call; W's copy is in `kept`)
+    n = std::max(n, lay_out(&c, nullptr, T, V, D, 1, true, false, 0));
   return n;
 }
 

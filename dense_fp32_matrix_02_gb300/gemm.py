@@ -142,7 +142,7 @@ def lib() -> ctypes.CDLL:
             vp, cf, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
             i64, vp]
         L.gemm_f32_vocab_score_kept_size.restype = i64
-        L.gemm_f32_vocab_score_kept_size.argtypes = [i64, i64]
+        L.gemm_f32_vocab_score_kept_size.argtypes = [i64, i64, i64, ci]
         L.gemm_f32_vocab_score_workspace_size.restype = i64
         L.gemm_f32_vocab_score_workspace_size.argtypes = [i64, i64, i64, i64,
                                                           ci, ci, ci]

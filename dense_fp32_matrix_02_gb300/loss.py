@@ -288,7 +288,8 @@ def log_probs(x, w, ids, top=0, temperature=1.0, keep=False, workspace=None,
     exp(logits/temperature), the distribution's entropy and, with ``top``, the
     likeliest words, largest first, equal logits by the lower id.  A token
     whose id is outside [0, vocab) is not scored (zeros; ids of -1).  ``keep``:
-    the logits stay in memory (4 bytes each) for log_probs_grad."""
+    the logits stay in memory (4 bytes each) for log_probs_grad, and a copy of
+    w if its rows do not start on 16-byte boundaries."""
     head, aligned = _operands(x, w)
     device, T, V = x.device, head[1], head[2]
     y, _ = _vector(ids, "ids", T, torch.int64, device)
@@ -307,7 +308,9 @@ def log_probs(x, w, ids, top=0, temperature=1.0, keep=False, workspace=None,
             top_ids = _new((T, top), torch.int64, device, stream)
             tp, ip = top_logp.data_ptr() or None, top_ids.data_ptr() or None
         if keep:
-            kn = int(_g.lib().gemm_f32_vocab_score_kept_size(T, V))
+            kn = int(_g.lib().gemm_f32_vocab_score_kept_size(
+                T, V, head[3], int((head[6] or 0) % 16 == 0
+                                   and head[7] % 8 == 0)))
             if kn < 0:
                 _g._check(-kn, "gemm_f32_vocab_score_kept_size")
             kept = _new(kn, torch.uint8, device, stream)

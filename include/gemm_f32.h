@@ -536,9 +536,10 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  * logp, lse, entropy and top_logp are 0, its top_ids -1, whatever its row of X
  * holds.
  *
- * `kept`, where it is not NULL, receives the logits for the gradients: 16-byte
- * aligned device memory of at least gemm_f32_vocab_score_kept_size(T, V) bytes
- * (4 an element), whose layout is the library's own.
+ * `kept`, where it is not NULL, receives the logits for the gradients, and a
+ * copy of W where its rows do not start on 16-byte boundaries: 16-byte aligned
+ * device memory of at least gemm_f32_vocab_score_kept_size bytes (4 a logit, 2
+ * an element of the copy), whose layout is the library's own.
  *
  * gemm_f32_vocab_score_grad takes ids, lse, entropy and kept as the forward
  * call of the same operands left them, and the gradients of logp
@@ -572,9 +573,10 @@ GEMM_F32_API int gemm_f32_vocab_score_grad(
     void *dW, int64_t lddw, void *workspace, int64_t workspace_bytes,
     gemm_f32_stream_t stream);
 
-/* Bytes of the kept logits of T tokens (no device call).  Minus a status on
- * error. */
-GEMM_F32_API int64_t gemm_f32_vocab_score_kept_size(int64_t T, int64_t V);
+/* Bytes of `kept` (no device call).  aligned = 1: W is 16-byte aligned and ldw
+ * a multiple of 8.  Minus a status on error. */
+GEMM_F32_API int64_t gemm_f32_vocab_score_kept_size(int64_t T, int64_t V,
+                                                    int64_t D, int aligned);
 
 /* Workspace bytes of the log probabilities (no device call): the forward call
  * (grad = 0; keep = 1: with `kept`) or the gradients (grad = 1; enough for the

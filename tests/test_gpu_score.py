@@ -369,6 +369,22 @@ def test_pieces_of_the_vocabulary(T):
     check_step(x, w, ids, a, b)
 
 
+def test_gradients_want_what_was_kept():
+    """Kept without a copy of w (its rows were aligned), gradients of the same
+    values in rows that are not are refused: their copy is not there."""
+    x, w, ids, a, b = case(70, 300, 64, BF16, 34)
+    off = matrix(300, 64, BF16, 1, 1.0, 3, 1)
+    off.copy_(w)
+    s = L.log_probs(x, w, ids, keep=True)
+    with pytest.raises(G.GemmError):
+        L.log_probs_grad(x, off, ids, s, a, b)
+    want = L.log_probs_grad(x, w, ids, s, a, b)
+    s = L.log_probs(x, off, ids, keep=True)  # the other way round nothing lacks
+    for wx in (off, w):
+        for p, q in zip(L.log_probs_grad(x, wx, ids, s, a, b), want):
+            assert torch.equal(p, q)
+
+
 def test_large_gradients_and_none():
     x, w, ids, a, b = case(200, 400, 40, F16, 18)
     for scale in (1e-30, 1e4):

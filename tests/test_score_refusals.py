@@ -83,9 +83,12 @@ def test_sizes(built_lib):  # noqa: F811
     lib = gemm.lib()
     size = lib.gemm_f32_vocab_score_workspace_size
     kept = lib.gemm_f32_vocab_score_kept_size
-    assert kept(4, 9) == 4 * 16 * 4 and kept(0, 5) == 0
-    assert kept(-1, 5) == -BAD and kept(4, 0) == -BAD
-    assert kept(2**31, 5) == -NO and kept(MOST, MOST) == -NO
+    assert kept(4, 9, 8, 1) == 4 * 16 * 4 and kept(0, 5, 8, 1) == 0
+    assert kept(5, 9, 8, 1) == 512  # (a copy of W would start behind it)
+    assert kept(4, 9, 9, 0) == 4 * 16 * 4 + 9 * 16 * 2  # with a copy of W
+    assert kept(-1, 5, 8, 1) == -BAD and kept(4, 0, 8, 1) == -BAD
+    assert kept(4, 5, 0, 1) == -BAD and kept(4, 5, 8, 2) == -BAD
+    assert kept(2**31, 5, 8, 1) == -NO and kept(MOST, MOST, 1, 1) == -NO
     for bad in ((-1, 8, 8, 0, 0, 0, 1), (4, 0, 8, 0, 0, 0, 1),
                 (4, 8, 0, 0, 0, 0, 1), (4, 8, 8, -1, 0, 0, 1),
                 (4, 8, 8, 9, 0, 0, 1), (4, 999, 8, 257, 0, 0, 1),
