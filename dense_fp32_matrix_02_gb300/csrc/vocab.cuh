@@ -174,6 +174,8 @@ struct VocabCall {
   long long slot_rows, ld_slot;
   float* dw_slots;    // [dw_max_splits · dw_slot_rows][ld_slot], or null
   int dw_slot_rows, dw_max_splits;
+  void* dWp;  // dW in rows that have a tensor map, where its own have none and
+              // there is room (ldxp apart); or null
 };
 
 // The products of a call (vocab_gemm.cu): its tensor maps, made once, and

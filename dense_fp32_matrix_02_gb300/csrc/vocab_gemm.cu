@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       const float inv_scale = header->inv_scale;
       const float grad_scale = p.tau * header->scale;
-      const bool dw_direct = !vocab_maps(p.dW, p.lddw);
+      const bool dw_direct = !p.dWp && !vocab_maps(p.dW, p.lddw);
       const int slot_rows = vocab_tiles(learnt) * kVocabTile;
       const int most = sum_steps(p, learnt);
       // dW's and dX's tiles, then the logits': a loop each, so that the sums
@@ -1189,9 +1189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((c0 & 32) == 0 && n + 32 < cols) continue;
             const int nb = n - (c0 & 32);
             if (!LOGITS && dw_direct) {
-              // rows on any 2-byte boundary: a warp writes 64 columns of one
-              // row at a time (an odd row in pairs shifted over the lanes
-              // instead of single columns: 100000 × 2045 455 us, 389 so)
+              // rows on any 2-byte boundary, and no room for them elsewhere: a
+              // warp writes 64 columns of one row at a time
               __syncwarp();
               const int rows = min(32, walk.back_n - m0);
               for (int k = 0; k < rows; ++k) {
@@ -1316,7 +1315,9 @@ bool make_maps(const VocabCall& p, bool grad, Maps* maps) {
     ok = ok && encode(&maps->dw_slots, t32, 4, p.dw_slots, p.D,
                       (long long)p.dw_slot_rows * p.dw_max_splits, p.ld_slot,
                       32);
-  if (vocab_maps(p.dW, p.lddw))
+  if (p.dWp)
+    ok = ok && encode(&maps->dw, t16, 2, p.dWp, p.D, p.V, p.ldxp, 32);
+  else if (vocab_maps(p.dW, p.lddw))
     ok = ok && encode(&maps->dw, t16, 2, p.dW, p.D, p.V, p.lddw, 32);
   return ok;
 }

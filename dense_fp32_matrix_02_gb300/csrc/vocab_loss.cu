@@ -224,6 +224,76 @@ __device__ __forceinline__ void pack_long_rows(
   }
 }
 
+// dW's rows to where they belong, on any 2-byte boundary: the other way round.
+// A warp writes a row in aligned 16-byte pieces, each from its lane's chunk and
+// the one before; a piece that lies partly outside the row as single elements.
+// (Written by the products' epilogue instead, two or four bytes a lane, dW of
+// 100000 × 2045 took 390 us, 280 in rows that have a tensor map and from there.)
+__global__ void __launch_bounds__(1024)
+    unpack_dw_kernel(const __grid_constant__ VocabCall p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (p.header->dw_splits > 1) return;  // (finish_grad_kernel has written it)
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31, n = p.D, chunks = (n + 7) / 8;
+  const long long extent = 2 * ((p.V - 1) * p.lddw + n);
+  for (long long r = blockIdx.x * 32ll + (threadIdx.x >> 5); r < p.V;
+       r += gridDim.x * 32ll) {
+    const uint4* from = reinterpret_cast<const uint4*>(
+        static_cast<const uint16_t*>(p.dWp) + r * p.ldxp);
+    uint16_t* row = static_cast<uint16_t*>(p.dW) + r * p.lddw;
+    const int off = (reinterpret_cast<uintptr_t>(row) & 15u) >> 1;
+    const int start = (8 - off) & 7;  // in the chunk before
+    const bool two = start & 4, one = start & 2;
+    const int bits = (start & 1) * 16;
+    const int pieces = (n + off + 7) / 8;
+    for (int j0 = 0; j0 < pieces; j0 += 32 * kAhead) {
+      uint4 v[kAhead], first[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int j = j0 + 32 * a + lane;
+        v[a] = first[a] = make_uint4(0, 0, 0, 0);
+        if (j < chunks) v[a] = from[j];
+        if (lane == 0 && j > 0 && j - 1 < chunks) first[a] = from[j - 1];
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int j = j0 + 32 * a + lane, e = 8 * j - off;
+        uint4 b;
+        b.x = __shfl_up_sync(0xffffffffu, v[a].x, 1);
+        b.y = __shfl_up_sync(0xffffffffu, v[a].y, 1);
+        b.z = __shfl_up_sync(0xffffffffu, v[a].z, 1);
+        b.w = __shfl_up_sync(0xffffffffu, v[a].w, 1);
+        if (lane == 0) b = first[a];
+        const uint32_t in[8] = {b.x,    b.y,    b.z,    b.w,
+                                v[a].x, v[a].y, v[a].z, v[a].w};
+        uint32_t s[6], w[5];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) s[i] = two ? in[i + 2] : in[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = one ? s[i + 1] : s[i];
+        uint4 o = make_uint4(__funnelshift_r(w[0], w[1], bits),
+                             __funnelshift_r(w[1], w[2], bits),
+                             __funnelshift_r(w[2], w[3], bits),
+                             __funnelshift_r(w[3], w[4], bits));
+        if (off == 0) o = v[a];
+        if (j >= pieces) continue;
+        if (e >= 0 && e + 8 <= n) {
+          if (span_ok(row + e, 16, p.dW, extent, p.status))
+            *reinterpret_cast<uint4*>(row + e) = o;
+          continue;
+        }
+        const uint32_t q[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e + i >= 0 && e + i < n &&
+              span_ok(row + e + i, 2, p.dW, extent, p.status))
+            row[e + i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
+      }
+    }
+  }
+}
+
 // A tile's time in 64-deep steps: its own, or its epilogue's where that is
 // longer (about eight steps: 8 warps make 128 × 256 outputs per CTA).
 __device__ __forceinline__ int tile_cost(int steps) {
@@ -690,10 +760,14 @@ int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // Places a call's state in its workspace (c.token .. c.dw_max_splits), from
 // T, V, D, top and what follows them alone; returns its bytes.  The pointers
 // are offsets from `ws` and only numbers where it is null.  alternatives: of
-// log probabilities (-1: of a loss), whose logits are kept or not.
+// log probabilities (-1: of a loss), whose logits are kept or not.  aligned: W
+// has a tensor map (else there is room for its packed copy, unless that is kept).
 int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
-                int64_t top, bool grad, bool pack_w, int64_t alternatives = -1,
+                int64_t top, bool grad, bool aligned, int64_t alternatives = -1,
                 bool keep = false) {
+  const bool pack_w = !aligned && !keep;
+  // dW of such a width, one row behind the other, has no tensor map either
+  const bool odd_rows = !aligned && D % 8 != 0;
   // A piece's G: small enough that it and its part of W stay near the L2
   // they are read from again (1800 learnt tokens of 6000, 65537 × 2048: 32,
   // 64, 128, 256 MB 1560, 1400, 1350, 1500 us a step), large enough that a
@@ -791,6 +865,11 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
                 kMostDwSlots / (c->dw_slot_rows * c->ld_slot * 4)}));
   if (c->dw_max_splits > 1)
     take(&c->dw_slots, c->dw_max_splits * c->dw_slot_rows * c->ld_slot * 4);
+  c->dWp = nullptr;
+  if (odd_rows) {
+    take(&bytes, V * c->ldxp * 2);
+    c->dWp = bytes;
+  }
   return at;
 }
 
@@ -972,13 +1051,18 @@ cudaError_t run_gradients(const VocabCall& c, int sms, const WaitCfg& wc,
   using Bf16 = __nv_bfloat16;
   const bool bf16 = c.type == GEMM_F32_MIXED_BF16;
   if (c.T <= kVocabFewTokens)
-    return bf16 ? launch(finish_grad_kernel<Bf16, 12, 2>)
-                : launch(finish_grad_kernel<__half, 12, 2>);
-  if (c.T <= kVocabTile)
-    return bf16 ? launch(finish_grad_kernel<Bf16, 16, 1>)
-                : launch(finish_grad_kernel<__half, 16, 1>);
-  return bf16 ? launch(finish_grad_kernel<Bf16, 4, 1>)
-              : launch(finish_grad_kernel<__half, 4, 1>);
+    e = bf16 ? launch(finish_grad_kernel<Bf16, 12, 2>)
+             : launch(finish_grad_kernel<__half, 12, 2>);
+  else if (c.T <= kVocabTile)
+    e = bf16 ? launch(finish_grad_kernel<Bf16, 16, 1>)
+             : launch(finish_grad_kernel<__half, 16, 1>);
+  else
+    e = bf16 ? launch(finish_grad_kernel<Bf16, 4, 1>)
+             : launch(finish_grad_kernel<__half, 4, 1>);
+  if (e != cudaSuccess || !c.dWp) return e;
+  return launch_pdl(unpack_dw_kernel,
+                    dim3((unsigned)std::min<int64_t>(2 * sms, (c.V + 31) / 32)),
+                    dim3(1024), 0, stream, c);
 }
 
 int run(const Request& r) {
@@ -988,8 +1072,8 @@ int run(const Request& r) {
   VocabCall c = {};
   const int64_t need =
       lay_out(&c, static_cast<char*>(r.ws), r.T, r.V, r.D, r.top, r.grad,
-              !vocab_maps(r.W, r.ldw) && !r.kept,
-              r.score ? r.alternatives : -1, r.kept != nullptr);
+              vocab_maps(r.W, r.ldw), r.score ? r.alternatives : -1,
+              r.kept != nullptr);
   if (!r.ws || (reinterpret_cast<uintptr_t>(r.ws) & 15u) != 0 ||
       r.ws_bytes < need)
     return GEMM_F32_ERR_INVALID_ARG;
@@ -1033,6 +1117,7 @@ int run(const Request& r) {
   c.alternatives = (int)r.alternatives;
   c.entropy = r.entropy, c.grad_entropy = r.grad_entropy;
   c.entropy_stride = r.entropy_stride;
+  if (vocab_maps(r.dW, r.lddw)) c.dWp = nullptr;
   c.pairs = vocab_pairs(sms);
   c.status = wc.status;
   c.wide = c.pieces > 1 ? kVocabTile
@@ -1183,10 +1268,10 @@ int64_t gemm_f32_vocab_score_workspace_size(int64_t T, int64_t V, int64_t D,
   if (!countable(T, V, D)) return -GEMM_F32_ERR_UNSUPPORTED;
   VocabCall c = {};
   int64_t n =
-      lay_out(&c, nullptr, T, V, D, 1, false, aligned == 0 && !keep, top,
-              keep != 0);
+      lay_out(&c, nullptr, T, V, D, 1, false, aligned != 0, top, keep != 0);
   if (grad)  // (room for either call; W's copy is in `kept`)
-    n = std::max(n, lay_out(&c, nullptr, T, V, D, 1, true, false, 0));
+    n = std::max(n,
+                 lay_out(&c, nullptr, T, V, D, 1, true, aligned != 0, 0, true));
   return n;
 }
 
@@ -1197,9 +1282,9 @@ int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V, int64_t D,
     return -GEMM_F32_ERR_INVALID_ARG;
   if (!countable(T, V, D)) return -GEMM_F32_ERR_UNSUPPORTED;
   VocabCall c = {};
-  int64_t n = lay_out(&c, nullptr, T, V, D, top, false, aligned == 0);
+  int64_t n = lay_out(&c, nullptr, T, V, D, top, false, aligned != 0);
   if (grad)  // (room for either call)
-    n = std::max(n, lay_out(&c, nullptr, T, V, D, top, true, aligned == 0));
+    n = std::max(n, lay_out(&c, nullptr, T, V, D, top, true, aligned != 0));
   return n;
 }
 
