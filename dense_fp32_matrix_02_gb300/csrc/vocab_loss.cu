@@ -227,8 +227,7 @@ __device__ __forceinline__ void pack_long_rows(
 // dW's rows to where they belong, on any 2-byte boundary: the other way round.
 // A warp writes a row in aligned 16-byte pieces, each from its lane's chunk and
 // the one before; a piece that lies partly outside the row as single elements.
-// (Written by the products' epilogue instead, two or four bytes a lane, dW of
-// 100000 × 2045 took 390 us, 280 in rows that have a tensor map and from there.)
+// (Written by the products' epilogue instead, two or four bytes a lane: lay_out.)
 __global__ void __launch_bounds__(1024)
     unpack_dw_kernel(const __grid_constant__ VocabCall p) {
   griddep_wait();
@@ -766,8 +765,14 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
                 int64_t top, bool grad, bool aligned, int64_t alternatives = -1,
                 bool keep = false) {
   const bool pack_w = !aligned && !keep;
-  // dW of such a width, one row behind the other, has no tensor map either
-  const bool odd_rows = !aligned && D % 8 != 0;
+  // dW of such a width, one row behind the other, has no tensor map either.  One
+  // row of tiles waits for memory: it writes dW in rows that have one, which
+  // are then moved (a step of 16 × 50000 × 2045 305 us, 339 without; 256 tokens
+  // 348 and 372).  Short rows cost the move more (16 × 50000 × 201 106 us, 101
+  // without), and more tokens' products hide what the epilogue takes (600 ×
+  // 50000 × 1001 320 us, 311 without).
+  const bool odd_rows =
+      !aligned && D % 8 != 0 && D >= 256 && T <= kVocabTile;
   // A piece's G: small enough that it and its part of W stay near the L2
   // they are read from again (1800 learnt tokens of 6000, 65537 × 2048: 32,
   // 64, 128, 256 MB 1560, 1400, 1350, 1500 us a step), large enough that a
