@@ -509,6 +509,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int k = min(p.alternatives + kSpare, p.V);
   const float* z = p.logits + (long long)blockIdx.x * p.ld_logits;
   if (tid == 0) s_stretches = s_count = 0;
+  // (where the products gave up, maxima and logits need not belong together, and
+  // fewer than k elements may reach the bound: no id is ever left as it was)
+  for (int c = tid; c < k; c += THREADS) s_id[c] = 0;
 
   // the statistics, and the stretches' maxima
   const bool held = parts <= kHeldKeys;

@@ -361,6 +361,43 @@ def test_logits_of_some_tokens_at_a_time(T):
         assert torch.equal(got["top_ids"], want["top_ids"])
 
 
+def test_kept_logits_past_32_bits():
+    """More kept logits than 2^31: the gradients of the last words and of the
+    last tokens, from the definition."""
+    T, V, D = 520, (1 << 22) + 77, 16
+    x, w, ids, a, b = case(T, V, D, BF16, 35)
+    ids[-8:] = torch.arange(V - 8, V, device=DEV)
+    s = L.log_probs(x, w, ids, keep=True)
+    dx, dw = L.log_probs_grad(x, w, ids, s, a, b)
+    lse, H = s.lse.double(), s.entropy.double()
+
+    def grads(rows, words):
+        log_p = x[rows].double() @ w[words].double().t() - lse[rows][:, None]
+        g = -log_p.exp() * (a[rows].double()[:, None] + b[rows].double()[:, None]
+                            * (log_p + H[rows][:, None]))
+        hit = ids[rows][:, None] == torch.arange(V, device=DEV)[words]
+        return g + hit * a[rows].double()[:, None]
+
+    u = 2.0 ** -8  # G's rounding and the result's; p's own error, 1e-4
+    every, last = slice(0, T), slice(V - 300, V)
+    g = grads(every, last)
+    want = g.t() @ x.double()
+    tol = (u + 1e-4) * (g.abs().t() @ x.double().abs()) + u * want.abs()
+    assert bool(((dw[last].double() - want).abs() <= tol).all())
+    rows = slice(T - 4, T)
+    want = torch.zeros(4, D, dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(want)
+    for v in range(0, V, 1 << 20):
+        g = grads(rows, slice(v, min(V, v + (1 << 20))))
+        wv = w[v:v + (1 << 20)].double()
+        want += g @ wv
+        size += g.abs() @ wv.abs()
+    tol = (u + 1e-4) * size + u * want.abs()
+    assert bool(((dx[rows].double() - want).abs() <= tol).all())
+    torch.cuda.synchronize()
+    assert G.device_status() == 0
+
+
 @pytest.mark.parametrize("T", [30, 600])
 def test_pieces_of_the_vocabulary(T):
     """Gradients in several pieces of G (128 MB each)."""
@@ -564,6 +601,39 @@ def test_other_device_is_refused_or_used():
         L.log_probs_grad(x, w, ids, s, a.cpu())
     with pytest.raises(ValueError, match="device"):
         L.log_probs_grad(x, w, ids, s._replace(kept=s.kept.cpu()), a)
+
+
+def test_waits_that_run_out():
+    """Products whose operands never come give up, report it and leave the
+    device usable; what follows them works on whatever the workspace holds, here
+    words' maxima that belong to no logits."""
+    x, w, ids, a, b = case(300, 40000, 128, BF16, 36, 0.1)
+    want = L.log_probs(x, w, ids, top=20, keep=True)
+    grads = L.log_probs_grad(x, w, ids, want, a, b)
+    torch.cuda.synchronize()
+    n = L.score_workspace_size(300, 40000, 128, 20, False, False)
+    gen = torch.Generator(device=DEV).manual_seed(37)
+    old = G.set_wait_timeout_ns(20_000_000)
+    G.set_debug_flags(G.DEBUG_STALL_PRODUCER)
+    try:
+        for _ in range(2):
+            ws = torch.randint(0, 256, (n,), generator=gen, device=DEV,
+                               dtype=torch.uint8)
+            s = L.log_probs(x, w, ids, top=20, workspace=ws)
+            torch.cuda.synchronize()
+            assert G.device_status() == 4
+            assert bool(((s.top_ids >= -1) & (s.top_ids < 40000)).all())
+        L.log_probs_grad(x, w, ids, want, a, b)
+        torch.cuda.synchronize()
+        assert G.device_status() == 4
+    finally:
+        G.set_debug_flags(0)
+        G.set_wait_timeout_ns(old)
+    s = L.log_probs(x, w, ids, top=20, keep=True)
+    got = L.log_probs_grad(x, w, ids, s, a, b)
+    for p, q in zip((*s[:5], *got), (*want[:5], *grads)):
+        assert torch.equal(p, q)
+    assert G.device_status() == 0
 
 
 def test_two_streams_at_once():
