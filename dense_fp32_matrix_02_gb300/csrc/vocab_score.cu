@@ -29,6 +29,7 @@
 // the logits again would cost 2·D operations an element instead.
 #include <algorithm>
 
+#include "bound_search.h"
 #include "gemm_f32.h"
 #include "kernels.h"
 #include "vocab.cuh"
@@ -208,26 +209,22 @@ __device__ __forceinline__ uint32_t kth_largest(SelectState& s, int n, int k,
   return prefix;
 }
 
-// A bound that at least k of n >= k keys in [low, high] reach, and not many
-// more: the range in 256 steps, and the step with the k-th largest in 256
-// again while it holds many.  (Keys of one row mostly differ in their last 24
-// bits: a histogram of the first 8 would have one bin, and every atomic on it
-// in turn.)
+// A bound that at least k of n >= k keys from low on reach, and not many more
+// (bound_search.h).  (Keys of one row mostly differ in their last 24 bits: a
+// histogram of the first 8 would have one bin, and every atomic on it in turn.)
 template <int THREADS, typename Key>
 __device__ __forceinline__ uint32_t reached_by(SelectState& s, int n, int k,
                                                uint32_t low, uint32_t high,
                                                Key key) {
   constexpr int kEnough = 32;
   const int tid = threadIdx.x;
-  for (;;) {
-    const int shift = max(0, 24 - __clz(high - low));
-    for (int b = tid; b < 256; b += THREADS) s.hist[b] = 0;
+  auto count = [&](uint32_t low, uint32_t high, int shift, int& in_step) {
+    for (int b = tid; b < kBoundBins; b += THREADS) s.hist[b] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int i = tid; i < n; i += THREADS) {
       const uint32_t x = key(i);
-      // (what is above the range is in the last bin)
-      if (x >= low) atomicAdd(&s.hist[min((x - low) >> shift, 255u)], 1);
+      if (x >= low) atomicAdd(&s.hist[bound_bin(x, low, high, shift)], 1);
     }
     __syncthreads();
     if (tid < 32) {  // 8 bins a lane, the largest first
@@ -249,12 +246,12 @@ __device__ __forceinline__ uint32_t reached_by(SelectState& s, int n, int k,
       }
     }
     __syncthreads();
-    const uint32_t step = low + ((uint32_t)s.digit << shift);
-    if (s.left <= kEnough || shift == 0) return step;
-    low = step;
-    high = min(high, step + (1u << shift) - 1u);
+    in_step = s.left;
+    const int digit = s.digit;
     __syncthreads();
-  }
+    return digit;
+  };
+  return bound_search(low, high, kEnough, count);
 }
 
 // put(place, i) for the keys above `least` and the first `equal` of those
