@@ -462,8 +462,12 @@ __device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
 #pragma unroll 4
     for (int o = 0; o < k; ++o) {
       const float2 w = value[o];
+      // (an id twice, where the products gave up: by its place, so that every
+      // rank is some word's and every result is written)
       rank += w.x > v.x ||
-              (w.x == v.x && (w.y > v.y || (w.y == v.y && ids[o] < id)));
+              (w.x == v.x &&
+               (w.y > v.y ||
+                (w.y == v.y && (ids[o] < id || (ids[o] == id && o < c)))));
     }
     if (rank < p.alternatives) {
       p.top_out[t * p.alternatives + rank] = id;
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const float* z = p.logits + (long long)blockIdx.x * p.ld_logits;
   if (tid == 0) s_stretches = s_count = 0;
   // (where the products gave up, maxima and logits need not belong together, and
-  // fewer than k elements may reach the bound: no id is ever left as it was)
+  // fewer than k elements may reach the bound: what is missing is word 0)
   for (int c = tid; c < k; c += THREADS) s_id[c] = 0;
 
   // the statistics, and the stretches' maxima

@@ -61,3 +61,35 @@ def test_maxima_of_other_logits(stalled, T, V, top):
         torch.cuda.synchronize()
         assert G.device_status() == 4
         assert bool(((s.top_ids >= -1) & (s.top_ids < V)).all())
+
+
+def scores_into(x, w, ids, top, workspace, fill):
+    """The C call on outputs that hold `fill` before it: (top_logp, top_ids)."""
+    T = x.shape[0]
+    head, _ = L._operands(x, w)
+    out = torch.full((3, T), fill, device=DEV)
+    logp = torch.full((T, top), fill, device=DEV)
+    words = torch.full((T, top), int(fill), dtype=torch.int64, device=DEV)
+    st = G.lib().gemm_f32_vocab_score(
+        *head, ids.data_ptr(), 1.0, top, *(row.data_ptr() for row in out),
+        logp.data_ptr(), words.data_ptr(), None, 0, workspace.data_ptr(),
+        workspace.numel(), torch.cuda.current_stream().cuda_stream or None)
+    assert st == 0
+    torch.cuda.synchronize()
+    return logp, words
+
+
+@pytest.mark.parametrize("T,V,top", [(300, 40000, 20), (300, 40000, 256),
+                                     (3, 20000, 20), (70, 3000, 120)])
+def test_every_word_is_written_where_the_products_gave_up(stalled, T, V, top):
+    """Maxima that no logit reaches: no word is found, and none of the outputs
+    is left as it was."""
+    x, w, ids = operands(T, V, 64, BF16, T + V)
+    n = L.score_workspace_size(T, V, 64, top)
+    logits = (4 * T * ((V + 7) // 8 * 8) + 255) // 256 * 256
+    ws = torch.full((n // 4,), 3.0, device=DEV)
+    ws[-(logits // 4):] = -1.0
+    logp, words = scores_into(x, w, ids, top, ws.view(torch.uint8), -7777.0)
+    assert G.device_status() == 4
+    assert bool(((words >= 0) & (words < V)).all())
+    assert not bool((logp == -7777.0).any())
