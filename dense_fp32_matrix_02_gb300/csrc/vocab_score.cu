@@ -19,7 +19,10 @@
 //   The rank of two logits should not hang on how a sum rounds (on the tile it
 // was made in, so on the batch): the k + kSpare largest are computed again
 // from the operands, products exact in fp32, summed in pairs of fp32 (48
-// bits), and ranked by that.
+// bits), and ranked by that.  A word that is not among them can only belong to
+// the first k if its fp32 logit lies within its own error of the k-th exact
+// one; where there may be such words (a row in some million: 8 ranks lie far
+// further apart) all of them are computed again.
 //
 // Gradients.  G = (a·([v = y] − p) − b·p·(log p + H))/τ from the kept logits,
 // 4 bytes read and 2 written an element, a piece of the vocabulary at a time,
@@ -153,6 +156,14 @@ __global__ void __launch_bounds__(kFinishThreads)
 // ------------------------------------------------------- likeliest words
 constexpr int kSpare = 8;  // ranked beyond those asked for
 constexpr int kMostRanked = kVocabMaxTop + kSpare;
+// What an fp32 logit may be off by, times the sum of its terms' magnitudes: 32
+// additions (kind::f16 takes 16 products each, 8 steps of 64 are a sum) short
+// of four last places, 2^-21, each, and half a last place, 2^-24, for each sum
+// of 512 that is added.  Doubled, as the sum is that of some of the largest
+// words, not of all.
+__device__ __forceinline__ float logit_error(int D) {
+  return 0x1p-15f + 0x1p-32f * (float)D;
+}
 constexpr int kStretches = 512;    // read at most, but for equal maxima
 constexpr int kCandidates = 1024;  // ranked at most, but for equal logits
 constexpr int kHeldKeys = 2048;
@@ -303,6 +314,11 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
   asm("sub.rn.f32x2 %0, %1, %2;\n" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t v;
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(v) : "l"(a), "l"(b), "l"(c));
@@ -353,23 +369,35 @@ struct ExactSum {
     }
   }
 };
+// size + |x·w|
+template <int AB_TYPE>
+__device__ __forceinline__ uint64_t add_sizes(uint64_t size, uint4 x, uint4 w) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    size = add2(size, mul2(widen<AB_TYPE>(xs[j]), widen<AB_TYPE>(ws[j])) &
+                          0x7fffffff7fffffffull);
+  return size;
+}
 __device__ __forceinline__ float2 across(float2 v, int o) {
   return make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
                      __shfl_xor_sync(0xffffffffu, v.y, o));
 }
 
 // WORDS rows of W at a time, AHEAD loads of each side by side (a row of W comes
-// from far).
+// from far).  measure: with this lane's part of Σ |x·w| of the first.
 template <int AB_TYPE, int WORDS, int AHEAD>
 __device__ __forceinline__ void exact_dots(const uint16_t* x,
                                            const uint16_t* const (&w)[WORDS],
                                            int n, int lane,
-                                           float2 (&v)[WORDS]) {
+                                           float2 (&v)[WORDS], bool measure,
+                                           float& size) {
   bool even = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
 #pragma unroll
   for (int i = 0; i < WORDS; ++i)
     even = even && (reinterpret_cast<uintptr_t>(w[i]) & 15u) == 0;
   ExactSum sum[WORDS];
+  uint64_t sizes = 0;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int whole = even ? n & ~7 : 0;
 #pragma unroll 1
@@ -390,14 +418,18 @@ __device__ __forceinline__ void exact_dots(const uint16_t* x,
           at < whole ? *reinterpret_cast<const uint4*>(x + at) : zero;
 #pragma unroll
       for (int i = 0; i < WORDS; ++i) sum[i].template add<AB_TYPE>(a, b[i][j]);
+      if (measure) sizes = add_sizes<AB_TYPE>(sizes, a, b[0][j]);
     }
   }
 #pragma unroll 1
   for (int c = whole + 8 * lane; c < n; c += 256) {
     const uint4 a = read_8(x, c, n, false);
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      sum[i].template add<AB_TYPE>(a, read_8(w[i], c, n, false));
+    for (int i = 0; i < WORDS; ++i) {
+      const uint4 b = read_8(w[i], c, n, false);
+      sum[i].template add<AB_TYPE>(a, b);
+      if (i == 0 && measure) sizes = add_sizes<AB_TYPE>(sizes, a, b);
+    }
   }
 #pragma unroll
   for (int i = 0; i < WORDS; ++i) {
@@ -406,6 +438,10 @@ __device__ __forceinline__ void exact_dots(const uint16_t* x,
     v[i] = add_exactly(
         add_exactly(two_sum(h0.x, l0.x), two_sum(h0.y, l0.y)),
         add_exactly(two_sum(h1.x, l1.x), two_sum(h1.y, l1.y)));
+  }
+  if (measure) {  // (an infinite or missing logit has no error)
+    const float2 m = apart(sizes);
+    if (m.x + m.y < INFINITY) size = m.x + m.y;
   }
   // Halves of the lanes sum halves of the words, down to one: v[0] is that of
   // word lane / (32 / WORDS).
@@ -427,14 +463,16 @@ template <int AB_TYPE, int WORDS, int AHEAD>
 __device__ __forceinline__ void exact_logits(const VocabCall& p, long long t,
                                              const float* z, const int* ids,
                                              int c0, int k, int lane,
-                                             float2* value) {
+                                             float2* value, bool measure,
+                                             float& size) {
   const uint16_t* w[WORDS];
   float2 v[WORDS];
 #pragma unroll
   for (int i = 0; i < WORDS; ++i)  // (past the end, the last again)
     w[i] = static_cast<const uint16_t*>(p.W) + ids[min(c0 + i, k - 1)] * p.ldw;
   exact_dots<AB_TYPE, WORDS, AHEAD>(
-      static_cast<const uint16_t*>(p.X) + t * p.ldx, w, p.D, lane, v);
+      static_cast<const uint16_t*>(p.X) + t * p.ldx, w, p.D, lane, v, measure,
+      size);
   const int c = c0 + lane / (32 / WORDS);
   if (lane % (32 / WORDS) == 0 && c < k) {
     // (an infinity has no remainder; a NaN is ranked last)
@@ -485,11 +523,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   __shared__ SelectState s;
   __shared__ Stat s_stat[kWarps];
   __shared__ uint2 s_range[kWarps];
-  __shared__ uint32_t s_key[kHeldKeys];  // of the stretches, then candidates
+  // of the stretches, then candidates; then the values of many candidates
+  __shared__ __align__(16) uint32_t s_key[kHeldKeys];
   __shared__ int s_stretch[kStretches], s_id[kMostRanked];
   __shared__ int s_candidate[kCandidates], s_stretches, s_count;
+  __shared__ uint32_t s_last, s_size;
   __shared__ float2 s_value[kMostRanked];
-  static_assert(kCandidates <= kHeldKeys, "candidates' keys");
+  static_assert(2 * kCandidates <= kHeldKeys, "candidates' values");
   griddep_wait();
   griddep_launch_dependents();
   const int learnt = p.header ? p.header->learnt : p.T;
@@ -509,7 +549,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int parts = (int)((2ll * p.V + wide - 1) / wide);
   const int k = min(p.alternatives + kSpare, p.V);
   const float* z = p.logits + (long long)blockIdx.x * p.ld_logits;
-  if (tid == 0) s_stretches = s_count = 0;
+  if (tid == 0) {
+    s_stretches = s_count = 0;
+    s_last = s_size = 0;
+  }
   // (where the products gave up, maxima and logits need not belong together, and
   // fewer than k elements may reach the bound: what is missing is word 0)
   for (int c = tid; c < k; c += THREADS) s_id[c] = 0;
@@ -561,6 +604,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       s_key[at] = x;
       s_candidate[at] = v;
     }
+  };
+  auto largest = [&](int g) {  // (where what is held of them is gone)
+    return order_of(p.sums[(long long)r * parts + g].w);
   };
   // A bound that k elements reach: one that k maxima reach, or elements where
   // there are fewer stretches.  Little more than k reach it, unless many are
@@ -632,14 +678,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       for (int o = 0; o < count; ++o)
         rank += s_key[o] > x || (s_key[o] == x && s_candidate[o] < id);
       if (rank < k) s_id[rank] = id;
+      if (rank == k - 1) s_last = x;
     }
   } else {
     // Many are equal: the k first stretches, in order, and of their elements
     // the k first.
     int stretches = parts, equal;
-    auto largest = [&](int g) {  // (what is held of them is gone)
-      return order_of(p.sums[(long long)r * parts + g].w);
-    };
     __syncthreads();
     if (parts > k) {
       stretches = k;
@@ -659,6 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     const uint32_t least = kth_largest<THREADS>(s, n, k, element, equal);
     in_order<THREADS>(s, n, k, least, equal, element,
                       [&](int at, int i) { s_id[at] = column(i); });
+    if (tid == 0) s_last = least;
   }
   __syncthreads();
 
@@ -666,11 +711,58 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   // (many rows: two words a warp, which share x; few: one, with more of it
   // side by side)
   constexpr int kWords = THREADS == 1024 ? 1 : 2;
-  for (int c0 = warp * kWords; c0 < k; c0 += kWarps * kWords)
-    exact_logits<AB_TYPE, kWords, kWords == 1 ? 4 : 2>(p, t, z, s_id, c0, k,
-                                                       lane, s_value);
-  __syncthreads();
-  write_ranked<THREADS>(p, t, z, s_id, s_value, k, tid, st.m, log_sum);
+  constexpr int kAhead = kWords == 1 ? 4 : 2;
+  const int* ids = s_id;
+  float2* values = s_value;
+  int n = k;
+  float size = 0.f;
+  for (bool first = true;; first = false) {
+    // (of a warp's first word the sum of its terms' magnitudes too: of all words
+    // it took 22 us more, 1024 tokens, 100000 × 2048, 64 words; this and what
+    // follows 8 us of 405, and 3 to 6 of 255, 4096 tokens, 32000 × 768, 5 words)
+#pragma unroll 1
+    for (int c0 = warp * kWords; c0 < n; c0 += kWarps * kWords)
+      exact_logits<AB_TYPE, kWords, kAhead>(
+          p, t, z, ids, c0, n, lane, values, first && c0 < kWarps * kWords,
+          size);
+    if (!first) {
+      __syncthreads();
+      break;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
+    if (lane == 0) atomicMax(&s_size, __float_as_uint(size));  // (size >= 0)
+    __syncthreads();
+
+    // Words of smaller logits than all of these, but not by more than those may
+    // be off: every word that may belong to the first is ranked.
+    uint32_t lowest = 0xffffffffu;
+    for (int c = lane; c < p.alternatives; c += 32)
+      lowest = min(lowest, order_of(s_value[c].x));
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+    const float error = logit_error(p.D) * __uint_as_float(s_size);
+    const uint32_t need = order_of(reference_of(lowest) - error);
+    if (k == p.V || !(error > 0.f) || lowest == kLowest || need > s_last) break;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    for (int g = warp; g < parts; g += kWarps) {
+      if (largest(g) < need) continue;
+#pragma unroll 1
+      for (int i = lane; i < half; i += 32) {
+        const int v = (g << bits) + i;
+        const uint32_t x = logit(v);
+        if (x >= need) candidate(v, x);
+      }
+    }
+    __syncthreads();
+    const int count = s_count;
+    if (count < p.alternatives || count > kCandidates) break;
+    __syncthreads();  // (the keys make room for the values)
+    n = count;
+    ids = s_candidate;
+    values = reinterpret_cast<float2*>(s_key);
+  }
+  write_ranked<THREADS>(p, t, z, ids, values, n, tid, st.m, log_sum);
 }
 
 // ------------------------------------------------------------- gradients

@@ -528,8 +528,12 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  * and for top > 0 the `top` words of the largest logits, largest first, equal
  * ones by the lower id: top_ids[t·top + j] and their log probabilities
  * top_logp[t·top + j].  They are ranked by Σ_k X·W as the operands give it (to
- * 2^-46 of the sum's terms) among the top + 8 largest of the fp32 logits, so
- * that the rank does not hang on how a sum rounds; the log probabilities are
+ * 2^-46 of the sum's terms), so that neither the words nor their rank hang on
+ * how a sum rounds: among the top + 8 largest of the fp32 logits and, where
+ * smaller ones lie within (2^-15 + 2^-32·D)·Σ_k |X·W| of the top-th of these
+ * (the sum of some of the largest words; an fp32 logit is off by half of that at
+ * most), among all that do.  Beyond 1024 of them, among the first top + 8 by
+ * fp32 logit and id.  The log probabilities are
  * those of the fp32 logits, the given word's to the bit (two that differ by
  * less than these round may stand the other way round).  A logit that is NaN
  * ranks last.  0 <= top <= min(256, V); top_logp and top_ids may

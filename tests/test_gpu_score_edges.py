@@ -93,3 +93,61 @@ def test_every_word_is_written_where_the_products_gave_up(stalled, T, V, top):
     assert G.device_status() == 4
     assert bool(((words >= 0) & (words < V)).all())
     assert not bool((logp == -7777.0).any())
+
+
+def close_words(V, D, n, dtype, seed):
+    """x of ones, and n words at random ids whose logits differ by multiples of
+    2^-17 around 40: pairs of terms that cancel out, of sizes from 2^-6 to 2^7
+    (bfloat16: 2^-9 to 2^10), so that sums in 32 bits are off by more than that
+    (a partial sum of 500 or more has a last place of 2^-15 or more).  All
+    other logits are below 20."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def rand(*shape):
+        return torch.rand(*shape, generator=gen, device=DEV)
+
+    w = (torch.randn(V, D, generator=gen, device=DEV) * 2 / D ** 0.5).to(dtype)
+    at = torch.argsort(rand(V))[:n]
+    half = (D - 2) // 2
+    e = 6 if dtype == F16 else 9
+    r = ((rand(n, half) + 1) * 2.0 ** torch.randint(
+        -e, e + 1, (n, half), generator=gen, device=DEV)).to(dtype)
+    pairs = torch.cat([r, -r], 1)
+    rows = torch.zeros(n, D, dtype=dtype, device=DEV)
+    rows[:, 2:2 + 2 * half] = pairs.gather(1, torch.argsort(rand(n, 2 * half), 1))
+    rows[:, 0] = 40.0
+    rows[:, 1] = torch.arange(n, device=DEV) * 2.0 ** -17
+    w[at] = rows
+    return torch.ones(1, D, dtype=dtype, device=DEV), w
+
+
+@TYPES
+@pytest.mark.parametrize("V,D,n,top", [
+    (5000, 1024, 60, 5), (5000, 1024, 40, 20), (40000, 1024, 200, 1),
+    (40000, 2048, 250, 64), (3000, 1000, 250, 200), (900, 520, 120, 10),
+    (5000, 1001, 60, 5)])
+def test_rank_of_many_words_that_rounding_would_exchange(V, D, n, top, dtype):
+    """More words than are looked at beyond `top` lie within what a sum in 32
+    bits may be off: the words are those of the operands all the same, and of
+    batches of one token, a few tiles and many the same."""
+    x, w = close_words(V, D, n, dtype, V + n)
+    z = x.double() @ w.double().t()
+    want = z.sort(dim=1, descending=True, stable=True).indices[:, :top]
+    for T in (1, 200, 300, 1500):  # (blocks of every size)
+        ids = torch.zeros(T, dtype=torch.int64, device=DEV)
+        s = L.log_probs(x.repeat(T, 1), w, ids, top=top)
+        assert torch.equal(s.top_ids, want.expand(T, top))
+    assert G.device_status() == 0
+
+
+def test_rank_among_the_first_words_is_not_enough():
+    """The search must go below its first bound: words whose logits in 32 bits
+    come out clearly lower than those of others, though theirs are larger."""
+    x, w = close_words(6000, 4096, 500, BF16, 3)
+    z = x.double() @ w.double().t()
+    for top in (1, 3, 30, 100):
+        want = z.sort(dim=1, descending=True, stable=True).indices[:, :top]
+        for T in (2, 200, 900):
+            ids = torch.zeros(T, dtype=torch.int64, device=DEV)
+            s = L.log_probs(x.repeat(T, 1), w, ids, top=top)
+            assert torch.equal(s.top_ids, want.expand(T, top))
