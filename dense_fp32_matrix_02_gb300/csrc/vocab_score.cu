@@ -19,7 +19,7 @@
 //   The rank of two logits should not hang on how a sum rounds (on the tile it
 // was made in, so on the batch): the k + kSpare largest are computed again
 // from the operands, products exact in fp32, summed in pairs of fp32 (48
-// bits), and ranked by that.  A word that is not among them can only belong to
+// bits as a rule; ExactSum has the bound), and ranked by that.  A word that is not among them can only belong to
 // the first k if its fp32 logit lies within its own error of the k-th exact
 // one; where there may be such words (a row in some million: 8 ranks lie far
 // further apart) all of them are computed again.
@@ -352,6 +352,13 @@ __device__ __forceinline__ uint64_t widen(uint32_t w) {
 // Σ x·w over a warp: a product of two 16-bit floats is exact in fp32; each
 // addition keeps what it rounds off, in a second sum.  (In fp64 this took
 // twice the time: two additions a clock and SM.)
+//   The second sum rounds too.  A lane has four pairs of sums, of n = D/128
+// products each.  The two terms that an addition leaves are 2^-23 of M = Σ |x·w|
+// each at most, so the j-th finds a second sum of at most j·2^-22·M, and adding
+// two to it rounds off j·2^-45·M: n²·2^-46 of M together, D²·2^-60 (4096 columns:
+// 2^-36).  That is if all errors have one sign and M is there from the first
+// product on; of random ones the second sum stays near 2^-24, 2^-46 together.
+// The seven joins of pairs and lanes leave 2^-46 of M each.
 struct ExactSum {
   uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
   template <int AB_TYPE>

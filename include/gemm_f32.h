@@ -527,8 +527,8 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  *   entropy_t = −Σ_v p·log p,  p = exp(z[t][v]/τ − lse_t)  (0·log 0 = 0),
  * and for top > 0 the `top` words of the largest logits, largest first, equal
  * ones by the lower id: top_ids[t·top + j] and their log probabilities
- * top_logp[t·top + j].  They are ranked by Σ_k X·W as the operands give it (to
- * 2^-46 of the sum's terms), so that neither the words nor their rank hang on
+ * top_logp[t·top + j].  They are ranked by Σ_k X·W as the operands give it (as
+ * a rule to 2^-46 of Σ_k |X·W|, at worst to 2^-43 + D²·2^-60 of it), so that neither the words nor their rank hang on
  * how a sum rounds: among the top + 8 largest of the fp32 logits and, where
  * smaller ones lie within (2^-15 + 2^-32·D)·Σ_k |X·W| of the top-th of these
  * (the sum of some of the largest words; an fp32 logit is off by half of that at
