@@ -284,19 +284,46 @@ __device__ __forceinline__ double sum_chunk(const Entry& e, long long chunk,
   return sum;
 }
 
+// min(1, max_norm / n) in two parts, hi rounded down, so that a product with it
+// rounds once (g·hi + g·lo, its sum in one step and of one sign: a zero keeps
+// its own).  A quotient below 2^-60 is kept in fp64: it may be below fp32's
+// smallest normal number.
+struct Factor {
+  float hi, lo;
+  double small;  // or 0
+  __device__ __forceinline__ bool one() const { return hi == 1.f; }
+};
+__device__ __forceinline__ Factor factor_of(double n, float max_norm) {
+  Factor f = {1.f, 0.f, 0.0};
+  if (!(n > (double)max_norm && n < INFINITY)) return f;
+  const double q = max_norm / n;
+  if (q < 0x1p-60) return Factor{0.f, 0.f, q};
+  // (what rounds to 1 moves no fp32 number by more than half a step)
+  if ((float)q == 1.f) return f;
+  f.hi = __double2float_rd(q);
+  f.lo = (float)(q - f.hi);
+  return f;
+}
+
 template <int TYPE>
 __device__ __forceinline__ void scale_chunk(const Entry& e, long long chunk,
-                                            int size, float factor,
+                                            int size, const Factor& factor,
                                             unsigned int* status) {
   const Chunk<TYPE> c(e, chunk, size);
   constexpr int N = Chunk<TYPE>::N;
   // factor 1: a copy, of NaN and infinities too
   auto scaled = [&](uint4 v) {
-    if (factor == 1.f) return v;
+    if (factor.one()) return v;
     float f[N];
     unpack<TYPE>(v, f);
+    if (factor.hi > 0.f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] *= factor;
+      for (int i = 0; i < N; ++i)
+        f[i] = fmaf(f[i], factor.hi, f[i] * factor.lo);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = (float)(f[i] * factor.small);
+    }
     return pack<TYPE>(f);
   };
   c.each(0, c.count, [&](const Place(&p)[kAhead]) {
@@ -362,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 int partials, float max_norm, float* norm) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float s_factor;
+  __shared__ Factor s_factor;
   if (threadIdx.x < 32) {
     double sum = 0.0;
 #pragma unroll 8
@@ -371,18 +398,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     if (threadIdx.x == 0) {
       const double n = sqrt(sum);
       if (norm && blockIdx.x == 0) *norm = (float)n;
-      s_factor = n > (double)max_norm && n < INFINITY ? (float)(max_norm / n)
-                                                      : 1.f;
+      s_factor = factor_of(n, max_norm);
     }
   }
   __syncthreads();
-  const float factor = s_factor;
+  const Factor factor = s_factor;
   const long long last = list.first[list.n] - 1;
 #pragma unroll 1
   for (long long i = blockIdx.x; i <= last; i += gridDim.x) {
     long long chunk = last - i;
     const Entry& e = list.entry[find(list, chunk)];
-    if (factor == 1.f && e.in == e.out && e.ld == e.ld_out) continue;
+    if (factor.one() && e.in == e.out && e.ld == e.ld_out) continue;
     if (e.type == GEMM_F32_GRAD_BF16)
       scale_chunk<GEMM_F32_GRAD_BF16>(e, chunk, list.chunk, factor,
                                       list.status);

@@ -614,10 +614,12 @@ typedef struct {
 /*
  * The global norm of n gradients, and clipping by it.
  *   norm = sqrt(Σ over every element of every gradient of g²),
- *   out  = g·min(1, max_norm / norm), rounded once to the gradient's type.
+ *   out  = g·min(1, max_norm / norm), rounded to fp32 (once, but for results
+ * below 2^-120, which are within a step) and from there to a 16-bit type.
  * `grads` is an array in host memory, read before the call returns; `norm`
- * is one float on the device.  A norm that is not finite (a NaN or an
- * infinity in a gradient) clips nothing: out is a copy, to the bit, as it is
+ * is one float on the device (infinity for a norm beyond fp32's range, which
+ * clips all the same).  A norm that is not finite (a NaN or an infinity in a
+ * gradient) clips nothing: out is a copy, to the bit, as it is
  * where norm <= max_norm; a gradient clipped in place is then not written.
  * max_norm is >= 0 (infinity: never clipped).  Squares are summed in fp32
  * over at most 128 elements, the sums in fp64, in a fixed order: the same
