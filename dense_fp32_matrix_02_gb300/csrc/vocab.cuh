@@ -160,8 +160,9 @@ struct VocabCall {
   float4* sums;    // in place of stats, [learnt][half tiles' columns]: (max,
                    // sum, Σ e·log2 e of its terms e, the largest logit)
   float* logits;   // [chunk][ld_logits]: the logits of the learnt tokens, of
-  long long ld_logits;  // all (kept for the gradients) or, for their largest,
-  int chunk, keep;      // of `chunk` in turn; or null
+  long long ld_logits;  // all (kept for the gradients, and behind each row its
+  int chunk, keep;      // reference and log S) or, for their largest, of
+                        // `chunk` in turn; or null
   // gradients
   int piece, pieces;  // columns of G; the pieces of the vocabulary
   float4* terms;      // log probabilities: what G needs of each learnt row
@@ -253,16 +254,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// The log probability of a logit z in a row of reference m and log S.
+__device__ __forceinline__ float vocab_log_prob(const VocabCall& p, float z,
+                                                float m, float log_sum) {
+  return fmaf(0.69314718056f, fmaf(z, p.inv_tau * 1.4426950408889634f, -m),
+              -log_sum);
+}
 // Log probabilities' G = (a·([v = y] − p) − b·p·(log p + H))/τ, of the kept
 // logits z: with t = z·c − lse·log2 e, c = log2 e / τ, p = 2^t,
 //   G = p·(A + B·t) + [v = y]·a,  A = −(a + b·H),  B = −b·ln 2
-// (a, b: times 1/τ and the scale of G).  Of a row: A, B, a, −lse·log2 e.
+// (a, b: times 1/τ and the scale of G).  Of a row: −b·H, B, a, −lse·log2 e.
+//   lse's rounding (1e-6 of an lse of 16) makes a factor of p.  At the word y
+// itself 1 − p would be off by it, however small it is: there log p comes from
+// the row's reference and sum, which lie behind its logits, as logp does, and
+//   G = −a·(exp(log p) − 1) − b·p·(H + log p).
 __device__ __forceinline__ float4 score_terms(const VocabCall& p, long long t) {
   const float scale = p.header->scale * p.inv_tau;
   const float a = p.grad_loss[t * p.grad_stride] * scale;
   const float b =
       p.grad_entropy ? p.grad_entropy[t * p.entropy_stride] * scale : 0.f;
-  return make_float4(-(a + b * p.entropy[t]), -b * 0.69314718056f, a,
+  return make_float4(-b * p.entropy[t], -b * 0.69314718056f, a,
                      -p.lse[t] * 1.4426950408889634f);
 }
 
@@ -306,13 +317,18 @@ __device__ __forceinline__ void score_g_run(const VocabCall& p, uint16_t* G,
     for (int j = 0; j < 8; ++j) {
       const float t = fmaf(f[i][j], c2, of.w), e = exp2_fast(t);
       // (2^-200 is 0: an infinity's product with it would not be)
-      const float g = e * fmaf(of.y, fmaxf(t, -200.f), of.x);
+      const float g = e * fmaf(of.y, fmaxf(t, -200.f), of.x - of.z);
       f[i][j] = here && c + j < cols ? g : 0.f;
     }
     if (goal >= c && goal < c + 8) {
+      const float* of_row = p.logits + (long long)r * p.ld_logits + p.V;
+      const float log_p = vocab_log_prob(p, z[goal], of_row[0], of_row[1]);
+      const float less = expm1f(log_p);  // p - 1
+      const float t = fmaxf(log_p * 1.4426950408889634f, -200.f);
+      const float g = fmaf(-of.z, less, (1.f + less) * fmaf(of.y, t, of.x));
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (goal == c + j) f[i][j] += of.z;
+        if (goal == c + j) f[i][j] = g;
     }
     uint32_t w[4];
 #pragma unroll

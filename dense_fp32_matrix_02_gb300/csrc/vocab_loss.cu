@@ -926,9 +926,12 @@ bool logits_countable(int64_t T, int64_t V) {
   return vocab_tiles(T) * (V / kVocabTile + 1) <= 1 << 30;
 }
 
-// Bytes of the kept logits, whole rows on 32-byte boundaries, and of W's packed
-// copy behind them.
-int64_t kept_logits(int64_t T, int64_t V) { return up(T * up(V, 8) * 4, 256); }
+// Bytes of the kept logits, whole rows on 32-byte boundaries with two numbers
+// more each, and of W's packed copy behind them.
+int64_t kept_ld(int64_t V) { return up(V + 2, 8); }
+int64_t kept_logits(int64_t T, int64_t V) {
+  return up(T * kept_ld(V) * 4, 256);
+}
 int64_t kept_bytes(int64_t T, int64_t V, int64_t D, bool pack_w) {
   return kept_logits(T, V) + (pack_w ? V * up(D, 8) * 2 : 0);
 }
@@ -1109,7 +1112,7 @@ int run(const Request& r) {
   c.dW = r.dW, c.lddw = r.lddw;
   if (r.kept) {
     c.logits = static_cast<float*>(r.kept);
-    c.ld_logits = up(r.V, 8);
+    c.ld_logits = kept_ld(r.V);
     c.chunk = c.T;
     c.keep = 1;
     if (!vocab_maps(r.W, r.ldw)) {

@@ -110,19 +110,19 @@ __device__ __forceinline__ Stat share_of(const VocabCall& p, int r, int first,
   return st;
 }
 
-// The log probability of a logit z in a row of reference m and log S.
-__device__ __forceinline__ float log_prob(const VocabCall& p, float z, float m,
-                                          float log_sum) {
-  return fmaf(kLn2, fmaf(z, p.inv_tau * kLog2e, -m), -log_sum);
-}
-
-// A row's results; z: its word's logit.
+// A row's results; z: its word's logit.  What the gradients need of it goes
+// behind its kept logits.
 __device__ __forceinline__ void store_results(const VocabCall& p, long long t,
-                                              bool scored, Stat st,
+                                              int r, bool scored, Stat st,
                                               float log_sum, float z) {
+  if (p.keep) {
+    float* of_row = p.logits + (long long)r * p.ld_logits + p.V;
+    of_row[0] = st.m;
+    of_row[1] = log_sum;
+  }
   // (the difference of equal numbers where one word has all: not below 0)
   const float entropy = log_sum - kLn2 * (st.e / st.s);
-  p.loss[t] = scored ? log_prob(p, z, st.m, log_sum) : 0.f;
+  p.loss[t] = scored ? vocab_log_prob(p, z, st.m, log_sum) : 0.f;
   p.lse_out[t] = scored ? fmaf(kLn2, st.m, log_sum) : 0.f;
   p.entropy_out[t] = scored && !(entropy < 0.f) ? entropy : 0.f;
 }
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (warp > 0) return;
   st = lane < kFinishThreads / 32 ? s_part[lane] : Stat{-INFINITY, 0.f, 0.f};
   st = merge_warp(st);
-  if (lane == 0) store_results(p, t, scored, st, logf(st.s), z);
+  if (lane == 0) store_results(p, t, r, scored, st, logf(st.s), z);
 }
 
 // ------------------------------------------------------- likeliest words
@@ -517,7 +517,7 @@ __device__ __forceinline__ void write_ranked(const VocabCall& p, long long t,
     if (rank < p.alternatives) {
       p.top_out[t * p.alternatives + rank] = id;
       p.top_logp[t * p.alternatives + rank] =
-          log_prob(p, logit, m, log_sum);
+          vocab_log_prob(p, logit, m, log_sum);
     }
   }
 }
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const long long t = learnt != p.T ? p.token[r] : r;
   if (!p.header && !vocab_is_learnt(p, t)) {
     if (tid == 0) {
-      store_results(p, t, false, Stat{0.f, 1.f, 0.f}, 0.f, 0.f);
+      store_results(p, t, r, false, Stat{0.f, 1.f, 0.f}, 0.f, 0.f);
       vocab_unscored(p, t);
     }
     return;
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   // (in every thread as the first has it)
   st.m = __shfl_sync(0xffffffffu, st.m, 0);
   const float log_sum = logf(__shfl_sync(0xffffffffu, st.s, 0));
-  if (tid == 0) store_results(p, t, true, st, log_sum, p.picked[r]);
+  if (tid == 0) store_results(p, t, r, true, st, log_sum, p.picked[r]);
 
   auto maximum = [&](int g) {
     return held ? s_key[g] : order_of(p.sums[(long long)r * parts + g].w);

@@ -543,8 +543,9 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  *
  * `kept`, where it is not NULL, receives the logits for the gradients, and a
  * copy of W where its rows do not start on 16-byte boundaries: 16-byte aligned
- * device memory of at least gemm_f32_vocab_score_kept_size bytes (4 a logit, 2
- * an element of the copy), whose layout is the library's own.
+ * device memory of at least gemm_f32_vocab_score_kept_size bytes (4 a logit, 8 a
+ * token and what aligns its row, 2 an element of the copy), whose layout is the
+ * library's own.
  *
  * gemm_f32_vocab_score_grad takes ids, lse, entropy and kept as the forward
  * call of the same operands left them, and the gradients of logp

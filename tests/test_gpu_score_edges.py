@@ -151,3 +151,62 @@ def test_rank_among_the_first_words_is_not_enough():
             ids = torch.zeros(T, dtype=torch.int64, device=DEV)
             s = L.log_probs(x.repeat(T, 1), w, ids, top=top)
             assert torch.equal(s.top_ids, want.expand(T, top))
+
+
+@TYPES
+@pytest.mark.parametrize("T", [3, 64, 128])
+def test_gradients_of_near_certain_words(T, dtype):
+    """1 - p of a word with p near 1 comes from the row's reference and sum,
+    not from lse, whose last place is 8e-6 of logits around 80.  The logits are
+    exact (small integers over 4), and of 128 tokens and fewer G is kept in two
+    16-bit parts, so that what is off in a row of G is
+      * at the word: a logarithm's error of 6e-7 (the exponentials, the sum of
+        the others and its logarithm, as for logp), |a|·6e-7, and for the
+        entropy's gradient 1e-5 of |b| (its own, ten times that);
+      * elsewhere p's, a factor of 1 ± 4e-5 (lse's rounding) of |G|;
+      * 2^-15 of |G| (binary16 and bfloat16 in two parts), and binary16's
+        smallest step under the scale that brings the largest to 2^14.
+    dX and dW add those up and round once."""
+    V, D = 1000, 64
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -11
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randint(-1, 2, (T, D), generator=gen, device=DEV).to(dtype)
+    w = (torch.randint(-4, 5, (V, D), generator=gen, device=DEV) / 4).to(dtype)
+    ids = torch.arange(T, device=DEV)
+    w[:T] = x / 2
+    x[:, 0], w[:, 0] = 8.0, 8.0  # all logits 64 higher
+    a = torch.rand(T, generator=gen, device=DEV) + 0.5
+    b = 0.1 * torch.rand(T, generator=gen, device=DEV)
+    z = x.double() @ w.double().t()
+    lse = torch.logsumexp(z, 1)
+    log_p = z - lse[:, None]
+    p = log_p.exp()
+    H = -(p * log_p).sum(1)
+    rows = torch.arange(T, device=DEV)
+    some = (1 - p[rows, ids]) < 1e-2
+    assert int(some.sum()) > T // 2 and float(lse.min()) > 64
+    for with_b in (False, True):
+        s = L.log_probs(x, w, ids, keep=True)
+        dx, dw = L.log_probs_grad(x, w, ids, s, a, b if with_b else None)
+        A = a.double()[:, None]
+        B = b.double()[:, None] * with_b
+        g = -p * (A + B * (log_p + H[:, None]))
+        # (1 - p without the difference)
+        rest = p.clone()
+        rest[rows, ids] = 0.0
+        g[rows, ids] = (A[:, 0] * rest.sum(1)
+                        - B[:, 0] * (p[rows, ids] * (log_p[rows, ids] + H)))
+        most = float((A + B * (0.4 + H[:, None])).max())
+        wrong = g.abs() * (4e-5 + 2.0 ** -15) + p * B * 1e-5
+        wrong[rows, ids] += A[:, 0] * 6e-7
+        if dtype == F16:
+            wrong += most * 2.0 ** -24 / 2.0 ** 13
+        for got, left, other, dleft in (
+                (dx, g, w.double(), wrong), (dw, g.t(), x.double(), wrong.t())):
+            want = left @ other
+            tol = (dleft @ other.abs() + u * want.abs()
+                   + 1e-6 * (left.abs() @ other.abs())
+                   + (2.0 ** -25 if dtype == F16 else 0.0))
+            err = (got.double() - want).abs()
+            assert bool((err <= tol).all()), float((err / tol).max())
+    assert G.device_status() == 0
