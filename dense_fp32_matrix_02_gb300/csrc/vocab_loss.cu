@@ -767,10 +767,14 @@ int64_t lay_out(VocabCall* c, char* ws, int64_t T, int64_t V, int64_t D,
   const bool pack_w = !aligned && !keep;
   // dW of such a width, one row behind the other, has no tensor map either.  One
   // row of tiles waits for memory: it writes dW in rows that have one, which
-  // are then moved (a step of 16 × 50000 × 2045 305 us, 339 without; 256 tokens
-  // 348 and 372).  Short rows cost the move more (16 × 50000 × 201 106 us, 101
-  // without), and more tokens' products hide what the epilogue takes (600 ×
-  // 50000 × 1001 320 us, 311 without).
+  // are then moved.  Short rows cost the move more, and more tokens' products
+  // hide what the epilogue takes.  Gradients of 16 tokens, 50000 words, moved
+  // and not: width 129 86 and 79 us, 201 95 and 91, 257 98 and 100, 401 114 and
+  // 121, 1001 180 and 195, 2045 309 and 337; of 256 tokens: 201 88 and 88, 257 99
+  // and 98, 401 117 and 119, 2045 325 and 345; of 300 tokens 120 and 116 at 257,
+  // 141 and 136 at 401, 215 and 220 at 1001, 384 and 400 at 2045; of 600 never
+  // less (498 and 480 at 2045).  8000 words: the same bounds, but for 256 tokens
+  // of widths 401 to 1501 (3 us, up to 7 %, lost).
   const bool odd_rows =
       !aligned && D % 8 != 0 && D >= 256 && T <= kVocabTile;
   // A piece's G: small enough that it and its part of W stay near the L2

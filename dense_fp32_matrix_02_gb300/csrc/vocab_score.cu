@@ -30,6 +30,11 @@
 // bound by memory, the later ones by the products' epilogue warps, which
 // otherwise wait for the tensor cores most of the time (vocab_gemm.cu).  Making
 // the logits again would cost 2·D operations an element instead.
+//   G is rounded to the operands' 16 bits, which kind::f16 asks for: beyond 128
+// tokens once, so that dX and dW are 2.4e-3 off float64 in bfloat16 and 2.9e-4
+// in binary16, where rounding the results alone leaves 1.65e-3 and 2.1e-4.  G in
+// two parts (vocab.cuh, kVocabFewTokens) would leave that too, for twice the
+// operations of both products, two thirds of a step's.
 #include <algorithm>
 
 #include "bound_search.h"
@@ -61,11 +66,13 @@ __device__ __forceinline__ float moved(float m, float ref) {
   return fmaxf(m - ref, -1e30f);
 }
 
-// The statistics of all lanes joined.
+// The number of an order.
 __device__ __forceinline__ float reference_of(uint32_t order) {
   const uint32_t u = order & 0x80000000u ? order ^ 0x80000000u : ~order;
   return __uint_as_float(u);
 }
+
+// The statistics of all lanes joined.
 __device__ __forceinline__ Stat merge_warp(Stat st) {
   const float m = reference_of(
       __reduce_max_sync(0xffffffffu, order_of(st.m)));

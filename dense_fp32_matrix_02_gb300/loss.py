@@ -7,9 +7,9 @@ loss: softmax cross entropy, or distillation from a teacher's top logits; or
 with the log probabilities of given words, their distribution's entropy and
 the likeliest words.  The losses never store the logits;
 ``include/gemm_f32.h`` (gemm_f32_vocab_*) gives the formulas.  Like every call
-of the binding these are asynchronous on ``stream`` (None: the current one), raise ``GemmError`` for a status other
-than 0, and take an optional ``workspace`` (a CUDA tensor of at least
-``workspace_size`` bytes; allocated here when None).
+of the binding these are asynchronous on ``stream`` (None: the current one), raise
+``GemmError`` for a status other than 0, and take an optional ``workspace`` (a
+CUDA tensor of at least ``workspace_size`` bytes; allocated here when None).
 
     loss, lse = cross_entropy(x, w, targets)             # per token, fp32
     dx, dw = cross_entropy_grad(x, w, targets, lse, grad_loss)
@@ -288,8 +288,9 @@ def log_probs(x, w, ids, top=0, temperature=1.0, keep=False, workspace=None,
     exp(logits/temperature), the distribution's entropy and, with ``top``, the
     likeliest words, largest first, equal logits by the lower id.  A token
     whose id is outside [0, vocab) is not scored (zeros; ids of -1).  ``keep``:
-    the logits stay in memory (4 bytes each) for log_probs_grad, and a copy of
-    w if its rows do not start on 16-byte boundaries."""
+    the logits stay in memory (4 bytes each, 4 GB of 8192 tokens and 128000
+    words) for log_probs_grad, and a copy of w if its rows do not start on
+    16-byte boundaries."""
     head, aligned = _operands(x, w)
     device, T, V = x.device, head[1], head[2]
     y, _ = _vector(ids, "ids", T, torch.int64, device)
@@ -335,7 +336,9 @@ def log_probs_grad(x, w, ids, scores, grad_logp, grad_entropy=None,
     """(dx, dw) in x's dtype from the gradients of each token's logp and
     entropy (float32; an expanded scalar is taken as it is; None: 0).
     ``scores``: what log_probs returned for the same operands, ids and
-    temperature with ``keep``."""
+    temperature with ``keep``; there is no form that makes the logits again, as
+    the losses' gradients do.  A batch whose logits are too many is given in
+    parts, whose dw (overwritten by each call) the caller adds up."""
     head, aligned = _operands(x, w)
     device, (_, T, V, D) = x.device, head[:4]
     y, _ = _vector(ids, "ids", T, torch.int64, device)

@@ -555,7 +555,9 @@ GEMM_F32_API int64_t gemm_f32_vocab_workspace_size(int64_t T, int64_t V,
  *   G[t][v] = (a_t·([v = ids[t]] − p) − b_t·p·(log p + entropy_t)) / τ,
  *   dX = G·W (T×D, lddx),   dW = Gᵀ·X (V×D, lddw)
  * as the losses' _grad forms do (rounding, order and overlap included; G's
- * scale goes by the largest (|a_t| + |b_t|·(0.4 + entropy_t))/τ).
+ * scale goes by the largest (|a_t| + |b_t|·(0.4 + entropy_t))/τ).  There is no
+ * form without kept logits; dW is overwritten, so that tokens given in parts
+ * have theirs added up by the caller.
  *
  * Workspace, limits, empty calls and errors are those of the losses, with
  * gemm_f32_vocab_score_workspace_size bytes; for top > 0 without `kept` it
