@@ -210,3 +210,22 @@ def test_gradients_of_near_certain_words(T, dtype):
             err = (got.double() - want).abs()
             assert bool((err <= tol).all()), float((err / tol).max())
     assert G.device_status() == 0
+
+
+def test_checked_build_runs_clean():
+    """The checked build, in a process of its own: no index leaves its buffer
+    where many words are ranked, and where products gave up."""
+    import os
+    import subprocess
+    import sys
+
+    from dense_fp32_matrix_02_gb300 import build
+    path = build.build(checked=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run(
+        [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-k",
+         "rank or certain or gave_up or maxima",
+         os.path.join(here, "test_gpu_score_edges.py")],
+        env=dict(os.environ, GEMM_F32_LIBRARY=path), cwd=here,
+        capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
